@@ -11,6 +11,7 @@ PyTorch is used only to allocate device memory and to name the stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -24,6 +25,7 @@ GQ_FMT_Q4_0, GQ_FMT_KSB = 0, 1
 GQ_DEV_NONFINITE, GQ_DEV_RANGE, GQ_DEV_TIMEOUT = 1, 2, 4
 GQ_GEMV_PDL = 1
 GQ_QUANT_REF_RULE = 1
+GQ_ROUTE_NORM, GQ_ROUTE_SIGMOID = 2, 4
 
 # every symbol include/gq.h declares
 EXPORTS = (
@@ -37,6 +39,8 @@ EXPORTS = (
     "gq_selftest_gemv_timeout", "gq_gemv_q4_0_noalloc", "gq_stream_read",
     "gq_tiled_bytes", "gq_repack_q4_0", "gq_repack_ksb", "gq_gemv_q4_0_tiled", "gq_gemv_ksb_tiled",
     "gq_gemv_q4_0_tiled_grouped", "gq_gemv_ksb_tiled_grouped",
+    "gq_moe_route_workspace_bytes", "gq_moe_route",
+    "gq_moe_workspace_bytes", "gq_moe_q4_0_tiled", "gq_moe_ksb_tiled",
 )
 
 _DTYPE_CODE = {torch.float32: GQ_F32, torch.float16: GQ_F16, torch.bfloat16: GQ_BF16}
@@ -109,6 +113,18 @@ def _load() -> ctypes.CDLL:
     for name in ("gq_gemv_q4_0_tiled_grouped", "gq_gemv_ksb_tiled_grouped"):
         f = getattr(L, name)
         f.argtypes = [vp, c_int, i64, vp, c_int, c_int, c_uint, vp, vp]
+        f.restype = c_int
+    L.gq_moe_route_workspace_bytes.argtypes = [i64, i64]
+    L.gq_moe_route_workspace_bytes.restype = ctypes.c_size_t
+    L.gq_moe_route.argtypes = [vp, c_int, i64, i64, vp, c_int, i64, vp, i64, ctypes.c_float, vp, vp,
+                               vp, ctypes.c_size_t, c_uint, vp, vp]
+    L.gq_moe_route.restype = c_int
+    L.gq_moe_workspace_bytes.argtypes = [c_int, i64, i64, i64, i64]
+    L.gq_moe_workspace_bytes.restype = ctypes.c_size_t
+    for name in ("gq_moe_q4_0_tiled", "gq_moe_ksb_tiled"):
+        f = getattr(L, name)
+        f.argtypes = [vp, vp, vp, i64, i64, i64, vp, c_int, i64, vp, vp, i64, vp, c_int, vp,
+                      ctypes.c_size_t, c_uint, vp, vp]
         f.restype = c_int
     return L
 
@@ -473,3 +489,149 @@ def gq_gemv_ksb_tiled_grouped(Ts, Ms, K: int, x: torch.Tensor, y_dtype=torch.flo
     """[y_i = W_hat_i @ x for each super-block matrix in tiled storage T_i], one fp16 x."""
     return _gemv_tiled_grouped("gq_gemv_ksb_tiled_grouped", Ts, Ms, K, x, y_dtype, outs, flags,
                                dev_status, stream)
+
+
+# Zeroed workspaces of the calls below, one per (call, device, stream): calls on
+# one stream run in order, and each leaves its workspace ready for the next.
+_call_ws: dict = {}
+
+
+def _auto_workspace(name: str, need: int, device: torch.device, stream: int) -> torch.Tensor:
+    key = (name, device.index, stream)
+    ws = _call_ws.get(key)
+    if ws is None or ws.numel() < need:
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+            ws = torch.zeros(need, dtype=torch.uint8, device=device)
+            # a captured call keeps a workspace of its own, which its graph clears
+            if not torch.cuda.is_current_stream_capturing():
+                _call_ws[key] = ws
+    elif torch.cuda.is_current_stream_capturing():
+        ws = torch.zeros(need, dtype=torch.uint8, device=device)
+    return ws
+
+
+def _on_device(call):
+    """Run the call with its first tensor's device as the current one."""
+    @functools.wraps(call)
+    def wrapped(first, *args, **kw):
+        dev = first.device
+        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return call(first, *args, **kw)
+        return call(first, *args, **kw)
+    return wrapped
+
+
+def _raw_stream(stream, device: torch.device) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _workspace(name: str, workspace, need: int, device: torch.device, stream: int):
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be 'auto' or a uint8 CUDA tensor")
+        workspace = _auto_workspace(name, need, device, stream)
+    if workspace is None:
+        return None, 0
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def gq_moe_route_workspace_bytes(T: int, E: int) -> int:
+    return int(lib.gq_moe_route_workspace_bytes(int(T), int(E)))
+
+
+@_on_device
+def gq_moe_route(x: torch.Tensor, Wr: torch.Tensor, k: int, bias: torch.Tensor | None = None,
+                 scale: float = 1.0, flags: int = 0, ids: torch.Tensor | None = None,
+                 weights: torch.Tensor | None = None, workspace="auto",
+                 dev_status: torch.Tensor | None = None, stream=None):
+    """(ids [T, k] int32, weights [T, k] fp32): the k experts of each token of x
+    [T, H] by their scores x @ Wr^T (Wr [E, H]), and their weights.
+
+    flags: GQ_ROUTE_NORM (weights divided by their sum), GQ_ROUTE_SIGMOID
+    (sigmoid scores; `bias` [E] fp32 is added for the choice only), GQ_GEMV_PDL.
+    workspace: "auto" (a zeroed buffer cached per device and stream) or a uint8
+    CUDA tensor of gq_moe_route_workspace_bytes(T, E) bytes, zero before its
+    first use."""
+    if x.dim() != 2 or Wr.dim() != 2 or x.shape[1] != Wr.shape[1]:
+        raise ValueError("x is [T, H] and Wr [E, H]")
+    if x.dtype not in _DTYPE_CODE or Wr.dtype not in _DTYPE_CODE:
+        raise TypeError("x and Wr must be float32, float16 or bfloat16")
+    T, H = x.shape
+    E = Wr.shape[0]
+    if bias is not None and (bias.dtype != torch.float32 or bias.numel() != E):
+        raise ValueError("bias holds E fp32 values")
+    s = _raw_stream(stream, x.device)
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
+    elif ids.dtype != torch.int32 or ids.numel() != T * k:
+        raise ValueError("ids holds T * k int32 values")
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=x.device)
+    elif weights.dtype != torch.float32 or weights.numel() != T * k:
+        raise ValueError("weights holds T * k fp32 values")
+    ws, ws_bytes = _workspace("route", workspace, lib.gq_moe_route_workspace_bytes(T, E), x.device, s)
+    _check(lib.gq_moe_route(_ptr(x), _DTYPE_CODE[x.dtype], T, H, _ptr(Wr), _DTYPE_CODE[Wr.dtype], E,
+                            _ptr(bias), k, scale, _ptr(ids), _ptr(weights), ws, ws_bytes, flags,
+                            _ptr(dev_status), s), "gq_moe_route")
+    return ids, weights
+
+
+def gq_moe_workspace_bytes(fmt: int, H: int, I: int, T: int, k: int) -> int:
+    return int(lib.gq_moe_workspace_bytes(int(fmt), int(H), int(I), int(T), int(k)))
+
+
+def _moe(name: str, fmt: int, gate, up, down, E: int, I: int, x: torch.Tensor, ids: torch.Tensor,
+         weights: torch.Tensor, y_dtype, out, workspace, flags: int, dev_status, stream):
+    if x.dim() != 2 or ids.dim() != 2 or ids.shape != weights.shape or ids.shape[0] != x.shape[0]:
+        raise ValueError("x is [T, H], ids and weights [T, k]")
+    if x.dtype not in _DTYPE_CODE or y_dtype not in _DTYPE_CODE:
+        raise TypeError("activations and outputs must be float32, float16 or bfloat16")
+    if ids.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise TypeError("ids must be int32 and weights fp32")
+    T, H = x.shape
+    k = ids.shape[1]
+    gu, dn = lib.gq_tiled_bytes(fmt, E * I, H), lib.gq_tiled_bytes(fmt, E * H, I)
+    if gate.numel() < gu or up.numel() < gu or down.numel() < dn:
+        raise ValueError("gate, up or down is smaller than the tiled storage of E experts")
+    s = _raw_stream(stream, x.device)
+    if out is None:
+        out = torch.empty((T, H), dtype=y_dtype, device=x.device)
+    elif out.dtype not in _DTYPE_CODE or out.numel() != T * H:
+        raise ValueError("out holds T * H values")
+    ws, ws_bytes = _workspace(name, workspace, lib.gq_moe_workspace_bytes(fmt, H, I, T, k), x.device, s)
+    _check(getattr(lib, name)(_ptr(gate), _ptr(up), _ptr(down), E, H, I, _ptr(x), _DTYPE_CODE[x.dtype],
+                              T, _ptr(ids), _ptr(weights), k, _ptr(out), _DTYPE_CODE[out.dtype], ws,
+                              ws_bytes, flags, _ptr(dev_status), s), name)
+    return out
+
+
+@_on_device
+def gq_moe_q4_0_tiled(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, E: int, I: int,
+                      x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                      y_dtype=torch.float16, out: torch.Tensor | None = None, workspace="auto",
+                      flags: int = 0, dev_status: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """y [T, H] of a mixture-of-experts layer on Q4_0 experts in tiled storage:
+    y[t] = sum_j weights[t, j] * down_e(silu(gate_e x[t]) * (up_e x[t])), e = ids[t, j].
+
+    gate, up: gq_repack of the E * I x H matrix of all experts' rows; down: of
+    the E * H x I one.  x: [T, H], T <= 64; ids, weights: [T, k], as
+    gq_moe_route returns them.  workspace: "auto" (a zeroed buffer cached per
+    device and stream) or a uint8 CUDA tensor of gq_moe_workspace_bytes(...)
+    bytes, zero before its first use."""
+    return _moe("gq_moe_q4_0_tiled", GQ_FMT_Q4_0, gate, up, down, E, I, x, ids, weights, y_dtype, out,
+                workspace, flags, dev_status, stream)
+
+
+@_on_device
+def gq_moe_ksb_tiled(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, E: int, I: int,
+                     x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                     y_dtype=torch.float16, out: torch.Tensor | None = None, workspace="auto",
+                     flags: int = 0, dev_status: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """gq_moe_q4_0_tiled on super-block experts."""
+    return _moe("gq_moe_ksb_tiled", GQ_FMT_KSB, gate, up, down, E, I, x, ids, weights, y_dtype, out,
+                workspace, flags, dev_status, stream)

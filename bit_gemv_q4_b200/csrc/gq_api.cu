@@ -77,7 +77,7 @@ GQ_API const char* gq_status_string(int status) {
     case GQ_ERR_ALIGNMENT: return "pointer not 16-byte aligned";
     case GQ_ERR_DTYPE: return "unsupported element type";
     case GQ_ERR_NONFINITE: return "NaN or infinity in quantizer input";
-    case GQ_ERR_RANGE: return "scale overflowed FP16";
+    case GQ_ERR_RANGE: return "a scale overflowed its type, or an expert id is out of range";
     case GQ_ERR_TIMEOUT: return "a bounded wait inside a kernel gave up";
     case GQ_ERR_CUDA: return "CUDA launch or runtime error";
     case GQ_ERR_WORKSPACE: return "workspace missing or too small";

@@ -1,0 +1,727 @@
+// gq_moe.cu -- a mixture-of-experts layer for a few tokens on 4-bit experts in
+// tiled storage.
+//
+// Operation: y[t] = sum_j w[t][j] * D_e (silu(G_e x_t) * (U_e x_t)), e =
+// ids[t][j], with G, U, D decoded from Q4_0 blocks ("GGUF 量化内幕 第4章" 4.3:
+// d * (code - 8)) or super-blocks ("GGUF K-quants" 套娃, step 5).  The taken
+// experts' weights set the time (the decode setting of the TurboQuant W4A8
+// post, section 2.3): every byte of them is read once, and nothing else is
+// large.
+//
+// Three launches joined by programmatic dependent launch: gate and up with the
+// activation between them (h, fp32, in the workspace), down (one fp32 row of
+// outputs for each token and slot), and the weighted sum over a token's slots.
+//
+// Plan.  Every CTA reads the ids and builds the same plan in shared memory:
+// the (token, slot) pairs sorted by expert (stable), and segments of an expert
+// with at most `cap` of its pairs.  The work of all segments, 16 weight rows
+// at a time, is cut into even runs, one for each CTA; a run's row groups form
+// one string of units (the 576 or 1104 bytes that one warp multiplies at a
+// time), which its 16 warps share evenly, so that the split is even whatever
+// the sizes are.  Units are read straight into registers, a few ahead: tiled
+// storage is ordered by the lanes that multiply it, so a warp reads whole
+// lines.  Sums of a row group that several warps share meet in a shared table
+// and are added in warp order: results do not depend on scheduling.
+//
+// Arithmetic.  As in the tiled GEMV a nibble mask makes an fp16 subnormal out
+// of a code, exactly.  The warp MMA's eight columns are the expert's tokens.
+// Activations are scaled by a power of two for each token so that the largest
+// lies in [2^14, 2^15); 16-bit inputs then enter as one fp16 column, exact down
+// to 2^-39 of the largest.  fp32 inputs, and h when y is fp32, enter as two
+// columns (the fp16 value and the fp16 remainder: 22 bits); for a 16-bit y, h
+// enters as one column, rounded to 11 bits, which is below the rounding of y.
+// Weights 16..31 of a block stay in the high nibble, 16 times too large, and
+// their activations are scaled by 1/16; the offset -8 enters as the MMA's
+// accumulator input, -8 * (block sum of x).  Products are exact, sums are
+// fp32.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gq.h"
+#include "gq_device.cuh"
+#include "gq_host.h"
+
+namespace gq {
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxT = 64, kMaxTopK = 16, kMaxE = 1024;
+constexpr int kMaxPairs = kMaxT * kMaxTopK;
+constexpr int kMaxK = 16384;
+constexpr int kMaxCols = 16;                // columns of a segment: two n8 tiles
+constexpr size_t kSmemBudget = 227 * 1024;
+
+// A unit of tiled storage: what one warp multiplies at a time.
+template <int FMT>
+struct Unit;
+template <>
+struct Unit<GQ_FMT_Q4_0> {  // two blocks of 32 weights x 16 rows
+  static constexpr int kBlocks = 2, kTileUnits = 32, kTileBytes = 18432, kCodeBytes = 512;
+  static constexpr int kWords = 6, kAhead = 8;
+};
+template <>
+struct Unit<GQ_FMT_KSB> {   // four sub-blocks of 32 weights x 16 rows
+  static constexpr int kBlocks = 4, kTileUnits = 16, kTileBytes = 17664, kCodeBytes = 1024;
+  static constexpr int kWords = 12, kAhead = 4;
+};
+
+struct MoeArgs {
+  const uint8_t* w0;        // gate, or down
+  const uint8_t* w1;        // up (gate-up launch only)
+  const void* x;            // x [T][H], or h [pairs][I] by slot
+  const int32_t* ids;       // [T][k]
+  float* h;                 // [pairs][I], by slot
+  float* out;               // [pairs][H], by pair
+  int* dev_status;
+  unsigned* hmax;           // [pairs] largest |h| of a slot as bits, zero between calls
+  int T, k, E, K;           // K: columns of this launch's weights
+  int groups;               // row groups (16 rows) of one expert
+  int xtype, two;           // element type of x; two columns for each token
+  int cap;                  // tokens of a segment at most
+  int tabslots;             // parts that one table holds
+  int tabfloats;            // floats of one table
+  int64_t group_bytes;
+  uint32_t b_off, corr_off, tab_off;  // dynamic shared memory
+};
+
+struct Seg {
+  int e, slot0, n;
+};
+
+struct Plan {
+  int nseg, npairs;
+  int cnt[kMaxE];           // pairs of an expert, then its first slot
+  short rank[kMaxPairs];
+  short order[kMaxPairs];   // slot -> pair
+  Seg seg[kMaxPairs];
+  float inv[2][kMaxCols];   // 2^24 / scale of a segment's tokens
+  unsigned amax[2][kMaxCols];
+};
+
+extern __shared__ __align__(1024) uint8_t msm[];
+
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void ldg_stream8(const uint8_t* p, uint32_t* w) {  // 32-byte aligned
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+                 "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ uint32_t ldg_word(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ldg_half(const uint8_t* p) {
+  unsigned short v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+
+// ------------------------------------------------------------------- plan
+// Pairs sorted by expert (stable), and the segments.  ids outside [0, E) are
+// left out.  All threads call it.
+__device__ void make_plan(Plan& pl, const MoeArgs& a) {
+  const int P = a.T * a.k;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < a.E; e += kThreads) pl.cnt[e] = 0;
+  __syncthreads();
+  if (warp == 0) {
+    // rank of each pair among its expert's, 32 pairs at a time
+    for (int p0 = 0; p0 < P; p0 += 32) {
+      const int p = p0 + lane;
+      const int id = p < P ? __ldcg(a.ids + p) : -1;
+      const bool ok = id >= 0 && id < a.E;
+      if (blockIdx.x == 0 && (id < -1 || id >= a.E)) report(a.dev_status, GQ_DEV_RANGE);
+      const unsigned peers = __match_any_sync(0xFFFFFFFFu, ok ? id : -1 - lane);
+      const int before = __popc(peers & ((1u << lane) - 1u));
+      const int base = ok ? pl.cnt[id] : 0;
+      __syncwarp();
+      if (ok && before == 0) pl.cnt[id] = base + __popc(peers);
+      if (p < P) pl.rank[p] = static_cast<short>(ok ? base + before : -1);
+      __syncwarp();
+    }
+    // counts -> first slots, and segments, in the order of the experts
+    int slots = 0, segs = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int n = e < a.E ? pl.cnt[e] : 0;
+      const int ns = (n + a.cap - 1) / a.cap;
+      int sn = n, ss = ns;  // inclusive sums over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, sn, o), v = __shfl_up_sync(0xFFFFFFFFu, ss, o);
+        if (lane >= o) {
+          sn += u;
+          ss += v;
+        }
+      }
+      const int first = slots + sn - n, sfirst = segs + ss - ns;
+      if (e < a.E) pl.cnt[e] = first;
+      for (int i = 0; i < ns; ++i)
+        pl.seg[sfirst + i] = Seg{e, first + i * a.cap, min(a.cap, n - i * a.cap)};
+      slots += __shfl_sync(0xFFFFFFFFu, sn, 31);
+      segs += __shfl_sync(0xFFFFFFFFu, ss, 31);
+    }
+    if (lane == 0) {
+      pl.nseg = segs;
+      pl.npairs = slots;
+    }
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < P; p += kThreads) {
+    const int r = pl.rank[p];
+    if (r >= 0) pl.order[pl.cnt[__ldcg(a.ids + p)] + r] = static_cast<short>(p);
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------- activations
+// Eight consecutive values of an element type as floats.
+__device__ __forceinline__ void load8(const void* base, int64_t i, int type, float v[8]) {
+  if (type == GQ_F32) {
+    const float4 a = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
+    const float4 b = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i + 4));
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (type == GQ_F16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[q]));
+        v[2 * q] = f.x, v[2 * q + 1] = f.y;
+      } else {
+        v[2 * q] = __uint_as_float(w[q] << 16);
+        v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
+// The power of two that brings the largest |value| (its bits) into [2^14,
+// 2^15); 1 for infinities and NaN, which stay what they are.
+__device__ __forceinline__ float scale_of(unsigned maxbits) {
+  const int e = static_cast<int>(maxbits >> 23) - 127;
+  if (e > 127) return 1.0f;
+  return __uint_as_float(static_cast<unsigned>(127 + 14 - max(e, -100)) << 23);
+}
+
+// B fragments and block corrections of a segment's tokens.  Column c of block
+// b and lane group t: 16 bytes at ((b * ncol + c) * 4 + t) * 16, the values
+// 4t, 4t+2, 4t+1, 4t+3 of the block and the same at +16 (these / 16).
+template <bool GATE_UP>
+__device__ void load_b(const MoeArgs& a, Plan& pl, const Seg& sg, int buf) {
+  const int ncol = a.two ? 2 * sg.n : sg.n;
+  const int vecs = a.K / 8;
+  auto row_of = [&](int c) -> int64_t {
+    return GATE_UP ? static_cast<int64_t>(pl.order[sg.slot0 + c] / a.k) * a.K
+                   : static_cast<int64_t>(sg.slot0 + c) * a.K;
+  };
+  if (threadIdx.x < sg.n)
+    pl.amax[buf][threadIdx.x] = GATE_UP ? 0u : __ldcg(a.hmax + sg.slot0 + threadIdx.x);
+  __syncthreads();
+  if (GATE_UP) {
+    for (int c = 0; c < sg.n; ++c) {
+      unsigned m = 0;
+      const int64_t row = row_of(c);
+      for (int i = threadIdx.x; i < vecs; i += kThreads) {
+        float v[8];
+        load8(a.x, row + 8 * i, a.xtype, v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(v[q]) & 0x7FFFFFFFu);
+      }
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      if ((threadIdx.x & 31) == 0 && m) atomicMax(&pl.amax[buf][c], m);
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x < sg.n)  // scale_of() is a power of two: the reciprocal is exact
+    pl.inv[buf][threadIdx.x] = 1.0f / scale_of(pl.amax[buf][threadIdx.x]);
+  float* corr = reinterpret_cast<float*>(msm + a.corr_off);
+  const int ncp = (ncol + 1) & ~1;
+  const int nvec = sg.n * vecs;  // a multiple of 8: whole blocks
+  for (int i0 = 0; i0 < nvec; i0 += kThreads) {  // every thread takes part in the shuffles
+    const int i = i0 + threadIdx.x;
+    const bool in = i < nvec;
+    const int c = in ? i / vecs : 0, r = in ? i - c * vecs : 0;
+    const int b = r >> 2, q = threadIdx.x & 3;
+    const float s = scale_of(pl.amax[buf][c]) * (q >= 2 ? 0.0625f : 1.0f);
+    float v[8];
+    load8(a.x, row_of(c) + 8 * r, a.xtype, v);
+    const int col = a.two ? 2 * c : c;
+    const int t0 = 2 * (q & 1);
+    float sum[2] = {0.f, 0.f};
+    for (int part = 0; part <= a.two; ++part) {
+      __half hv[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f = part ? v[j] : v[j] * s;  // the second pass holds remainders
+        hv[j] = __float2half_rn(f);
+        const float g = __half2float(hv[j]);
+        v[j] = f - g;
+        sum[part] += g;
+      }
+      if (!in) continue;
+      uint8_t* d = msm + a.b_off + (static_cast<uint32_t>(b * ncol + col + part) * 4 + t0) * 16 + (q >> 1) * 8;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const __half2 lo = __halves2half2(hv[4 * u], hv[4 * u + 2]);
+        const __half2 hi = __halves2half2(hv[4 * u + 1], hv[4 * u + 3]);
+        *reinterpret_cast<uint2*>(d + 16 * u) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                           *reinterpret_cast<const uint32_t*>(&hi));
+      }
+    }
+    // block sums: the four lanes of a block (a warp holds whole blocks)
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      float f = q >= 2 ? 16.0f * sum[part] : sum[part];
+      f += __shfl_xor_sync(0xFFFFFFFFu, f, 1);
+      f += __shfl_xor_sync(0xFFFFFFFFu, f, 2);
+      if (in && q == 0 && part <= a.two) corr[b * ncp + col + part] = f * -4.76837158203125e-07f;  // -8 * 2^-24
+    }
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------- units
+// The words that this lane needs of one unit, from its row group's bytes.
+template <int FMT>
+__device__ __forceinline__ void load_unit(const uint8_t* group, int u, int units, int lane, uint32_t* w) {
+  using F = Unit<FMT>;
+  const int c = u / F::kTileUnits, i = u - c * F::kTileUnits;
+  const int nu = min(F::kTileUnits, units - c * F::kTileUnits);  // units of the tile
+  const uint8_t* tile = group + static_cast<int64_t>(c) * F::kTileBytes;
+  const int g8 = lane >> 2;
+  if constexpr (FMT == GQ_FMT_Q4_0) {
+    const uint4 v = ldg_stream(tile + 512 * i + 16 * lane);
+    const uint8_t* sc = tile + 512 * nu + 64 * i + 4 * g8;
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    w[4] = ldg_word(sc);
+    w[5] = ldg_word(sc + 32);
+  } else {
+    ldg_stream8(tile + 1024 * i + 32 * lane, w);
+    const uint8_t* sc = tile + 1024 * nu + 64 * i + 4 * g8;
+    const uint8_t* ss = tile + 1088 * nu + 32 * (i >> 1) + 2 * g8;
+    w[8] = ldg_word(sc);
+    w[9] = ldg_word(sc + 32);
+    w[10] = ldg_half(ss);
+    w[11] = ldg_half(ss + 16);
+  }
+}
+
+__device__ __forceinline__ float2 halves(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+// INT8 in byte h of q (its sign bit flipped beforehand) as a float, exact.
+__device__ __forceinline__ float flipped_byte(uint32_t q, int h) {
+  return __uint_as_float(__byte_perm(q, 0x4B000000u, 0x7540u + h)) - 8388736.0f;  // 2^23 + 128
+}
+
+// acc += the unit's products for NT column tiles.  xb, cb: this lane's
+// B fragment and correction of column tile 0 in the unit's first block.
+template <int FMT, int NT>
+__device__ __forceinline__ void unit_math(const uint32_t* w, float acc[NT][4], const uint8_t* xb,
+                                          uint32_t xpitch, uint32_t xtile, const float* cb, int cpitch,
+                                          int ctile) {
+  using F = Unit<FMT>;
+  float da[F::kBlocks], db[F::kBlocks];  // scales of rows g and g+8
+  if constexpr (FMT == GQ_FMT_Q4_0) {
+    const float2 p = halves(w[4]), q = halves(w[5]);
+    da[0] = p.x, da[1] = p.y, db[0] = q.x, db[1] = q.y;
+  } else {
+    const float sa = halves(w[10]).x, sb = halves(w[11]).x;
+    const uint32_t qa = w[8] ^ 0x80808080u, qb = w[9] ^ 0x80808080u;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      da[h] = sa * flipped_byte(qa, h);
+      db[h] = sb * flipped_byte(qb, h);
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < F::kBlocks; ++b) {
+    const uint32_t wa = w[2 * b], wb = w[2 * b + 1];
+    const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const uint4 xv = *reinterpret_cast<const uint4*>(xb + b * xpitch + j * xtile);
+      const float2 cr = *reinterpret_cast<const float2*>(cb + b * cpitch + j * ctile);
+      float c[4] = {cr.x, cr.y, cr.x, cr.y};
+      mma_f16(c, wa & 0x000F000Fu, wb & 0x000F000Fu, wa8 & 0x000F000Fu, wb8 & 0x000F000Fu, xv.x, xv.y);
+      mma_f16(c, wa & 0x00F000F0u, wb & 0x00F000F0u, wa8 & 0x00F000F0u, wb8 & 0x00F000F0u, xv.z, xv.w);
+      acc[j][0] = fmaf(da[b], c[0], acc[j][0]);
+      acc[j][1] = fmaf(da[b], c[1], acc[j][1]);
+      acc[j][2] = fmaf(db[b], c[2], acc[j][2]);
+      acc[j][3] = fmaf(db[b], c[3], acc[j][3]);
+    }
+  }
+}
+
+// A string of row groups [i0, i0 + n) of one expert (gate and up: row group i
+// is one of gate's, then the same of up's).
+template <bool GATE_UP>
+__device__ __forceinline__ const uint8_t* group_at(const MoeArgs& a, int e, int i) {
+  const uint8_t* w = (GATE_UP && (i & 1)) ? a.w1 : a.w0;
+  const int g = GATE_UP ? i >> 1 : i;
+  return w + (static_cast<int64_t>(e) * a.groups + g) * a.group_bytes;
+}
+
+// This warp's units [u, u1) of the string, `w` holding the first kAhead of
+// them: partial sums to the table, part (row group + warp) for each row group
+// that the warp has units of.
+template <int FMT, int NT, bool GATE_UP>
+__device__ __forceinline__ void stream(const MoeArgs& a, int e, int i0, int units, int u, int u1,
+                                       int ncol, uint32_t (*w)[Unit<FMT>::kWords], float* tab) {
+  using F = Unit<FMT>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
+  const int ncp = (ncol + 1) & ~1;
+  // columns past the last read an existing one; their sums are not stored
+  const uint32_t xlane = static_cast<uint32_t>(min(g8, ncol - 1) * 64 + t * 16);
+  const uint32_t xtile = NT > 1 ? static_cast<uint32_t>(min(8 + g8, ncol - 1) * 64 + t * 16) - xlane : 0u;
+  const int clane = min(2 * t, ncp - 2);
+  const int ctile = NT > 1 ? min(8 + 2 * t, ncp - 2) - clane : 0;
+  const uint32_t xpitch = static_cast<uint32_t>(ncol) * 64;
+  const float* corr = reinterpret_cast<const float*>(msm + a.corr_off);
+  float acc[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+  int q = u / units, k = u - q * units;               // row group of the string, unit in it
+  int pq = (u + F::kAhead) / units, pk = u + F::kAhead - pq * units;  // the same, kAhead on
+  const uint8_t* pg = u + F::kAhead < u1 ? group_at<GATE_UP>(a, e, i0 + pq) : nullptr;
+  auto flush = [&]() {
+    float* d = tab + static_cast<int64_t>(q + warp) * 16 * ncp;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int c = 8 * j + 2 * t;
+      if (c < ncp) {
+        *reinterpret_cast<float2*>(d + g8 * ncp + c) = make_float2(acc[j][0], acc[j][1]);
+        *reinterpret_cast<float2*>(d + (g8 + 8) * ncp + c) = make_float2(acc[j][2], acc[j][3]);
+      }
+      acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+    }
+  };
+  while (u < u1) {
+#pragma unroll
+    for (int s = 0; s < F::kAhead; ++s) {
+      if (u < u1) {
+        unit_math<FMT, NT>(w[s], acc, msm + a.b_off + static_cast<uint32_t>(k * F::kBlocks) * xpitch + xlane,
+                           xpitch, xtile, corr + k * F::kBlocks * ncp + clane, ncp, ctile);
+        ++u;
+        if (++k == units || u == u1) {
+          flush();
+          if (k == units) {
+            k = 0;
+            ++q;
+          }
+        }
+        if (u + F::kAhead - 1 < u1) {
+          load_unit<FMT>(pg, pk, units, lane, w[s]);
+          if (++pk == units) {
+            pk = 0;
+            ++pq;
+            if (u + F::kAhead < u1) pg = group_at<GATE_UP>(a, e, i0 + pq);
+          }
+        }
+      }
+    }
+  }
+}
+
+// The run of this CTA: row groups (pairs of them for gate and up) [r0, r1) of
+// all segments', cut into strings of one segment that the table holds.
+struct String {
+  int seg, i0, n;  // segment, first row group (of the string's kind), how many
+};
+template <bool GATE_UP>
+struct Cursor {
+  int64_t r, r1;
+  int groups, most;  // row groups of an expert (pairs counted once), most in a string
+  __device__ __forceinline__ bool next(String& s) {
+    if (r >= r1) return false;
+    s.seg = static_cast<int>(r / groups);
+    const int g = static_cast<int>(r - static_cast<int64_t>(s.seg) * groups);
+    const int left = static_cast<int>(i64min(r1 - r, groups - g));
+    const int strings = (left + most - 1) / most;
+    const int n = (left + strings - 1) / strings;  // even strings
+    s.i0 = GATE_UP ? 2 * g : g;
+    s.n = GATE_UP ? 2 * n : n;
+    r += n;
+    return true;
+  }
+};
+
+template <int FMT, bool GATE_UP>
+__global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs a) {
+  using F = Unit<FMT>;
+  __shared__ Plan pl;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (GATE_UP) pdl_wait();  // ids and x are final (the down launch starts after that)
+  pdl_launch_dependents();
+  make_plan(pl, a);
+  const int units = a.K / (32 * F::kBlocks);
+  const int64_t total = static_cast<int64_t>(pl.nseg) * a.groups;
+  Cursor<GATE_UP> cur{total * blockIdx.x / gridDim.x, total * (blockIdx.x + 1) / gridDim.x, a.groups,
+                      (a.tabslots - kWarps) / (GATE_UP ? 2 : 1)};
+  String st;
+  bool more = cur.next(st);
+  uint32_t w[F::kAhead][F::kWords];
+  // the first units of this warp's share of a string
+  auto fetch = [&](const String& s, int e) {
+    const int tu = s.n * units;
+    const int u0 = tu * warp / kWarps, u1 = tu * (warp + 1) / kWarps;
+#pragma unroll
+    for (int i = 0; i < F::kAhead; ++i) {
+      const int u = u0 + i;
+      if (u < u1) {
+        const int q = u / units;
+        load_unit<FMT>(group_at<GATE_UP>(a, e, s.i0 + q), u - q * units, units, lane, w[i]);
+      }
+    }
+  };
+  if (more) fetch(st, pl.seg[st.seg].e);
+  if (!GATE_UP) pdl_wait();  // h and the slots' largest values are final
+  int buf = 0, loaded = -1;
+  while (more) {
+    const Seg sg = pl.seg[st.seg];
+    const int ncol = a.two ? 2 * sg.n : sg.n, ncp = (ncol + 1) & ~1;
+    if (loaded != st.seg) {
+      load_b<GATE_UP>(a, pl, sg, st.seg & 1);
+      loaded = st.seg;
+    }
+    float* tab = reinterpret_cast<float*>(msm + a.tab_off) + buf * a.tabfloats;
+    const int tu = st.n * units;
+    const int u0 = tu * warp / kWarps, u1 = tu * (warp + 1) / kWarps;
+    if (ncol <= 8)
+      stream<FMT, 1, GATE_UP>(a, sg.e, st.i0, units, u0, u1, ncol, w, tab);
+    else
+      stream<FMT, 2, GATE_UP>(a, sg.e, st.i0, units, u0, u1, ncol, w, tab);
+    const String done = st;
+    more = cur.next(st);
+    if (more) fetch(st, pl.seg[st.seg].e);
+    __syncthreads();  // the table is complete; B and the other table are free
+    // sums of the row groups, in warp order
+    auto sum = [&](int q, int row, int c) {
+      const int first = q * units, last = first + units - 1;
+      const int w0 = (16 * (first + 1) - 1) / tu, w1 = (16 * (last + 1) - 1) / tu;
+      float v = 0.f;
+      for (int ww = w0; ww <= w1; ++ww) {
+        if (tu * ww / kWarps == tu * (ww + 1) / kWarps) continue;  // no units
+        const float* p = tab + (static_cast<int64_t>(q + ww) * 16 + row) * ncp + c;
+        v += a.two ? p[0] + p[1] : p[0];
+      }
+      return v;
+    };
+    const float* inv = pl.inv[done.seg & 1];
+    if constexpr (GATE_UP) {
+      const int cells = done.n / 2 * 16 * sg.n;
+      for (int i = threadIdx.x; i < cells; i += kThreads) {
+        const int row = i & 15, rest = i >> 4;
+        const int c = rest % sg.n, p = rest / sg.n;
+        const int col = a.two ? 2 * c : c;
+        const float g = sum(2 * p, row, col) * 16777216.0f * inv[c];
+        const float up = sum(2 * p + 1, row, col) * 16777216.0f * inv[c];
+        const float h = g / (1.0f + expf(-g)) * up;
+        const int slot = sg.slot0 + c;
+        a.h[static_cast<int64_t>(slot) * (a.groups * 16) + (done.i0 / 2 + p) * 16 + row] = h;
+        // the 16 rows of one token lie in one half of a warp
+        unsigned m = __float_as_uint(h) & 0x7FFFFFFFu;
+        const unsigned half = 0xFFFFu << (lane & 16);
+        m = __reduce_max_sync(half, m);
+        if (row == 0) atomicMax(a.hmax + slot, m);
+      }
+    } else {
+      const int cells = done.n * 16 * sg.n;
+      for (int i = threadIdx.x; i < cells; i += kThreads) {
+        const int row = i & 15, rest = i >> 4;
+        const int c = rest % sg.n, q = rest / sg.n;
+        const float v = sum(q, row, a.two ? 2 * c : c) * 16777216.0f * inv[c];
+        const int pair = pl.order[sg.slot0 + c];
+        a.out[static_cast<int64_t>(pair) * (a.groups * 16) + (done.i0 + q) * 16 + row] = v;
+      }
+    }
+    buf ^= 1;
+  }
+}
+
+// y[t] = sum_j w[t][j] * out[t][j] over the slots that name an expert; the
+// slots' largest values are cleared for the next call.
+__global__ void __launch_bounds__(256) moe_sum_kernel(const float* out, const int32_t* ids,
+                                                      const float* weights, unsigned* hmax, void* y,
+                                                      int T, int k, int E, int H, int ytype) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t n = static_cast<int64_t>(T) * H;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i < T * k) hmax[i] = 0u;
+  if (i >= n) return;
+  const int t = static_cast<int>(i / H), c = static_cast<int>(i - static_cast<int64_t>(t) * H);
+  float v = 0.f;
+  for (int j = 0; j < k; ++j) {
+    const int id = __ldcg(ids + t * k + j);
+    if (id >= 0 && id < E)
+      v = fmaf(__ldcg(weights + t * k + j), __ldcg(out + (static_cast<int64_t>(t) * k + j) * H + c), v);
+  }
+  store_elem(y, i, v, ytype);
+}
+
+// ------------------------------------------------------------------- host
+size_t round256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+struct Ws {
+  size_t hmax, h, out, total;
+};
+Ws ws_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
+  Ws w;
+  w.hmax = 0;
+  w.h = kMaxPairs * 4;  // one size for every call, so that calls of any sizes may follow
+  w.out = w.h + round256(static_cast<size_t>(T * k * I) * 4);
+  w.total = w.out + round256(static_cast<size_t>(T * k * H) * 4);
+  return w;
+}
+
+bool moe_dims(int64_t T, int64_t k, int64_t E) {
+  return T <= kMaxT && k <= kMaxTopK && E <= kMaxE;
+}
+bool moe_width(int fmt, int64_t K) { return K % (fmt == GQ_FMT_Q4_0 ? 64 : 256) == 0 && K <= kMaxK; }
+
+// Tokens of a segment and the layout of shared memory: the B fragments and
+// corrections take 2 + 1/8 bytes for each value of a column; the two tables
+// take what a string of 16 parts beyond the warps' needs.
+constexpr int kTabSlots = kWarps + 32;
+size_t shape_smem(MoeArgs& a) {
+  const size_t left = kSmemBudget - sizeof(Plan) - 2048;
+  const size_t colbytes = static_cast<size_t>(a.K) * 2 + static_cast<size_t>(a.K) / 32 * 4 + 2 * kTabSlots * 16 * 4;
+  int cols = static_cast<int>(left / colbytes < kMaxCols ? left / colbytes : kMaxCols) & ~1;
+  const int pairs = a.T * a.k * (a.two ? 2 : 1);
+  if (cols > pairs) cols = (pairs + 1) & ~1;
+  a.cap = a.two ? cols / 2 : cols;
+  a.tabslots = kTabSlots;
+  a.tabfloats = kTabSlots * 16 * cols;
+  a.tab_off = 0;
+  a.b_off = 2 * a.tabfloats * 4;
+  a.corr_off = a.b_off + static_cast<uint32_t>(cols) * a.K * 2;
+  return a.corr_off + static_cast<size_t>(cols) * a.K / 32 * 4;
+}
+
+template <int FMT, bool GATE_UP>
+gq_status launch_moe(MoeArgs& a, bool pdl, cudaStream_t s) {
+  auto kern = moe_kernel<FMT, GATE_UP>;
+  thread_local unsigned long long configured_ctx = 0;  // per host thread and context
+  const unsigned long long ctx = context_id();
+  if (ctx == 0 || ctx != configured_ctx) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemBudget - sizeof(Plan) - 1024)) != cudaSuccess)
+      return GQ_ERR_CUDA;
+    configured_ctx = ctx;
+  }
+  const size_t smem = shape_smem(a);
+  return launch(kern, dim3(sm_count()), dim3(kThreads), smem, s, pdl, a);
+}
+
+template <int FMT>
+gq_status moe_entry(const void* gate, const void* up, const void* down, int64_t E, int64_t H,
+                    int64_t I, const void* x, int x_dtype, int64_t T, const int32_t* ids,
+                    const float* weights, int64_t k, void* y, int y_dtype, void* workspace,
+                    size_t ws_bytes, unsigned flags, int* dev_status, void* stream) {
+  if (E < 0 || H < 0 || I < 0 || T < 0 || k < 0) return GQ_ERR_INVALID_ARG;
+  if (!valid_act_dtype(x_dtype) || !valid_act_dtype(y_dtype)) return GQ_ERR_DTYPE;
+  if (flags & ~GQ_GEMV_PDL) return GQ_ERR_INVALID_ARG;
+  if (!moe_dims(T, k, E) || !moe_width(FMT, H) || !moe_width(FMT, I)) return GQ_ERR_SHAPE;
+  if (dev_status && (reinterpret_cast<uintptr_t>(dev_status) & 3u)) return GQ_ERR_ALIGNMENT;
+  if (T == 0 || H == 0) return GQ_OK;
+  if (!y) return GQ_ERR_INVALID_ARG;
+  if (misaligned16(y)) return GQ_ERR_ALIGNMENT;
+  cudaStream_t s = as_stream(stream);
+  if (I == 0 || E == 0 || k == 0)
+    return cudaMemsetAsync(y, 0, static_cast<size_t>(T * H * dtype_size(y_dtype)), s) == cudaSuccess
+               ? GQ_OK
+               : GQ_ERR_CUDA;
+  if (!gate || !up || !down || !x || !ids || !weights) return GQ_ERR_INVALID_ARG;
+  if (misaligned16(gate) || misaligned16(up) || misaligned16(down) || misaligned16(x) ||
+      misaligned16(ids) || misaligned16(weights))
+    return GQ_ERR_ALIGNMENT;
+  // super-block units are read 32 bytes a lane
+  if (FMT == GQ_FMT_KSB && ((reinterpret_cast<uintptr_t>(gate) | reinterpret_cast<uintptr_t>(up) |
+                             reinterpret_cast<uintptr_t>(down)) & 31u))
+    return GQ_ERR_ALIGNMENT;
+  const Ws l = ws_layout(T, k, H, I);
+  if (!workspace || ws_bytes < l.total) return GQ_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GQ_ERR_ALIGNMENT;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+
+  MoeArgs a{};
+  a.ids = ids;
+  a.dev_status = dev_status;
+  a.hmax = reinterpret_cast<unsigned*>(ws + l.hmax);
+  a.h = reinterpret_cast<float*>(ws + l.h);
+  a.out = reinterpret_cast<float*>(ws + l.out);
+  a.T = static_cast<int>(T);
+  a.k = static_cast<int>(k);
+  a.E = static_cast<int>(E);
+  const auto row_bytes = [](int64_t K) { return FMT == GQ_FMT_Q4_0 ? K / 32 * 18 : K / 256 * 138; };
+
+  a.w0 = static_cast<const uint8_t*>(gate);
+  a.w1 = static_cast<const uint8_t*>(up);
+  a.x = x;
+  a.xtype = x_dtype;
+  a.two = x_dtype == GQ_F32;
+  a.K = static_cast<int>(H);
+  a.groups = static_cast<int>(I / 16);
+  a.group_bytes = 16 * row_bytes(H);
+  gq_status st = launch_moe<FMT, true>(a, (flags & GQ_GEMV_PDL) != 0, s);
+  if (st != GQ_OK) return st;
+
+  a.w0 = static_cast<const uint8_t*>(down);
+  a.w1 = nullptr;
+  a.x = a.h;
+  a.xtype = GQ_F32;
+  a.two = y_dtype == GQ_F32;
+  a.K = static_cast<int>(I);
+  a.groups = static_cast<int>(H / 16);
+  a.group_bytes = 16 * row_bytes(I);
+  st = launch_moe<FMT, false>(a, true, s);
+  if (st != GQ_OK) return st;
+
+  return launch(moe_sum_kernel, dim3(static_cast<unsigned>((T * H + 255) / 256)), dim3(256), 0, s, true,
+                a.out, ids, weights, a.hmax, y, a.T, a.k, a.E, static_cast<int>(H), y_dtype);
+}
+
+}  // namespace
+}  // namespace gq
+
+extern "C" {
+
+GQ_API size_t gq_moe_workspace_bytes(int fmt, int64_t H, int64_t I, int64_t T, int64_t k) {
+  if ((fmt != GQ_FMT_Q4_0 && fmt != GQ_FMT_KSB) || H <= 0 || I <= 0 || T <= 0 || k <= 0) return 0;
+  if (!gq::moe_dims(T, k, 0) || !gq::moe_width(fmt, H) || !gq::moe_width(fmt, I)) return 0;
+  return gq::ws_layout(T, k, H, I).total;
+}
+
+GQ_API gq_status gq_moe_q4_0_tiled(const void* gate, const void* up, const void* down, int64_t E,
+                                   int64_t H, int64_t I, const void* x, int x_dtype, int64_t T,
+                                   const int32_t* ids, const float* weights, int64_t k, void* y,
+                                   int y_dtype, void* workspace, size_t ws_bytes, unsigned flags,
+                                   int* dev_status, void* stream) {
+  return gq::moe_entry<GQ_FMT_Q4_0>(gate, up, down, E, H, I, x, x_dtype, T, ids, weights, k, y, y_dtype,
+                                    workspace, ws_bytes, flags, dev_status, stream);
+}
+
+GQ_API gq_status gq_moe_ksb_tiled(const void* gate, const void* up, const void* down, int64_t E,
+                                  int64_t H, int64_t I, const void* x, int x_dtype, int64_t T,
+                                  const int32_t* ids, const float* weights, int64_t k, void* y,
+                                  int y_dtype, void* workspace, size_t ws_bytes, unsigned flags,
+                                  int* dev_status, void* stream) {
+  return gq::moe_entry<GQ_FMT_KSB>(gate, up, down, E, H, I, x, x_dtype, T, ids, weights, k, y, y_dtype,
+                                   workspace, ws_bytes, flags, dev_status, stream);
+}
+
+}  // extern "C"

@@ -75,7 +75,7 @@ typedef enum gq_status {
     GQ_ERR_ALIGNMENT = 3,    /* pointer not 16-byte aligned                 */
     GQ_ERR_DTYPE = 4,        /* unsupported element type                    */
     GQ_ERR_NONFINITE = 5,    /* (device) NaN or infinity in quantizer input */
-    GQ_ERR_RANGE = 6,        /* (device) a scale overflowed FP16            */
+    GQ_ERR_RANGE = 6,        /* (device) a scale overflowed, or a bad id    */
     GQ_ERR_TIMEOUT = 7,      /* (device) a bounded wait in a kernel gave up */
     GQ_ERR_CUDA = 8,         /* a CUDA launch or runtime call failed        */
     GQ_ERR_WORKSPACE = 9     /* workspace missing or too small              */
@@ -370,6 +370,79 @@ GQ_API gq_status gq_gemm_ksb(const void* W, int64_t M, int64_t K,
                              const void* X, int x_dtype, int64_t B,
                              void* Y, int y_dtype, void* workspace, size_t ws_bytes,
                              int* dev_status, void* stream);
+
+/* Router of a mixture-of-experts layer (no counterpart on the pages: the step
+ * that says which experts' matrices a token multiplies).
+ *   z[t][e] = sum_h x[t][h] * Wr[e][h];  s = z, or sigmoid(z) with
+ *   GQ_ROUTE_SIGMOID.  ids[t][0..k-1]: the k experts of largest s + bias in
+ *   falling order, the lowest index first among equals.  weights[t][j]:
+ *   softmax(z)[ids] over all E experts, or sigmoid(z)[ids] (without the bias);
+ *   with GQ_ROUTE_NORM divided by their sum over the k (zeros if that is
+ *   zero); then times `scale`.
+ *   x: [T][H] of x_dtype; Wr: [E][H] of w_dtype (any of the three types);
+ *      H % 8 == 0, H <= 2^24, E <= 1024, k <= 16, k <= E, T <= 65536.
+ *   bias: E floats or NULL; only with GQ_ROUTE_SIGMOID (GQ_ERR_INVALID_ARG).
+ *   ids: [T][k] int32; weights: [T][k] fp32.
+ * Products and sums of z are fp64, so which experts are taken does not depend
+ * on the order of a sum; exponentials and weights are fp32 (sigmoids fp64).
+ * A token with a NaN or infinite score gets ids of -1 and weights of 0, and
+ * sets GQ_DEV_NONFINITE.
+ * workspace / ws_bytes: at least gq_moe_route_workspace_bytes(T, E) bytes
+ *   (GQ_ERR_WORKSPACE otherwise), 256-byte aligned, all zero before its first
+ *   use; a successful call leaves it ready for the next call of any sizes;
+ *   after a call that fails, zero it again.  Calls that may run at the same
+ *   time need separate workspaces.
+ * flags: GQ_ROUTE_* and GQ_GEMV_PDL (the call may be scheduled early; it waits
+ *   for the preceding kernel before it reads anything). */
+#define GQ_ROUTE_NORM    2u
+#define GQ_ROUTE_SIGMOID 4u
+GQ_API size_t gq_moe_route_workspace_bytes(int64_t T, int64_t E);
+GQ_API gq_status gq_moe_route(const void* x, int x_dtype, int64_t T, int64_t H, const void* Wr,
+                              int w_dtype, int64_t E, const float* bias, int64_t k, float scale,
+                              int32_t* ids, float* weights, void* workspace, size_t ws_bytes,
+                              unsigned flags, int* dev_status, void* stream);
+
+/* A whole mixture-of-experts layer for a few tokens on 4-bit experts (no
+ * counterpart on the pages: the products of gq_gemv_*_tiled on the matrices
+ * that a router names),
+ *   y[t] = sum_j weights[t][j] * D_e (silu(G_e x[t]) * (U_e x[t])),  e = ids[t][j],
+ * silu(v) = v / (1 + exp(-v)).
+ *   gate, up: tiled storage of the E experts' I x H matrices one after another,
+ *      i.e. of one (E * I) x H matrix (gq_repack_*); down: of E matrices H x I.
+ *      H and I are multiples of 64 (Q4_0) or 256 (KSB), at most 16384; E <= 1024.
+ *      32-byte aligned for KSB.
+ *   x: [T][H] of x_dtype; T <= 64, k <= 16; y: [T][H] of y_dtype.
+ *   ids: [T][k] int32 (as gq_moe_route writes them).  -1 names no expert; any
+ *      other value outside [0, E) counts as -1 and sets GQ_DEV_RANGE.  A token
+ *      may name an expert more than once.  A token that names none gets zeros.
+ *   weights: [T][k] fp32.
+ * Only the experts that some token names are read, each once for up to 16
+ * tokens (fewer for wide matrices).
+ * Arithmetic: products of exact codes with activations in fp16 scaled by a
+ * power of two for each token (16-bit x exactly, down to 2^-39 of the token's
+ * largest; fp32 x, and the activation between the products when y is fp32, as
+ * two fp16 terms, 22 bits; for a 16-bit y the activation between the products
+ * is rounded to 11 bits), fp32 accumulation, one rounding to y_dtype.  Results
+ * do not depend on scheduling.  Non-finite values of a token stay in its own
+ * outputs.
+ * workspace / ws_bytes: at least gq_moe_workspace_bytes(...) bytes, 256-byte
+ *   aligned, all zero before its first use; a successful call leaves it ready
+ *   for the next call of any sizes; after a call that fails, zero it again.
+ *   Calls that may run at the same time need separate workspaces.
+ * flags: 0 or GQ_GEMV_PDL (the first launch may be scheduled early; it waits
+ *   for the preceding kernel, which may be the router, before it reads ids or
+ *   x). */
+GQ_API size_t gq_moe_workspace_bytes(int fmt, int64_t H, int64_t I, int64_t T, int64_t k);
+GQ_API gq_status gq_moe_q4_0_tiled(const void* gate, const void* up, const void* down, int64_t E,
+                                   int64_t H, int64_t I, const void* x, int x_dtype, int64_t T,
+                                   const int32_t* ids, const float* weights, int64_t k, void* y,
+                                   int y_dtype, void* workspace, size_t ws_bytes, unsigned flags,
+                                   int* dev_status, void* stream);
+GQ_API gq_status gq_moe_ksb_tiled(const void* gate, const void* up, const void* down, int64_t E,
+                                  int64_t H, int64_t I, const void* x, int x_dtype, int64_t T,
+                                  const int32_t* ids, const float* weights, int64_t k, void* y,
+                                  int y_dtype, void* workspace, size_t ws_bytes, unsigned flags,
+                                  int* dev_status, void* stream);
 
 #ifdef __cplusplus
 }
