@@ -41,6 +41,8 @@ EXPORTS = (
     "gq_gemv_q4_0_tiled_grouped", "gq_gemv_ksb_tiled_grouped",
     "gq_moe_route_workspace_bytes", "gq_moe_route",
     "gq_moe_workspace_bytes", "gq_moe_q4_0_tiled", "gq_moe_ksb_tiled",
+    "gq_fp8_scales", "gq_quantize_fp8", "gq_dequantize_fp8",
+    "gq_gemm_fp8_workspace_bytes", "gq_gemm_fp8",
 )
 
 _DTYPE_CODE = {torch.float32: GQ_F32, torch.float16: GQ_F16, torch.bfloat16: GQ_BF16}
@@ -126,6 +128,17 @@ def _load() -> ctypes.CDLL:
         f.argtypes = [vp, vp, vp, i64, i64, i64, vp, c_int, i64, vp, vp, i64, vp, c_int, vp,
                       ctypes.c_size_t, c_uint, vp, vp]
         f.restype = c_int
+    L.gq_fp8_scales.argtypes = [i64, i64, i64]
+    L.gq_fp8_scales.restype = ctypes.c_size_t
+    L.gq_quantize_fp8.argtypes = [vp, c_int, i64, i64, i64, vp, vp, vp, vp]
+    L.gq_quantize_fp8.restype = c_int
+    L.gq_dequantize_fp8.argtypes = [vp, vp, i64, i64, i64, vp, c_int, vp]
+    L.gq_dequantize_fp8.restype = c_int
+    L.gq_gemm_fp8_workspace_bytes.argtypes = [i64, i64, i64]
+    L.gq_gemm_fp8_workspace_bytes.restype = ctypes.c_size_t
+    L.gq_gemm_fp8.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, c_int, vp, ctypes.c_size_t, c_uint, vp,
+                              vp]
+    L.gq_gemm_fp8.restype = c_int
     return L
 
 
@@ -635,3 +648,87 @@ def gq_moe_ksb_tiled(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, E
     """gq_moe_q4_0_tiled on super-block experts."""
     return _moe("gq_moe_ksb_tiled", GQ_FMT_KSB, gate, up, down, E, I, x, ids, weights, y_dtype, out,
                 workspace, flags, dev_status, stream)
+
+
+def gq_fp8_scales(R: int, K: int, rows: int) -> int:
+    """Number of scales of an R x K matrix in blocks of rows x 128."""
+    return int(lib.gq_fp8_scales(int(R), int(K), int(rows)))
+
+
+def _fp8_pair(q: torch.Tensor, scales: torch.Tensor, rows: int, what: str):
+    if q.dim() != 2 or q.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"{what} must be a float8_e4m3fn matrix")
+    R, K = q.shape
+    if scales.dtype != torch.float32 or scales.numel() < -(-R // rows) * -(-K // 128):
+        raise ValueError(f"{what} needs an fp32 scale for each block of {rows} x 128 values")
+    return R, K
+
+
+@_on_device
+def gq_quantize_fp8(x: torch.Tensor, rows: int, out: torch.Tensor | None = None,
+                    scales: torch.Tensor | None = None, dev_status: torch.Tensor | None = None,
+                    stream=None):
+    """(codes [R, K] float8_e4m3fn, scales [ceil(R / rows), ceil(K / 128)] fp32) of x
+    [R, K] (fp32, fp16 or bf16; K % 16 == 0) in blocks of rows x 128: rows = 1
+    for activations, 128 for weights."""
+    if x.dim() != 2:
+        raise ValueError("x is [R, K]")
+    if x.dtype not in _DTYPE_CODE:
+        raise TypeError("x must be float32, float16 or bfloat16")
+    if rows not in (1, 128):
+        raise ValueError("rows is 1 or 128")
+    R, K = x.shape
+    if out is None:
+        out = torch.empty((R, K), dtype=torch.float8_e4m3fn, device=x.device)
+    if scales is None:
+        scales = torch.empty((-(-R // rows), -(-K // 128)), dtype=torch.float32, device=x.device)
+    if _fp8_pair(out, scales, rows, "out") != (R, K):
+        raise ValueError("out has another shape than x")
+    _check(lib.gq_quantize_fp8(_ptr(x), _DTYPE_CODE[x.dtype], R, K, rows, _ptr(out), _ptr(scales),
+                               _ptr(dev_status), _raw_stream(stream, x.device)), "gq_quantize_fp8")
+    return out, scales
+
+
+@_on_device
+def gq_dequantize_fp8(q: torch.Tensor, scales: torch.Tensor, rows: int, dtype=torch.float32,
+                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """scale * code of a matrix in blocks of rows x 128, in `dtype`."""
+    R, K = _fp8_pair(q, scales, rows, "q")
+    if dtype not in _DTYPE_CODE:
+        raise TypeError("outputs must be float32, float16 or bfloat16")
+    if out is None:
+        out = torch.empty((R, K), dtype=dtype, device=q.device)
+    elif out.dtype not in _DTYPE_CODE or out.numel() != R * K:
+        raise ValueError("out holds R * K values")
+    _check(lib.gq_dequantize_fp8(_ptr(q), _ptr(scales), R, K, rows, _ptr(out), _DTYPE_CODE[out.dtype],
+                                 _raw_stream(stream, q.device)), "gq_dequantize_fp8")
+    return out
+
+
+def gq_gemm_fp8_workspace_bytes(M: int, K: int, B: int) -> int:
+    return int(lib.gq_gemm_fp8_workspace_bytes(int(M), int(K), int(B)))
+
+
+@_on_device
+def gq_gemm_fp8(W: torch.Tensor, w_scales: torch.Tensor, X: torch.Tensor, x_scales: torch.Tensor,
+                y_dtype=torch.bfloat16, out: torch.Tensor | None = None, workspace="auto",
+                flags: int = 0, dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [B, M] of W [M, K] in 128 x 128 blocks and X [B, K] in 1 x 128 blocks (codes and scales
+    as gq_quantize_fp8 returns them).  workspace: "auto" (a zeroed buffer cached per device and
+    stream) or a uint8 CUDA tensor of gq_gemm_fp8_workspace_bytes(M, K, B) bytes, zero before its
+    first use."""
+    M, K = _fp8_pair(W, w_scales, 128, "W")
+    B, K2 = _fp8_pair(X, x_scales, 1, "X")
+    if K != K2:
+        raise ValueError(f"X has {K2} columns, expected K={K}")
+    if y_dtype not in _DTYPE_CODE:
+        raise TypeError("outputs must be float32, float16 or bfloat16")
+    s = _raw_stream(stream, X.device)
+    if out is None:
+        out = torch.empty((B, M), dtype=y_dtype, device=X.device)
+    elif out.dtype not in _DTYPE_CODE or out.numel() != B * M:
+        raise ValueError("out holds B * M values")
+    ws, ws_bytes = _workspace("gq_gemm_fp8", workspace, lib.gq_gemm_fp8_workspace_bytes(M, K, B), X.device, s)
+    _check(lib.gq_gemm_fp8(_ptr(W), _ptr(w_scales), M, K, _ptr(X), _ptr(x_scales), B, _ptr(out),
+                           _DTYPE_CODE[out.dtype], ws, ws_bytes, flags, _ptr(dev_status), s), "gq_gemm_fp8")
+    return out

@@ -1,0 +1,234 @@
+// gq_fp8.cu -- 8-bit floating-point (e4m3) codes with one fp32 scale for each
+// block of 1 x 128 (activations) or 128 x 128 (weights) values.
+//
+// Rule, in the manner of this library's 4-bit quantizers: s = absmax / 448 (448
+// is e4m3's largest value) and code = e4m3(x / s), both quotients IEEE fp32
+// ones, the second rounded to nearest even and clamped to +-448; s == 0 gives
+// codes 0.  Decoding: x_hat = s * code, one fp32 rounding.
+//
+// All three kernels are bound by memory: each value is read once, in 16-byte
+// loads, eight values to a lane, and a block's values wait in registers for its
+// largest one.  A row block is half a warp's; a 128 x 128 block is a CTA's.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gq.h"
+#include "gq_device.cuh"
+#include "gq_host.h"
+
+namespace gq {
+namespace {
+
+constexpr int kBlk = 128;
+constexpr float kTop = 448.0f;
+
+template <int TYPE>
+__device__ __forceinline__ void load8(const void* base, int64_t at, float v[8]) {
+  if constexpr (TYPE == GQ_F32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    const float4 a = __ldcs(p), b = __ldcs(p + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if constexpr (TYPE == GQ_F16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[q]));
+        v[2 * q] = f.x, v[2 * q + 1] = f.y;
+      } else {
+        v[2 * q] = __uint_as_float(w[q] << 16);
+        v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ unsigned absmax8(const float v[8]) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+// Eight codes of values with scale s.
+__device__ __forceinline__ uint2 codes8(const float v[8], float s) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t c[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const float2 f = make_float2(s > 0.f ? __fdiv_rn(v[4 * h + 2 * p], s) : 0.f,
+                                   s > 0.f ? __fdiv_rn(v[4 * h + 2 * p + 1], s) : 0.f);
+      c[p] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+    }
+    w[h] = c[0] | (c[1] << 16);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Row blocks: half a warp each, eight values a lane.
+template <int TYPE>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const void* x, int64_t R, int K, int kblocks,
+                                                            uint8_t* q, float* scales, int* dev_status) {
+  const int64_t block = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 4;
+  const int lane = threadIdx.x & 15;
+  const bool in = block < R * kblocks;
+  const int64_t r = in ? block / kblocks : 0;
+  const int kb = in ? static_cast<int>(block - r * kblocks) : 0;
+  const int k = kb * kBlk + 8 * lane;
+  float v[8] = {};
+  const bool mine = in && k < K;
+  if (mine) load8<TYPE>(x, r * K + k, v);
+  unsigned m = absmax8(v);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const float s = __fdiv_rn(__uint_as_float(m), kTop);
+  if (!mine) return;
+  *reinterpret_cast<uint2*>(q + r * K + k) = codes8(v, s);
+  if (lane == 0) {
+    scales[block] = s;
+    if (m >= 0x7F800000u) report(dev_status, GQ_DEV_NONFINITE);
+  }
+}
+
+// 128 x 128 blocks: one CTA each, 16 lanes to a row, 16 rows at a time.
+template <int TYPE>
+__global__ void __launch_bounds__(256) quantize_tiles_kernel(const void* x, int64_t R, int K, int kblocks,
+                                                             uint8_t* q, float* scales, int* dev_status) {
+  __shared__ unsigned top[8];
+  const int64_t rb = blockIdx.x / kblocks;
+  const int kb = static_cast<int>(blockIdx.x - rb * kblocks);
+  const int k = kb * kBlk + 8 * (threadIdx.x & 15);
+  const int64_t r0 = rb * kBlk + (threadIdx.x >> 4);
+  float v[8][8];
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (r0 + 16 * i < R && k < K) {
+      load8<TYPE>(x, (r0 + 16 * i) * K + k, v[i]);
+      m = max(m, absmax8(v[i]));
+    }
+  }
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, top[i]);
+  const float s = __fdiv_rn(__uint_as_float(m), kTop);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (r0 + 16 * i < R && k < K)
+      *reinterpret_cast<uint2*>(q + (r0 + 16 * i) * K + k) = codes8(v[i], s);
+  if (threadIdx.x == 0) {
+    scales[blockIdx.x] = s;
+    if (m >= 0x7F800000u) report(dev_status, GQ_DEV_NONFINITE);
+  }
+}
+
+// Sixteen codes a thread.
+__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* q, const float* scales, int64_t R,
+                                                         int K, int kblocks, int shift, void* out, int type) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 16;
+  if (i >= R * K) return;
+  const int64_t r = i / K;
+  const int k = static_cast<int>(i - r * K);
+  const float s = __ldg(scales + (r >> shift) * kblocks + k / kBlk);
+  const uint4 u = __ldcs(reinterpret_cast<const uint4*>(q + i));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  float v[16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));  // exact
+    v[2 * j] = __fmul_rn(s, f.x);
+    v[2 * j + 1] = __fmul_rn(s, f.y);
+  }
+  if (type == GQ_F32) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(out) + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) __stcs(d + j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+  } else {
+    uint32_t p[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (type == GQ_F16) {
+        const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+        p[j] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        p[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + i);
+    __stcs(d, make_uint4(p[0], p[1], p[2], p[3]));
+    __stcs(d + 1, make_uint4(p[4], p[5], p[6], p[7]));
+  }
+}
+
+gq_status check_matrix(int64_t R, int64_t K, int64_t rows) {
+  if (R < 0 || K < 0 || (rows != 1 && rows != kBlk)) return GQ_ERR_INVALID_ARG;
+  if (K % 16 || K > (1LL << 24) || R > 0x7FFFFFFFLL) return GQ_ERR_SHAPE;
+  return GQ_OK;
+}
+
+}  // namespace
+}  // namespace gq
+
+extern "C" {
+
+GQ_API size_t gq_fp8_scales(int64_t R, int64_t K, int64_t rows) {
+  if (gq::check_matrix(R, K, rows) != GQ_OK) return 0;
+  return static_cast<size_t>((R + rows - 1) / rows) * static_cast<size_t>((K + gq::kBlk - 1) / gq::kBlk);
+}
+
+GQ_API gq_status gq_quantize_fp8(const void* x, int x_dtype, int64_t R, int64_t K, int64_t rows,
+                                 void* q, float* scales, int* dev_status, void* stream) {
+  using namespace gq;
+  if (!valid_act_dtype(x_dtype)) return GQ_ERR_DTYPE;
+  const gq_status st = check_matrix(R, K, rows);
+  if (st != GQ_OK) return st;
+  if (dev_status && (reinterpret_cast<uintptr_t>(dev_status) & 3u)) return GQ_ERR_ALIGNMENT;
+  if (R == 0 || K == 0) return GQ_OK;
+  if (!x || !q || !scales) return GQ_ERR_INVALID_ARG;
+  if (misaligned16(x) || misaligned16(q) || misaligned16(scales)) return GQ_ERR_ALIGNMENT;
+  const int kblocks = static_cast<int>((K + kBlk - 1) / kBlk);
+  const int64_t blocks = static_cast<int64_t>(gq_fp8_scales(R, K, rows));
+  const int64_t grid = rows == 1 ? (blocks + 15) / 16 : blocks;
+  if (grid > 0x7FFFFFFFLL) return GQ_ERR_SHAPE;
+  auto run = [&](auto kern) {
+    return launch(kern, dim3(static_cast<unsigned>(grid)), dim3(256), 0, as_stream(stream), false, x, R,
+                  static_cast<int>(K), kblocks, static_cast<uint8_t*>(q), scales, dev_status);
+  };
+  if (rows == 1)
+    return x_dtype == GQ_F32   ? run(quantize_rows_kernel<GQ_F32>)
+           : x_dtype == GQ_F16 ? run(quantize_rows_kernel<GQ_F16>)
+                               : run(quantize_rows_kernel<GQ_BF16>);
+  return x_dtype == GQ_F32   ? run(quantize_tiles_kernel<GQ_F32>)
+         : x_dtype == GQ_F16 ? run(quantize_tiles_kernel<GQ_F16>)
+                             : run(quantize_tiles_kernel<GQ_BF16>);
+}
+
+GQ_API gq_status gq_dequantize_fp8(const void* q, const float* scales, int64_t R, int64_t K,
+                                   int64_t rows, void* out, int out_dtype, void* stream) {
+  using namespace gq;
+  if (!valid_act_dtype(out_dtype)) return GQ_ERR_DTYPE;
+  const gq_status st = check_matrix(R, K, rows);
+  if (st != GQ_OK) return st;
+  if (R == 0 || K == 0) return GQ_OK;
+  if (!q || !scales || !out) return GQ_ERR_INVALID_ARG;
+  if (misaligned16(q) || misaligned16(scales) || misaligned16(out)) return GQ_ERR_ALIGNMENT;
+  const int64_t grid = (R * K / 16 + 255) / 256;
+  if (grid > 0x7FFFFFFFLL) return GQ_ERR_SHAPE;
+  return launch(dequantize_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, as_stream(stream), false,
+                static_cast<const uint8_t*>(q), scales, R, static_cast<int>(K),
+                static_cast<int>((K + kBlk - 1) / kBlk), rows == 1 ? 0 : 7, out, out_dtype);
+}
+
+}  // extern "C"

@@ -1,0 +1,516 @@
+// gq_fp8_gemm.cu -- product of 8-bit block-scaled matrices on the tcgen05
+// tensor cores,
+//   Y[b][m] = sum_g sx[b][g] * sw[m / 128][g] * sum_{k in group g} X[b][k] * W[m][k],
+// groups of 128 along K, e4m3 codes, fp32 scales.
+//
+// The scales change every 128 values of K, so the tensor core sums one group
+// at a time and the groups are added in registers.  Tokens are the rows of the
+// accumulator (the lanes of tensor memory) and weight rows its columns, which
+// makes the factor of a group one number for a thread: its token's scale times
+// the weight block's.
+//
+// One CTA per SM, over tiles of 128 tokens x BN weight rows and k-steps of one
+// group:
+//  * warp 8 (producer): both operands' 128-byte rows by TMA, 128-byte swizzle;
+//  * warp 9 (MMA): four tcgen05.mma (K = 32) to a k-step, into one of two
+//    accumulator buffers in tensor memory;
+//  * warps 0..7: read the buffer back and add it, times the factor, to sums in
+//    registers (a thread holds one token and BN / 2 columns); at the end of a
+//    tile they round once and store.
+// While the warps add one group the MMAs fill the other buffer.
+//
+// When tiles are few, the k-steps of all tiles are divided evenly over the SMs
+// and a tile cut between CTAs is joined through fp32 partial sums in the
+// workspace: the CTA that completes it adds the parts in CTA order, so results
+// do not depend on scheduling.  For fewer than 128 tokens only the rows that
+// exist are loaded; the other lanes hold garbage that nothing reads.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gq.h"
+#include "gq_device.cuh"
+#include "gq_host.h"
+#include "gq_tc.cuh"
+
+namespace gq {
+namespace {
+
+constexpr int kBM = 128;                 // tokens of a tile
+constexpr int kBK = 128;                 // bytes of K in a step: one group of scales
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kTileX = kBM * kBK;
+constexpr int kMaxCut = 4096;            // tiles of a split call at most
+constexpr size_t kCountBytes = kMaxCut * sizeof(int);
+
+// Unit u of T * S: k-step u % S of tile u / S.  CTA i of P takes [U i / P, U (i + 1) / P).
+struct Split {
+  int64_t U;
+  int S, T, P;
+  int tm;  // tiles along M; tile t covers tokens 128 (t / tm) and weight rows BN (t % tm)
+};
+
+struct Args {
+  const float* sx;
+  const float* sw;
+  void* Y;
+  int* dev_status;
+  long long budget;
+  int64_t M;
+  int B, kblocks, ytype, xrows;  // xrows: rows of an X box
+  int ybytes;                    // alignment of Y's rows, 16 or 32 bytes, or 0
+  Split sp;
+  int* counts;
+  float* parts;  // [P][2][rows][BN]
+};
+
+extern __shared__ __align__(1024) uint8_t fsm[];
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B (both K-major), fp32 D.
+constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t v[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, int type) {
+  if (type == GQ_F16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// N (a multiple of 16) consecutive outputs of one token from weight row m on.
+template <int N>
+__device__ __forceinline__ void store_row(const Args& a, int64_t row, int64_t m, const float* v) {
+  const int64_t at = row * a.M + m;
+  if (a.ybytes && m + N <= a.M) {
+    if (a.ytype == GQ_F32) {
+      float* d = static_cast<float*>(a.Y) + at;
+#pragma unroll
+      for (int i = 0; i < N; i += 8) {
+        if (a.ybytes == 32) {
+          store32(d + i, reinterpret_cast<const uint32_t*>(v + i));
+        } else {
+          *reinterpret_cast<float4*>(d + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          *reinterpret_cast<float4*>(d + i + 4) = make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
+        }
+      }
+    } else {
+      uint16_t* d = static_cast<uint16_t*>(a.Y) + at;
+#pragma unroll
+      for (int i = 0; i < N; i += 16) {
+        uint32_t p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = pack2(v[i + 2 * j], v[i + 2 * j + 1], a.ytype);
+        if (a.ybytes == 32) {
+          store32(d + i, p);
+        } else {
+          *reinterpret_cast<uint4*>(d + i) = make_uint4(p[0], p[1], p[2], p[3]);
+          *reinterpret_cast<uint4*>(d + i + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+        }
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (m + i < a.M) store_elem(a.Y, at + i, v[i], a.ytype);
+}
+
+__device__ __forceinline__ int64_t unit_begin(const Split& sp, int i) { return sp.U * i / sp.P; }
+__device__ __forceinline__ int unit_owner(const Split& sp, int64_t u) {
+  return static_cast<int>(((u + 1) * sp.P - 1) / sp.U);
+}
+
+// The tiles of a CTA's run and the k-steps of each: a cut first or last tile
+// before the whole ones between them, so that cut tiles complete early.
+struct Run {
+  int ta, tb, S;
+  int64_t u0, u1;
+  __device__ __forceinline__ int count() const { return tb - ta + 1; }
+  __device__ __forceinline__ void get(int k, int& t, int& k0, int& k1) const {
+    t = (k == 0) ? ta : (k == 1) ? tb : ta + k - 1;
+    k0 = (t == ta) ? static_cast<int>(u0 - static_cast<int64_t>(ta) * S) : 0;
+    k1 = (t == tb) ? static_cast<int>(u1 - static_cast<int64_t>(tb) * S) : S;
+  }
+};
+__device__ __forceinline__ Run run_of(const Split& sp, int i) {
+  Run r;
+  r.S = sp.S;
+  r.u0 = unit_begin(sp, i);
+  r.u1 = unit_begin(sp, i + 1);
+  r.ta = static_cast<int>(r.u0 / sp.S);
+  r.tb = static_cast<int>((r.u1 - 1) / sp.S);
+  return r;
+}
+
+template <int BN>
+struct Cfg {
+  static constexpr int kStageBytes = kTileX + BN * kBK;
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+                    const Args a) {
+  using C = Cfg<BN>;
+  constexpr int kStages = C::kStages, kHalf = BN / 2;
+  const uint32_t base = smem_addr(fsm);
+  const uint32_t ring = ((base + 1023u) & ~1023u) - base;
+  uint64_t* full = reinterpret_cast<uint64_t*>(fsm + ring + kStages * C::kStageBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* d_full = empty + kStages;  // [2] a group's sums are in the buffer
+  uint64_t* d_empty = d_full + 2;      // [2] they have been read
+  uint64_t* done = d_empty + 2;        // every MMA of the CTA has finished
+  uint64_t* e_bar = done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(e_bar + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  int* last_flag = abort_flag + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Run run = run_of(a.sp, blockIdx.x);
+  const int nrun = run.count();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], kEpiWarps);
+    }
+    mbar_init(done, 1);
+    mbar_init(e_bar, kEpiWarps);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kEpiWarps + 1) {
+    tmem_alloc(tmem_slot, 2 * BN);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  auto aborted = [&]() { return *reinterpret_cast<volatile int*>(abort_flag) != 0; };
+  auto fail = [&]() {
+    report(a.dev_status, GQ_DEV_TIMEOUT);
+    *reinterpret_cast<volatile int*>(abort_flag) = 1;
+  };
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == kEpiWarps) {
+    // ---------------------------------------------------------- producer
+    if (lane == 0) {
+      bool ok = true;
+      int g = 0;
+      const uint32_t bytes = static_cast<uint32_t>(a.xrows * kBK + BN * kBK);
+      for (int k = 0; k < nrun && ok; ++k) {
+        int t, k0, k1;
+        run.get(k, t, k0, k1);
+        const int row0 = (t / a.sp.tm) * kBM, m0 = (t % a.sp.tm) * BN;
+        for (int ks = k0; ks < k1; ++ks, ++g) {
+          const int s = g % kStages;
+          if (!mbar_wait(&empty[s], ((g / kStages) & 1u) ^ 1u, a.budget) || aborted()) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = fsm + ring + s * C::kStageBytes;
+          mbar_arrive_expect_tx(&full[s], bytes);
+          tma_load_2d(st, &xmap, ks * kBK, row0, &full[s]);
+          tma_load_2d(st + kTileX, &wmap, ks * kBK, m0, &full[s]);
+        }
+      }
+      if (!ok) fail();
+      // every issued copy lands before shared memory is released
+      for (int i = max(0, g - kStages); i < g; ++i)
+        if (!mbar_wait(&full[i % kStages], (i / kStages) & 1u, a.budget)) {
+          report(a.dev_status, GQ_DEV_TIMEOUT);
+          break;
+        }
+    }
+    __syncwarp();
+  } else if (warp == kEpiWarps + 1) {
+    // --------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(kBM, BN);
+      bool ok = true;
+      const int64_t steps = run.u1 - run.u0;
+      for (int64_t g = 0; g < steps; ++g) {
+        const int s = static_cast<int>(g % kStages), buf = static_cast<int>(g & 1);
+        if (!mbar_wait(&full[s], static_cast<uint32_t>(g / kStages) & 1u, a.budget) ||
+            !mbar_wait(&d_empty[buf], (static_cast<uint32_t>(g >> 1) & 1u) ^ 1u, a.budget) || aborted()) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t xs = base + ring + s * C::kStageBytes, wsm = xs + kTileX;
+#pragma unroll
+        for (int i = 0; i < kBK / 32; ++i)
+          umma_e4m3(tmem + buf * BN, umma_desc_sw128(xs + 32 * i), umma_desc_sw128(wsm + 32 * i), idesc, i != 0);
+        umma_commit(&empty[s]);
+        umma_commit(&d_full[buf]);
+      }
+      if (!ok) fail();
+      umma_commit(done);  // also on the abort path: tensor memory is quiet before exit
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- epilogue
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
+    const int cols0 = half * kHalf;
+    const int prows = min(kBM, a.B);  // rows of a part
+    uint32_t ephase = 0;
+    auto epi_sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(e_bar);
+      const bool r = mbar_wait(e_bar, ephase & 1u, a.budget);
+      ++ephase;
+      return r;
+    };
+    bool ok = true;
+    uint32_t g = 0;
+    for (int k = 0; k < nrun && ok; ++k) {
+      int t, k0, k1;
+      run.get(k, t, k0, k1);
+      const int row0 = (t / a.sp.tm) * kBM;
+      const int64_t m0 = static_cast<int64_t>(t % a.sp.tm) * BN;
+      const int row = row0 + 32 * quarter + lane;
+      const bool row_ok = row < a.B;
+      const bool any = row0 + 32 * quarter < a.B;  // some lane of the warp has a token
+      const float* sx = a.sx + static_cast<int64_t>(row_ok ? row : 0) * a.kblocks;
+      const int64_t wb = min((m0 + cols0) / 128, (a.M - 1) / 128);  // this half's weight block
+      const float* sw = a.sw + wb * a.kblocks;
+      float acc[kHalf];
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
+      float f = __ldg(sx + k0) * __ldg(sw + k0);
+      for (int ks = k0; ks < k1; ++ks, ++g) {
+        const int buf = g & 1;
+        const float fnext = ks + 1 < k1 ? __ldg(sx + ks + 1) * __ldg(sw + ks + 1) : 0.f;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&d_full[buf], (g >> 1) & 1u, a.budget)) || aborted()) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (any) {
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(tmem + lane_base + static_cast<uint32_t>(buf * BN + cols0 + c), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(f, __uint_as_float(v[i]), acc[c + i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&d_empty[buf]);
+        f = fnext;
+      }
+      if (!ok) break;
+      if (k1 - k0 == a.sp.S) {
+        if (row_ok) store_row<kHalf>(a, row, m0 + cols0, acc);
+        continue;
+      }
+      // a cut tile: publish this part; the CTA that completes the tile adds
+      // the parts in CTA order and resets the count
+      const int slot = (t == run.ta) ? 0 : 1;
+      const int prow = 32 * quarter + lane;
+      if (row_ok) {
+        float4* d = reinterpret_cast<float4*>(
+            a.parts + ((static_cast<int64_t>(blockIdx.x) * 2 + slot) * prows + prow) * BN + cols0);
+#pragma unroll
+        for (int i = 0; i < kHalf / 4; ++i)
+          __stcg(d + i, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
+      }
+      __threadfence();
+      if (!(ok = __all_sync(0xFFFFFFFFu, epi_sync()))) break;
+      if (threadIdx.x == 0)
+        *reinterpret_cast<volatile int*>(last_flag) =
+            atomicAdd(&a.counts[t], k1 - k0) + (k1 - k0) == a.sp.S;
+      if (!(ok = __all_sync(0xFFFFFFFFu, epi_sync()))) break;
+      if (!*reinterpret_cast<volatile int*>(last_flag)) continue;
+      __threadfence();
+      const int64_t first = static_cast<int64_t>(t) * a.sp.S;
+      const int i0 = unit_owner(a.sp, first), i1 = unit_owner(a.sp, first + a.sp.S - 1);
+      if (row_ok) {
+        for (int i = i0; i <= i1; ++i) {
+          const int sl = (unit_begin(a.sp, i) / a.sp.S == t) ? 0 : 1;
+          const float4* p = reinterpret_cast<const float4*>(
+              a.parts + ((static_cast<int64_t>(i) * 2 + sl) * prows + prow) * BN + cols0);
+#pragma unroll
+          for (int q = 0; q < kHalf / 4; ++q) {
+            const float4 v = __ldcg(p + q);
+            acc[4 * q] = (i == i0 ? 0.f : acc[4 * q]) + v.x;
+            acc[4 * q + 1] = (i == i0 ? 0.f : acc[4 * q + 1]) + v.y;
+            acc[4 * q + 2] = (i == i0 ? 0.f : acc[4 * q + 2]) + v.z;
+            acc[4 * q + 3] = (i == i0 ? 0.f : acc[4 * q + 3]) + v.w;
+          }
+        }
+        store_row<kHalf>(a, row, m0 + cols0, acc);
+      }
+      if (threadIdx.x == 0) a.counts[t] = 0;
+    }
+    if (!ok && lane == 0) fail();
+  }
+
+  // teardown: every MMA has finished before tensor memory is freed
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kEpiWarps + 1) {
+    if (lane == 0 && !mbar_wait(done, 0, a.budget)) report(a.dev_status, GQ_DEV_TIMEOUT);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * BN);
+  }
+}
+
+// ------------------------------------------------------------------- host
+// Tiles of 128 x 256 run the tensor core best (fewer shared-memory reads for
+// each multiply-add) and are taken when there are enough of them; otherwise
+// tiles of 128 x 128, whole ones if they fill most of the SMs, else cut.
+struct Choice {
+  int bn;
+  Split sp;
+};
+Choice choose(int64_t M, int64_t K, int64_t B) {
+  const int64_t sms = sm_count();
+  const int64_t tb = (B + kBM - 1) / kBM, S = (K + kBK - 1) / kBK;
+  auto split = [&](int bn, int64_t p) {
+    Split s;
+    s.S = static_cast<int>(S);
+    s.tm = static_cast<int>((M + bn - 1) / bn);
+    s.T = static_cast<int>(tb * s.tm);
+    s.U = tb * s.tm * S;
+    s.P = static_cast<int>(i64min(p, s.U));
+    return s;
+  };
+  const int64_t t256 = tb * ((M + 255) / 256), t128 = tb * ((M + 127) / 128);
+  if (t256 >= 2 * sms) return Choice{256, split(256, t256)};
+  if (t128 > sms) return Choice{128, split(128, t128)};
+  if (10 * t128 >= 8 * sms && B > 64) return Choice{128, split(128, t128)};
+  return Choice{128, split(128, sms)};
+}
+
+size_t ws_bytes_of(const Choice& c, int64_t B) {
+  if (c.sp.P == c.sp.T) return kCountBytes;  // whole tiles: no parts
+  const int64_t rows = B < kBM ? B : kBM;
+  return kCountBytes + static_cast<size_t>(c.sp.P) * 2 * static_cast<size_t>(rows) * c.bn * sizeof(float);
+}
+
+bool gemm_dims(int64_t M, int64_t K, int64_t B) {
+  if (K % 16 || K > (1LL << 24) || M > 0x7FFFFFFFLL - 256 || B > 0x7FFFFFFFLL - 256) return false;
+  const int64_t t = ((B + kBM - 1) / kBM) * ((M + 127) / 128);
+  return t <= 0x7FFFFFFFLL;
+}
+
+gq_status encode(CUtensorMap* map, const void* p, int64_t rows, int64_t K, int box_rows) {
+  EncodeTiled enc = tensor_map_encoder();
+  if (!enc) return GQ_ERR_CUDA;
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(K)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dim, stride, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? GQ_OK
+             : GQ_ERR_CUDA;
+}
+
+template <int BN>
+gq_status launch_fp8(const CUtensorMap& xmap, const CUtensorMap& wmap, const Args& a, bool pdl, cudaStream_t s) {
+  auto kern = fp8_gemm_kernel<BN>;
+  thread_local unsigned long long configured_ctx = 0;  // per host thread and context
+  const unsigned long long ctx = context_id();
+  if (ctx == 0 || ctx != configured_ctx) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::kSmem) != cudaSuccess)
+      return GQ_ERR_CUDA;
+    configured_ctx = ctx;
+  }
+  return launch(kern, dim3(static_cast<unsigned>(a.sp.P)), dim3(kThreads), Cfg<BN>::kSmem, s, pdl, xmap, wmap, a);
+}
+
+}  // namespace
+}  // namespace gq
+
+extern "C" {
+
+GQ_API size_t gq_gemm_fp8_workspace_bytes(int64_t M, int64_t K, int64_t B) {
+  if (M <= 0 || K <= 0 || B <= 0 || !gq::gemm_dims(M, K, B)) return 0;
+  return gq::ws_bytes_of(gq::choose(M, K, B), B);
+}
+
+GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, int64_t K, const void* X,
+                             const float* x_scales, int64_t B, void* Y, int y_dtype, void* workspace,
+                             size_t ws_bytes, unsigned flags, int* dev_status, void* stream) {
+  using namespace gq;
+  if (M < 0 || K < 0 || B < 0) return GQ_ERR_INVALID_ARG;
+  if (!valid_act_dtype(y_dtype)) return GQ_ERR_DTYPE;
+  if (flags & ~GQ_GEMV_PDL) return GQ_ERR_INVALID_ARG;
+  if (!gemm_dims(M, K, B)) return GQ_ERR_SHAPE;
+  if (dev_status && (reinterpret_cast<uintptr_t>(dev_status) & 3u)) return GQ_ERR_ALIGNMENT;
+  if (M == 0 || B == 0) return GQ_OK;
+  if (!Y) return GQ_ERR_INVALID_ARG;
+  if (misaligned16(Y)) return GQ_ERR_ALIGNMENT;
+  cudaStream_t s = as_stream(stream);
+  if (K == 0)
+    return cudaMemsetAsync(Y, 0, static_cast<size_t>(B) * M * dtype_size(y_dtype), s) == cudaSuccess
+               ? GQ_OK
+               : GQ_ERR_CUDA;
+  if (!W || !w_scales || !X || !x_scales) return GQ_ERR_INVALID_ARG;
+  if (misaligned16(W) || misaligned16(X) || misaligned16(w_scales) || misaligned16(x_scales))
+    return GQ_ERR_ALIGNMENT;
+  const Choice c = choose(M, K, B);
+  if (!workspace || ws_bytes < ws_bytes_of(c, B)) return GQ_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GQ_ERR_ALIGNMENT;
+
+  Args a{};
+  a.sx = x_scales;
+  a.sw = w_scales;
+  a.Y = Y;
+  a.dev_status = dev_status;
+  a.budget = kWaitBudget;
+  a.M = M;
+  a.B = static_cast<int>(B);
+  a.kblocks = static_cast<int>((K + kBK - 1) / kBK);
+  a.ytype = y_dtype;
+  a.xrows = static_cast<int>(B < kBM ? (B + 7) / 8 * 8 : kBM);
+  const int64_t align = static_cast<int64_t>((reinterpret_cast<uintptr_t>(Y) | static_cast<uintptr_t>(M * dtype_size(y_dtype))) & 31u);
+  a.ybytes = align == 0 ? 32 : align == 16 ? 16 : 0;
+  a.sp = c.sp;
+  a.counts = static_cast<int*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCountBytes);
+  CUtensorMap xmap, wmap;
+  gq_status st = encode(&xmap, X, B, K, a.xrows);
+  if (st == GQ_OK) st = encode(&wmap, W, M, K, c.bn);
+  if (st != GQ_OK) return st;
+  const bool pdl = (flags & GQ_GEMV_PDL) != 0;
+  return c.bn == 256 ? launch_fp8<256>(xmap, wmap, a, pdl, s) : launch_fp8<128>(xmap, wmap, a, pdl, s);
+}
+
+}  // extern "C"

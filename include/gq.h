@@ -444,6 +444,50 @@ GQ_API gq_status gq_moe_ksb_tiled(const void* gate, const void* up, const void* 
                                   int y_dtype, void* workspace, size_t ws_bytes, unsigned flags,
                                   int* dev_status, void* stream);
 
+/* 8-bit blocks (no counterpart on the pages: the library's rule for block
+ * quantization, with e4m3 floating-point codes).  A matrix of R rows of K
+ * values is stored as R x K one-byte codes (row-major) and one fp32 scale for
+ * each block of `rows` x 128 values: rows = 1 for activations, 128 for
+ * weights; blocks at the right and lower edges are shorter.  Scales:
+ * [ceil(R / rows)][ceil(K / 128)], row-major; gq_fp8_scales() is their number
+ * (0 for a bad shape).
+ * Quantizing: s = absmax / 448, code = e4m3(x / s) clamped to +-448, IEEE fp32
+ * quotients, round to nearest even; s == 0 gives codes 0.
+ *   x: [R][K] of x_dtype; K % 16 == 0, K <= 2^24, R <= 2^31 - 1.
+ *   q: R * K bytes; scales: gq_fp8_scales(R, K, rows) floats.
+ *   dev_status: optional; GQ_DEV_NONFINITE if any input is NaN or infinite
+ *     (that block's codes and scale are then unspecified).
+ * Decoding: out = s * code, rounded once to fp32 and then to out_dtype. */
+GQ_API size_t gq_fp8_scales(int64_t R, int64_t K, int64_t rows);
+GQ_API gq_status gq_quantize_fp8(const void* x, int x_dtype, int64_t R, int64_t K, int64_t rows,
+                                 void* q, float* scales, int* dev_status, void* stream);
+GQ_API gq_status gq_dequantize_fp8(const void* q, const float* scales, int64_t R, int64_t K,
+                                   int64_t rows, void* out, int out_dtype, void* stream);
+
+/* Product of 8-bit block-scaled matrices on the tcgen05 tensor cores (no
+ * counterpart on the pages),
+ *   Y[b][m] = sum_g x_scales[b][g] * w_scales[m / 128][g] *
+ *             sum_{k in 128 g .. 128 g + 127} X[b][k] * W[m][k].
+ *   W: [M][K] codes with scales of 128 x 128 blocks; X: [B][K] codes with
+ *      scales of 1 x 128 blocks (gq_quantize_fp8).  K % 16 == 0, K <= 2^24;
+ *      any M and B.
+ *   Y: [B][M] of y_dtype (GQ_F32, GQ_F16 or GQ_BF16), row-major.
+ * Arithmetic: exact products summed in fp32 over a group of 128 on the tensor
+ * core, the groups' sums times the two scales' fp32 product added in fp32,
+ * rounded once to y_dtype.  Results do not depend on scheduling.
+ * workspace / ws_bytes: at least gq_gemm_fp8_workspace_bytes(M, K, B) bytes
+ *   (GQ_ERR_WORKSPACE otherwise), 256-byte aligned, all zero before its first
+ *   use; a successful call leaves it ready for the next call of any sizes;
+ *   after a call that fails or reports GQ_DEV_TIMEOUT, zero it again.  Calls
+ *   that may run at the same time need separate workspaces.
+ * flags: 0 or GQ_GEMV_PDL (the call may be scheduled early; it waits for the
+ *   preceding kernel before it reads anything).
+ * dev_status: optional, receives GQ_DEV_TIMEOUT if a pipeline wait gives up. */
+GQ_API size_t gq_gemm_fp8_workspace_bytes(int64_t M, int64_t K, int64_t B);
+GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, int64_t K, const void* X,
+                             const float* x_scales, int64_t B, void* Y, int y_dtype, void* workspace,
+                             size_t ws_bytes, unsigned flags, int* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
