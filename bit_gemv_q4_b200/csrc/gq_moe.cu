@@ -16,24 +16,25 @@
 // the (token, slot) pairs sorted by expert (stable), and segments of an expert
 // with at most `cap` of its pairs.  The work of all segments, 16 weight rows
 // at a time, is cut into even runs, one for each CTA; a run's row groups form
-// one string of units (the 576 or 1104 bytes that one warp multiplies at a
-// time), which its 16 warps share evenly, so that the split is even whatever
-// the sizes are.  Units are read straight into registers, a few ahead: tiled
-// storage is ordered by the lanes that multiply it, so a warp reads whole
-// lines.  Sums of a row group that several warps share meet in a shared table
-// and are added in warp order: results do not depend on scheduling.
+// one string of stages (8 blocks of 32 weights x 16 rows, 2.3 KB), which its 16
+// warps share evenly, so that the split is even whatever the sizes are.  Each
+// warp copies its own stages to its own ring in shared memory (cp.async), a
+// few ahead: tiled storage is ordered by the lanes that multiply it, so the
+// copies are whole lines and a lane reads back its own codes, and warps wait
+// for nothing but their own copies.  (Reading units straight into registers,
+// eight ahead, ran at 1.5 TB/s: loads that share a scoreboard are waited for
+// together.)  Sums of a row group that several warps share meet in a shared
+// table and are added in warp order: results do not depend on scheduling.
 //
-// Arithmetic.  As in the tiled GEMV a nibble mask makes an fp16 subnormal out
-// of a code, exactly.  The warp MMA's eight columns are the expert's tokens.
-// Activations are scaled by a power of two for each token so that the largest
-// lies in [2^14, 2^15); 16-bit inputs then enter as one fp16 column, exact down
-// to 2^-39 of the largest.  fp32 inputs, and h when y is fp32, enter as two
-// columns (the fp16 value and the fp16 remainder: 22 bits); for a 16-bit y, h
-// enters as one column, rounded to 11 bits, which is below the rounding of y.
-// Weights 16..31 of a block stay in the high nibble, 16 times too large, and
-// their activations are scaled by 1/16; the offset -8 enters as the MMA's
-// accumulator input, -8 * (block sum of x).  Products are exact, sums are
-// fp32.
+// Arithmetic.  Codes become the fp16 values code - 8, exactly: the nibble goes
+// to the low mantissa bits of 1024, from which 1032 is subtracted, or stays in
+// the high nibble (1024 + 16 code, times 1/16, minus 72).  The warp MMA's eight
+// columns are the expert's tokens.  Activations are scaled by a power of two
+// for each token so that the largest lies in [2^14, 2^15); 16-bit inputs then
+// enter as one fp16 column, exact down to 2^-39 of the largest.  fp32 inputs,
+// and h when y is fp32, enter as two columns (the fp16 value and the fp16
+// remainder: 22 bits); for a 16-bit y, h enters as one column, rounded to 11
+// bits, which is below the rounding of y.  Products are exact, sums are fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -54,19 +55,12 @@ constexpr int kMaxK = 16384;
 constexpr int kMaxCols = 16;                // columns of a segment: two n8 tiles
 constexpr size_t kSmemBudget = 227 * 1024;
 
-// A unit of tiled storage: what one warp multiplies at a time.
-template <int FMT>
-struct Unit;
-template <>
-struct Unit<GQ_FMT_Q4_0> {  // two blocks of 32 weights x 16 rows
-  static constexpr int kBlocks = 2, kTileUnits = 32, kTileBytes = 18432, kCodeBytes = 512;
-  static constexpr int kWords = 6, kAhead = 8;
-};
-template <>
-struct Unit<GQ_FMT_KSB> {   // four sub-blocks of 32 weights x 16 rows
-  static constexpr int kBlocks = 4, kTileUnits = 16, kTileBytes = 17664, kCodeBytes = 1024;
-  static constexpr int kWords = 12, kAhead = 4;
-};
+// A stage: 8 blocks of 32 weights x 16 rows, what a warp copies at a time.  At
+// the end of a Q4_0 row group it may hold fewer (whole units of two blocks).
+constexpr int kStageCodes = 2048;
+constexpr int kStageBytes = 2304;   // codes, then scales
+constexpr int kDepth = 3;           // stages of a warp's ring
+constexpr size_t kRingBytes = static_cast<size_t>(kWarps) * kDepth * kStageBytes;
 
 struct MoeArgs {
   const uint8_t* w0;        // gate, or down
@@ -84,47 +78,35 @@ struct MoeArgs {
   int tabslots;             // parts that one table holds
   int tabfloats;            // floats of one table
   int64_t group_bytes;
-  uint32_t b_off, corr_off, tab_off;  // dynamic shared memory
+  uint32_t b_off, tab_off, plan_off;  // dynamic shared memory, after the rings
 };
 
 struct Seg {
-  int e, slot0, n;
+  short e, slot0;
+  int n;
 };
 
 struct Plan {
-  int nseg, npairs;
-  int cnt[kMaxE];           // pairs of an expert, then its first slot
-  short rank[kMaxPairs];
-  short order[kMaxPairs];   // slot -> pair
-  Seg seg[kMaxPairs];
-  float inv[2][kMaxCols];   // 2^24 / scale of a segment's tokens
+  int nseg;
+  float inv[2][kMaxCols];   // 1 / scale of a segment's tokens
   unsigned amax[2][kMaxCols];
+  // in dynamic shared memory
+  Seg* seg;                 // [pairs]
+  short* order;             // [pairs] slot -> pair
+  short* first;             // [E] pairs of an expert, then its first slot
+  short* rank;              // [pairs] only while planning (in the rings' place)
 };
 
 extern __shared__ __align__(1024) uint8_t msm[];
 
-__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// 16 bytes, global to shared, past L1.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void ldg_stream8(const uint8_t* p, uint32_t* w) {  // 32-byte aligned
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
-                 "=r"(w[7])
-               : "l"(p));
-}
-__device__ __forceinline__ uint32_t ldg_word(const uint8_t* p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint32_t ldg_half(const uint8_t* p) {
-  unsigned short v;
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
-  return v;
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the newest N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // ------------------------------------------------------------------- plan
@@ -133,7 +115,7 @@ __device__ __forceinline__ uint32_t ldg_half(const uint8_t* p) {
 __device__ void make_plan(Plan& pl, const MoeArgs& a) {
   const int P = a.T * a.k;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) pl.cnt[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += kThreads) pl.first[e] = 0;
   __syncthreads();
   if (warp == 0) {
     // rank of each pair among its expert's, 32 pairs at a time
@@ -144,9 +126,9 @@ __device__ void make_plan(Plan& pl, const MoeArgs& a) {
       if (blockIdx.x == 0 && (id < -1 || id >= a.E)) report(a.dev_status, GQ_DEV_RANGE);
       const unsigned peers = __match_any_sync(0xFFFFFFFFu, ok ? id : -1 - lane);
       const int before = __popc(peers & ((1u << lane) - 1u));
-      const int base = ok ? pl.cnt[id] : 0;
+      const int base = ok ? pl.first[id] : 0;
       __syncwarp();
-      if (ok && before == 0) pl.cnt[id] = base + __popc(peers);
+      if (ok && before == 0) pl.first[id] = static_cast<short>(base + __popc(peers));
       if (p < P) pl.rank[p] = static_cast<short>(ok ? base + before : -1);
       __syncwarp();
     }
@@ -154,7 +136,7 @@ __device__ void make_plan(Plan& pl, const MoeArgs& a) {
     int slots = 0, segs = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
-      const int n = e < a.E ? pl.cnt[e] : 0;
+      const int n = e < a.E ? pl.first[e] : 0;
       const int ns = (n + a.cap - 1) / a.cap;
       int sn = n, ss = ns;  // inclusive sums over the lanes
 #pragma unroll
@@ -166,21 +148,18 @@ __device__ void make_plan(Plan& pl, const MoeArgs& a) {
         }
       }
       const int first = slots + sn - n, sfirst = segs + ss - ns;
-      if (e < a.E) pl.cnt[e] = first;
+      if (e < a.E) pl.first[e] = static_cast<short>(first);
       for (int i = 0; i < ns; ++i)
-        pl.seg[sfirst + i] = Seg{e, first + i * a.cap, min(a.cap, n - i * a.cap)};
+        pl.seg[sfirst + i] = Seg{static_cast<short>(e), static_cast<short>(first + i * a.cap), min(a.cap, n - i * a.cap)};
       slots += __shfl_sync(0xFFFFFFFFu, sn, 31);
       segs += __shfl_sync(0xFFFFFFFFu, ss, 31);
     }
-    if (lane == 0) {
-      pl.nseg = segs;
-      pl.npairs = slots;
-    }
+    if (lane == 0) pl.nseg = segs;
   }
   __syncthreads();
   for (int p = threadIdx.x; p < P; p += kThreads) {
     const int r = pl.rank[p];
-    if (r >= 0) pl.order[pl.cnt[__ldcg(a.ids + p)] + r] = static_cast<short>(p);
+    if (r >= 0) pl.order[pl.first[__ldcg(a.ids + p)] + r] = static_cast<short>(p);
   }
   __syncthreads();
 }
@@ -216,9 +195,9 @@ __device__ __forceinline__ float scale_of(unsigned maxbits) {
   return __uint_as_float(static_cast<unsigned>(127 + 14 - max(e, -100)) << 23);
 }
 
-// B fragments and block corrections of a segment's tokens.  Column c of block
-// b and lane group t: 16 bytes at ((b * ncol + c) * 4 + t) * 16, the values
-// 4t, 4t+2, 4t+1, 4t+3 of the block and the same at +16 (these / 16).
+// B fragments of a segment's tokens.  Column c of block b and lane group t: 16
+// bytes at ((b * ncol + c) * 4 + t) * 16, the values 4t, 4t+2, 4t+1, 4t+3 of the
+// block and the same at +16.
 template <bool GATE_UP>
 __device__ void load_b(const MoeArgs& a, Plan& pl, const Seg& sg, int buf) {
   const int ncol = a.two ? 2 * sg.n : sg.n;
@@ -247,31 +226,23 @@ __device__ void load_b(const MoeArgs& a, Plan& pl, const Seg& sg, int buf) {
   }
   if (threadIdx.x < sg.n)  // scale_of() is a power of two: the reciprocal is exact
     pl.inv[buf][threadIdx.x] = 1.0f / scale_of(pl.amax[buf][threadIdx.x]);
-  float* corr = reinterpret_cast<float*>(msm + a.corr_off);
-  const int ncp = (ncol + 1) & ~1;
-  const int nvec = sg.n * vecs;  // a multiple of 8: whole blocks
-  for (int i0 = 0; i0 < nvec; i0 += kThreads) {  // every thread takes part in the shuffles
-    const int i = i0 + threadIdx.x;
-    const bool in = i < nvec;
-    const int c = in ? i / vecs : 0, r = in ? i - c * vecs : 0;
-    const int b = r >> 2, q = threadIdx.x & 3;
-    const float s = scale_of(pl.amax[buf][c]) * (q >= 2 ? 0.0625f : 1.0f);
+  const int nvec = sg.n * vecs;
+  for (int i = threadIdx.x; i < nvec; i += kThreads) {
+    const int c = i / vecs, r = i - c * vecs;
+    const int b = r >> 2, q = r & 3;
+    const float s = scale_of(pl.amax[buf][c]);
     float v[8];
     load8(a.x, row_of(c) + 8 * r, a.xtype, v);
     const int col = a.two ? 2 * c : c;
     const int t0 = 2 * (q & 1);
-    float sum[2] = {0.f, 0.f};
     for (int part = 0; part <= a.two; ++part) {
       __half hv[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float f = part ? v[j] : v[j] * s;  // the second pass holds remainders
         hv[j] = __float2half_rn(f);
-        const float g = __half2float(hv[j]);
-        v[j] = f - g;
-        sum[part] += g;
+        v[j] = f - __half2float(hv[j]);
       }
-      if (!in) continue;
       uint8_t* d = msm + a.b_off + (static_cast<uint32_t>(b * ncol + col + part) * 4 + t0) * 16 + (q >> 1) * 8;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -281,44 +252,40 @@ __device__ void load_b(const MoeArgs& a, Plan& pl, const Seg& sg, int buf) {
                                                            *reinterpret_cast<const uint32_t*>(&hi));
       }
     }
-    // block sums: the four lanes of a block (a warp holds whole blocks)
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      float f = q >= 2 ? 16.0f * sum[part] : sum[part];
-      f += __shfl_xor_sync(0xFFFFFFFFu, f, 1);
-      f += __shfl_xor_sync(0xFFFFFFFFu, f, 2);
-      if (in && q == 0 && part <= a.two) corr[b * ncp + col + part] = f * -4.76837158203125e-07f;  // -8 * 2^-24
-    }
   }
   __syncthreads();
 }
 
-// ------------------------------------------------------------------- units
-// The words that this lane needs of one unit, from its row group's bytes.
+// ------------------------------------------------------------------ stages
+// Copy stage k of a row group into the ring slot at shared address dst.
 template <int FMT>
-__device__ __forceinline__ void load_unit(const uint8_t* group, int u, int units, int lane, uint32_t* w) {
-  using F = Unit<FMT>;
-  const int c = u / F::kTileUnits, i = u - c * F::kTileUnits;
-  const int nu = min(F::kTileUnits, units - c * F::kTileUnits);  // units of the tile
-  const uint8_t* tile = group + static_cast<int64_t>(c) * F::kTileBytes;
-  const int g8 = lane >> 2;
+__device__ __forceinline__ void copy_stage(uint32_t dst, const uint8_t* group, int k, int K, int lane) {
   if constexpr (FMT == GQ_FMT_Q4_0) {
-    const uint4 v = ldg_stream(tile + 512 * i + 16 * lane);
-    const uint8_t* sc = tile + 512 * nu + 64 * i + 4 * g8;
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    w[4] = ldg_word(sc);
-    w[5] = ldg_word(sc + 32);
+    // tiles of 32 units (512 bytes of codes, 64 of scales); a stage is four
+    const int c = k >> 3, j = k & 7;
+    const int nu = min(32, (K >> 6) - 32 * c), n = min(4, nu - 4 * j);
+    const uint8_t* tile = group + static_cast<int64_t>(c) * 18432;
+    const uint8_t* src = tile + 2048 * j + 16 * lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) copy16(dst + 512 * i + 16 * lane, src + 512 * i);
+    if (lane < 4 * n) copy16(dst + kStageCodes + 16 * lane, tile + 512 * nu + 256 * j + 16 * lane);
   } else {
-    ldg_stream8(tile + 1024 * i + 32 * lane, w);
-    const uint8_t* sc = tile + 1024 * nu + 64 * i + 4 * g8;
-    const uint8_t* ss = tile + 1088 * nu + 32 * (i >> 1) + 2 * g8;
-    w[8] = ldg_word(sc);
-    w[9] = ldg_word(sc + 32);
-    w[10] = ldg_half(ss);
-    w[11] = ldg_half(ss + 16);
+    // tiles of 8 super-blocks (2048 bytes of codes, 128 of sub-scales, 32 of S); a stage is one
+    const int c = k >> 3, j = k & 7;
+    const int ns = min(8, (K >> 8) - 8 * c);
+    const uint8_t* tile = group + static_cast<int64_t>(c) * 17664;
+    const uint8_t* src = tile + 2048 * j + 16 * lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) copy16(dst + 512 * i + 16 * lane, src + 512 * i);
+    if (lane < 10)
+      copy16(dst + kStageCodes + 16 * lane, lane < 8 ? tile + 2048 * ns + 128 * j + 16 * lane
+                                                     : tile + 2176 * ns + 32 * j + 16 * (lane - 8));
   }
 }
 
+__device__ __forceinline__ uint32_t ld32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+__device__ __forceinline__ uint4 ld128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ float2 halves(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
@@ -327,41 +294,70 @@ __device__ __forceinline__ float flipped_byte(uint32_t q, int h) {
   return __uint_as_float(__byte_perm(q, 0x4B000000u, 0x7540u + h)) - 8388736.0f;  // 2^23 + 128
 }
 
-// acc += the unit's products for NT column tiles.  xb, cb: this lane's
-// B fragment and correction of column tile 0 in the unit's first block.
-template <int FMT, int NT>
-__device__ __forceinline__ void unit_math(const uint32_t* w, float acc[NT][4], const uint8_t* xb,
-                                          uint32_t xpitch, uint32_t xtile, const float* cb, int cpitch,
-                                          int ctile) {
-  using F = Unit<FMT>;
-  float da[F::kBlocks], db[F::kBlocks];  // scales of rows g and g+8
-  if constexpr (FMT == GQ_FMT_Q4_0) {
-    const float2 p = halves(w[4]), q = halves(w[5]);
-    da[0] = p.x, da[1] = p.y, db[0] = q.x, db[1] = q.y;
-  } else {
-    const float sa = halves(w[10]).x, sb = halves(w[11]).x;
-    const uint32_t qa = w[8] ^ 0x80808080u, qb = w[9] ^ 0x80808080u;
+// Two codes of a word as fp16 values code - 8: the low nibbles of bytes 0 and 2,
+// or their high nibbles.
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
+  const uint32_t u = lop3_and_or(w, 0x000F000Fu, 0x64006400u);  // 1024 + code
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6408)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
+  const uint32_t u = lop3_and_or(w, 0x00F000F0u, 0x64006400u);  // 1024 + 16 code
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x2C00)),
+                            __half2half2(__ushort_as_half(0xD480)));  // / 16 - 72
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// acc += one block of 32 weights: wa, wb this lane's code words of rows g and
+// g+8, da, db the rows' scales, xb this lane's B fragment of column tile 0.
+template <int NT>
+__device__ __forceinline__ void block_math(uint32_t wa, uint32_t wb, float da, float db, float acc[NT][4],
+                                           const uint8_t* xb, uint32_t xtile) {
+  const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
+  const uint32_t l0 = low_codes(wa), l1 = low_codes(wb), l2 = low_codes(wa8), l3 = low_codes(wb8);
+  const uint32_t h0 = high_codes(wa), h1 = high_codes(wb), h2 = high_codes(wa8), h3 = high_codes(wb8);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      da[h] = sa * flipped_byte(qa, h);
-      db[h] = sb * flipped_byte(qb, h);
-    }
+  for (int j = 0; j < NT; ++j) {
+    const uint4 xv = ld128(xb + j * xtile);
+    float c[4];
+    mma_f16_z(c, l0, l1, l2, l3, xv.x, xv.y);
+    mma_f16(c, h0, h1, h2, h3, xv.z, xv.w);
+    acc[j][0] = fmaf(da, c[0], acc[j][0]);
+    acc[j][1] = fmaf(da, c[1], acc[j][1]);
+    acc[j][2] = fmaf(db, c[2], acc[j][2]);
+    acc[j][3] = fmaf(db, c[3], acc[j][3]);
   }
+}
+
+// A stage of n units of two blocks (Q4_0) or of one super-block from its ring slot.
+template <int FMT, int NT>
+__device__ __forceinline__ void stage_math(const uint8_t* st, int n, int lane, float acc[NT][4],
+                                           const uint8_t* xb, uint32_t xpitch, uint32_t xtile) {
+  const int g8 = lane >> 2;
+  if constexpr (FMT == GQ_FMT_Q4_0) {
 #pragma unroll
-  for (int b = 0; b < F::kBlocks; ++b) {
-    const uint32_t wa = w[2 * b], wb = w[2 * b + 1];
-    const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
+    for (int i = 0; i < 4; ++i) {
+      if (i < n) {
+        const uint4 v = ld128(st + 512 * i + 16 * lane);
+        const float2 da = halves(ld32(st + kStageCodes + 64 * i + 4 * g8));
+        const float2 db = halves(ld32(st + kStageCodes + 64 * i + 32 + 4 * g8));
+        block_math<NT>(v.x, v.y, da.x, db.x, acc, xb + (2 * i) * xpitch, xtile);
+        block_math<NT>(v.z, v.w, da.y, db.y, acc, xb + (2 * i + 1) * xpitch, xtile);
+      }
+    }
+  } else {
+    const float sa = __half2float(*reinterpret_cast<const __half*>(st + kStageCodes + 128 + 2 * g8));
+    const float sb = __half2float(*reinterpret_cast<const __half*>(st + kStageCodes + 144 + 2 * g8));
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const uint4 xv = *reinterpret_cast<const uint4*>(xb + b * xpitch + j * xtile);
-      const float2 cr = *reinterpret_cast<const float2*>(cb + b * cpitch + j * ctile);
-      float c[4] = {cr.x, cr.y, cr.x, cr.y};
-      mma_f16(c, wa & 0x000F000Fu, wb & 0x000F000Fu, wa8 & 0x000F000Fu, wb8 & 0x000F000Fu, xv.x, xv.y);
-      mma_f16(c, wa & 0x00F000F0u, wb & 0x00F000F0u, wa8 & 0x00F000F0u, wb8 & 0x00F000F0u, xv.z, xv.w);
-      acc[j][0] = fmaf(da[b], c[0], acc[j][0]);
-      acc[j][1] = fmaf(da[b], c[1], acc[j][1]);
-      acc[j][2] = fmaf(db[b], c[2], acc[j][2]);
-      acc[j][3] = fmaf(db[b], c[3], acc[j][3]);
+    for (int i = 0; i < 2; ++i) {  // half a super-block: lane-ordered 32 bytes of codes
+      const uint32_t qa = ld32(st + kStageCodes + 64 * i + 4 * g8) ^ 0x80808080u;
+      const uint32_t qb = ld32(st + kStageCodes + 64 * i + 32 + 4 * g8) ^ 0x80808080u;
+      const uint4 v = ld128(st + 1024 * i + 32 * lane), w = ld128(st + 1024 * i + 32 * lane + 16);
+      const uint8_t* x = xb + (4 * i) * xpitch;
+      block_math<NT>(v.x, v.y, sa * flipped_byte(qa, 0), sb * flipped_byte(qb, 0), acc, x, xtile);
+      block_math<NT>(v.z, v.w, sa * flipped_byte(qa, 1), sb * flipped_byte(qb, 1), acc, x + xpitch, xtile);
+      block_math<NT>(w.x, w.y, sa * flipped_byte(qa, 2), sb * flipped_byte(qb, 2), acc, x + 2 * xpitch, xtile);
+      block_math<NT>(w.z, w.w, sa * flipped_byte(qa, 3), sb * flipped_byte(qb, 3), acc, x + 3 * xpitch, xtile);
     }
   }
 }
@@ -375,63 +371,66 @@ __device__ __forceinline__ const uint8_t* group_at(const MoeArgs& a, int e, int 
   return w + (static_cast<int64_t>(e) * a.groups + g) * a.group_bytes;
 }
 
-// This warp's units [u, u1) of the string, `w` holding the first kAhead of
-// them: partial sums to the table, part (row group + warp) for each row group
-// that the warp has units of.
+// A warp's next copy: stage k of row group q of the string, `left` stages in all.
+template <bool GATE_UP>
+struct Feed {
+  const uint8_t* group;
+  int e, q, k, left;
+  template <int FMT>
+  __device__ __forceinline__ void step(const MoeArgs& a, int i0, int stages, uint32_t dst, int lane) {
+    if (left > 0) {
+      copy_stage<FMT>(dst, group, k, a.K, lane);
+      --left;
+      if (++k == stages) {
+        k = 0;
+        ++q;
+        if (left > 0) group = group_at<GATE_UP>(a, e, i0 + q);
+      }
+    }
+    copies_commit();  // also an empty group: groups count stages
+  }
+};
+
+// This warp's stages [u, u1) of the string, the first kDepth of them under way:
+// partial sums to the table, part (row group + warp) for each row group that
+// the warp has stages of.
 template <int FMT, int NT, bool GATE_UP>
-__device__ __forceinline__ void stream(const MoeArgs& a, int e, int i0, int units, int u, int u1,
-                                       int ncol, uint32_t (*w)[Unit<FMT>::kWords], float* tab) {
-  using F = Unit<FMT>;
+__device__ __forceinline__ void stream(const MoeArgs& a, Feed<GATE_UP>& feed, int i0, int stages, int u,
+                                       int u1, int ncol, uint32_t ring, float* tab) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
   const int ncp = (ncol + 1) & ~1;
-  // columns past the last read an existing one; their sums are not stored
+  // columns past the last read an existing one; their sums are not used
   const uint32_t xlane = static_cast<uint32_t>(min(g8, ncol - 1) * 64 + t * 16);
   const uint32_t xtile = NT > 1 ? static_cast<uint32_t>(min(8 + g8, ncol - 1) * 64 + t * 16) - xlane : 0u;
-  const int clane = min(2 * t, ncp - 2);
-  const int ctile = NT > 1 ? min(8 + 2 * t, ncp - 2) - clane : 0;
   const uint32_t xpitch = static_cast<uint32_t>(ncol) * 64;
-  const float* corr = reinterpret_cast<const float*>(msm + a.corr_off);
+  const uint8_t* xb = msm + a.b_off + xlane;
+  const uint32_t sbase = smem_addr(msm);
   float acc[NT][4];
 #pragma unroll
   for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-  int q = u / units, k = u - q * units;               // row group of the string, unit in it
-  int pq = (u + F::kAhead) / units, pk = u + F::kAhead - pq * units;  // the same, kAhead on
-  const uint8_t* pg = u + F::kAhead < u1 ? group_at<GATE_UP>(a, e, i0 + pq) : nullptr;
-  auto flush = [&]() {
-    float* d = tab + static_cast<int64_t>(q + warp) * 16 * ncp;
+  int q = u / stages, k = u - q * stages, slot = 0;
+  for (; u < u1; ++u) {
+    copies_wait<kDepth - 1>();
+    __syncwarp();  // every lane's copies of the stage
+    const uint32_t st = ring + slot * kStageBytes;
+    const int n = FMT == GQ_FMT_Q4_0 ? min(4, (a.K >> 6) - 4 * k) : 4;
+    stage_math<FMT, NT>(msm + st, n, lane, acc, xb + static_cast<uint32_t>(8 * k) * xpitch, xpitch, xtile);
+    __syncwarp();  // every lane has read the stage
+    feed.template step<FMT>(a, i0, stages, sbase + st, lane);
+    if (++slot == kDepth) slot = 0;
+    if (++k == stages || u + 1 == u1) {
+      float* d = tab + (q + warp) * 16 * ncp;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int c = 8 * j + 2 * t;
-      if (c < ncp) {
-        *reinterpret_cast<float2*>(d + g8 * ncp + c) = make_float2(acc[j][0], acc[j][1]);
-        *reinterpret_cast<float2*>(d + (g8 + 8) * ncp + c) = make_float2(acc[j][2], acc[j][3]);
-      }
-      acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-    }
-  };
-  while (u < u1) {
-#pragma unroll
-    for (int s = 0; s < F::kAhead; ++s) {
-      if (u < u1) {
-        unit_math<FMT, NT>(w[s], acc, msm + a.b_off + static_cast<uint32_t>(k * F::kBlocks) * xpitch + xlane,
-                           xpitch, xtile, corr + k * F::kBlocks * ncp + clane, ncp, ctile);
-        ++u;
-        if (++k == units || u == u1) {
-          flush();
-          if (k == units) {
-            k = 0;
-            ++q;
-          }
+      for (int j = 0; j < NT; ++j) {
+        const int c = 8 * j + 2 * t;
+        if (c < ncp) {
+          *reinterpret_cast<float2*>(d + g8 * ncp + c) = make_float2(acc[j][0], acc[j][1]);
+          *reinterpret_cast<float2*>(d + (g8 + 8) * ncp + c) = make_float2(acc[j][2], acc[j][3]);
         }
-        if (u + F::kAhead - 1 < u1) {
-          load_unit<FMT>(pg, pk, units, lane, w[s]);
-          if (++pk == units) {
-            pk = 0;
-            ++pq;
-            if (u + F::kAhead < u1) pg = group_at<GATE_UP>(a, e, i0 + pq);
-          }
-        }
+        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
       }
+      k = 0;
+      ++q;
     }
   }
 }
@@ -461,33 +460,40 @@ struct Cursor {
 
 template <int FMT, bool GATE_UP>
 __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs a) {
-  using F = Unit<FMT>;
   __shared__ Plan pl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    pl.seg = reinterpret_cast<Seg*>(msm + a.plan_off);
+    pl.order = reinterpret_cast<short*>(pl.seg + a.T * a.k);
+    pl.first = pl.order + a.T * a.k;
+    pl.rank = reinterpret_cast<short*>(msm);
+  }
   if (GATE_UP) pdl_wait();  // ids and x are final (the down launch starts after that)
   pdl_launch_dependents();
+  __syncthreads();
   make_plan(pl, a);
-  const int units = a.K / (32 * F::kBlocks);
+  const int stages = FMT == GQ_FMT_Q4_0 ? (a.K + 255) / 256 : a.K / 256;  // of a row group
   const int64_t total = static_cast<int64_t>(pl.nseg) * a.groups;
   Cursor<GATE_UP> cur{total * blockIdx.x / gridDim.x, total * (blockIdx.x + 1) / gridDim.x, a.groups,
                       (a.tabslots - kWarps) / (GATE_UP ? 2 : 1)};
   String st;
   bool more = cur.next(st);
-  uint32_t w[F::kAhead][F::kWords];
-  // the first units of this warp's share of a string
-  auto fetch = [&](const String& s, int e) {
-    const int tu = s.n * units;
-    const int u0 = tu * warp / kWarps, u1 = tu * (warp + 1) / kWarps;
+  const uint32_t ring = static_cast<uint32_t>(warp * kDepth * kStageBytes);
+  Feed<GATE_UP> feed;
+  // the first stages of this warp's share of a string
+  auto fetch = [&](const String& s) {
+    const int tu = s.n * stages;
+    const int u0 = tu * warp / kWarps;
+    feed.e = pl.seg[s.seg].e;
+    feed.q = u0 / stages;
+    feed.k = u0 - feed.q * stages;
+    feed.left = tu * (warp + 1) / kWarps - u0;
+    feed.group = group_at<GATE_UP>(a, feed.e, s.i0 + min(feed.q, s.n - 1));
 #pragma unroll
-    for (int i = 0; i < F::kAhead; ++i) {
-      const int u = u0 + i;
-      if (u < u1) {
-        const int q = u / units;
-        load_unit<FMT>(group_at<GATE_UP>(a, e, s.i0 + q), u - q * units, units, lane, w[i]);
-      }
-    }
+    for (int i = 0; i < kDepth; ++i)
+      feed.template step<FMT>(a, s.i0, stages, smem_addr(msm) + ring + i * kStageBytes, lane);
   };
-  if (more) fetch(st, pl.seg[st.seg].e);
+  if (more) fetch(st);
   if (!GATE_UP) pdl_wait();  // h and the slots' largest values are final
   int buf = 0, loaded = -1;
   while (more) {
@@ -498,23 +504,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs a) {
       loaded = st.seg;
     }
     float* tab = reinterpret_cast<float*>(msm + a.tab_off) + buf * a.tabfloats;
-    const int tu = st.n * units;
+    const int tu = st.n * stages;
     const int u0 = tu * warp / kWarps, u1 = tu * (warp + 1) / kWarps;
     if (ncol <= 8)
-      stream<FMT, 1, GATE_UP>(a, sg.e, st.i0, units, u0, u1, ncol, w, tab);
+      stream<FMT, 1, GATE_UP>(a, feed, st.i0, stages, u0, u1, ncol, ring, tab);
     else
-      stream<FMT, 2, GATE_UP>(a, sg.e, st.i0, units, u0, u1, ncol, w, tab);
+      stream<FMT, 2, GATE_UP>(a, feed, st.i0, stages, u0, u1, ncol, ring, tab);
     const String done = st;
     more = cur.next(st);
-    if (more) fetch(st, pl.seg[st.seg].e);
+    if (more) fetch(st);
     __syncthreads();  // the table is complete; B and the other table are free
     // sums of the row groups, in warp order
     auto sum = [&](int q, int row, int c) {
-      const int first = q * units, last = first + units - 1;
+      const int first = q * stages, last = first + stages - 1;
       const int w0 = (16 * (first + 1) - 1) / tu, w1 = (16 * (last + 1) - 1) / tu;
       float v = 0.f;
       for (int ww = w0; ww <= w1; ++ww) {
-        if (tu * ww / kWarps == tu * (ww + 1) / kWarps) continue;  // no units
+        if (tu * ww / kWarps == tu * (ww + 1) / kWarps) continue;  // no stages
         const float* p = tab + (static_cast<int64_t>(q + ww) * 16 + row) * ncp + c;
         v += a.two ? p[0] + p[1] : p[0];
       }
@@ -527,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs a) {
         const int row = i & 15, rest = i >> 4;
         const int c = rest % sg.n, p = rest / sg.n;
         const int col = a.two ? 2 * c : c;
-        const float g = sum(2 * p, row, col) * 16777216.0f * inv[c];
-        const float up = sum(2 * p + 1, row, col) * 16777216.0f * inv[c];
+        const float g = sum(2 * p, row, col) * inv[c];
+        const float up = sum(2 * p + 1, row, col) * inv[c];
         const float h = g / (1.0f + expf(-g)) * up;
         const int slot = sg.slot0 + c;
         a.h[static_cast<int64_t>(slot) * (a.groups * 16) + (done.i0 / 2 + p) * 16 + row] = h;
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs a) {
       for (int i = threadIdx.x; i < cells; i += kThreads) {
         const int row = i & 15, rest = i >> 4;
         const int c = rest % sg.n, q = rest / sg.n;
-        const float v = sum(q, row, a.two ? 2 * c : c) * 16777216.0f * inv[c];
+        const float v = sum(q, row, a.two ? 2 * c : c) * inv[c];
         const int pair = pl.order[sg.slot0 + c];
         a.out[static_cast<int64_t>(pair) * (a.groups * 16) + (done.i0 + q) * 16 + row] = v;
       }
@@ -593,23 +599,30 @@ bool moe_dims(int64_t T, int64_t k, int64_t E) {
 }
 bool moe_width(int fmt, int64_t K) { return K % (fmt == GQ_FMT_Q4_0 ? 64 : 256) == 0 && K <= kMaxK; }
 
-// Tokens of a segment and the layout of shared memory: the B fragments and
-// corrections take 2 + 1/8 bytes for each value of a column; the two tables
-// take what a string of 16 parts beyond the warps' needs.
-constexpr int kTabSlots = kWarps + 32;
+// Tokens of a segment and the layout of shared memory after the rings: the
+// plan, the B fragments (2 bytes for each value of a column), and two tables of
+// parts.  A table holds at least a string of 16 row groups.
+constexpr int kMinSlots = kWarps + 16, kMaxSlots = kWarps + 64;
+static_assert(sizeof(Plan) <= 1024, "the static part, up to the dynamic one's alignment");
+constexpr size_t kDynSmem = kSmemBudget - 1024;
 size_t shape_smem(MoeArgs& a) {
-  const size_t left = kSmemBudget - sizeof(Plan) - 2048;
-  const size_t colbytes = static_cast<size_t>(a.K) * 2 + static_cast<size_t>(a.K) / 32 * 4 + 2 * kTabSlots * 16 * 4;
-  int cols = static_cast<int>(left / colbytes < kMaxCols ? left / colbytes : kMaxCols) & ~1;
-  const int pairs = a.T * a.k * (a.two ? 2 : 1);
-  if (cols > pairs) cols = (pairs + 1) & ~1;
+  const int pairs = a.T * a.k;
+  const size_t plan = (static_cast<size_t>(pairs) * (sizeof(Seg) + 2) + static_cast<size_t>(a.E) * 2 + 15) & ~size_t(15);
+  const size_t left = kDynSmem - kRingBytes - plan;
+  const size_t part = 2 * 16 * sizeof(float);  // of both tables, for each column
+  const size_t most = left / (static_cast<size_t>(a.K) * 2 + kMinSlots * part);
+  int cols = static_cast<int>(most < kMaxCols ? most : kMaxCols) & ~1;
+  const int need = pairs * (a.two ? 2 : 1);
+  if (cols > need) cols = (need + 1) & ~1;
+  const size_t b = static_cast<size_t>(cols) * a.K * 2;
+  const size_t slots = (left - b) / (part * cols);
   a.cap = a.two ? cols / 2 : cols;
-  a.tabslots = kTabSlots;
-  a.tabfloats = kTabSlots * 16 * cols;
-  a.tab_off = 0;
-  a.b_off = 2 * a.tabfloats * 4;
-  a.corr_off = a.b_off + static_cast<uint32_t>(cols) * a.K * 2;
-  return a.corr_off + static_cast<size_t>(cols) * a.K / 32 * 4;
+  a.tabslots = static_cast<int>(slots < kMaxSlots ? slots : kMaxSlots);
+  a.tabfloats = a.tabslots * 16 * cols;
+  a.b_off = kRingBytes;
+  a.tab_off = a.b_off + static_cast<uint32_t>(b);
+  a.plan_off = a.tab_off + 2 * a.tabfloats * 4;
+  return a.plan_off + plan;
 }
 
 template <int FMT, bool GATE_UP>
@@ -619,7 +632,7 @@ gq_status launch_moe(MoeArgs& a, bool pdl, cudaStream_t s) {
   const unsigned long long ctx = context_id();
   if (ctx == 0 || ctx != configured_ctx) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSmemBudget - sizeof(Plan) - 1024)) != cudaSuccess)
+                             static_cast<int>(kDynSmem)) != cudaSuccess)
       return GQ_ERR_CUDA;
     configured_ctx = ctx;
   }
@@ -648,10 +661,6 @@ gq_status moe_entry(const void* gate, const void* up, const void* down, int64_t 
   if (!gate || !up || !down || !x || !ids || !weights) return GQ_ERR_INVALID_ARG;
   if (misaligned16(gate) || misaligned16(up) || misaligned16(down) || misaligned16(x) ||
       misaligned16(ids) || misaligned16(weights))
-    return GQ_ERR_ALIGNMENT;
-  // super-block units are read 32 bytes a lane
-  if (FMT == GQ_FMT_KSB && ((reinterpret_cast<uintptr_t>(gate) | reinterpret_cast<uintptr_t>(up) |
-                             reinterpret_cast<uintptr_t>(down)) & 31u))
     return GQ_ERR_ALIGNMENT;
   const Ws l = ws_layout(T, k, H, I);
   if (!workspace || ws_bytes < l.total) return GQ_ERR_WORKSPACE;

@@ -410,7 +410,6 @@ GQ_API gq_status gq_moe_route(const void* x, int x_dtype, int64_t T, int64_t H, 
  *   gate, up: tiled storage of the E experts' I x H matrices one after another,
  *      i.e. of one (E * I) x H matrix (gq_repack_*); down: of E matrices H x I.
  *      H and I are multiples of 64 (Q4_0) or 256 (KSB), at most 16384; E <= 1024.
- *      32-byte aligned for KSB.
  *   x: [T][H] of x_dtype; T <= 64, k <= 16; y: [T][H] of y_dtype.
  *   ids: [T][k] int32 (as gq_moe_route writes them).  -1 names no expert; any
  *      other value outside [0, E) counts as -1 and sets GQ_DEV_RANGE.  A token

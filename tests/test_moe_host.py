@@ -58,8 +58,6 @@ def test_layer_refusals(name, fmt, step):
     for n in ("g", "u", "d", "x", "ids", "w", "y"):
         assert call(**{n: None}) == INVALID
         assert call(**{n: A + 4}) == ALIGN
-    if fmt == 1:
-        assert call(d=A + 16) == ALIGN                   # read 32 bytes at a time
     assert call(st=A + 1) == ALIGN
     need = gq.gq_moe_workspace_bytes(fmt, 2 * step, step, 3, 2)
     assert need > 0
