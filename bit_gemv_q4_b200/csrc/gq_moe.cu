@@ -195,12 +195,18 @@ __device__ __forceinline__ float scale_of(unsigned maxbits) {
   return __uint_as_float(static_cast<unsigned>(127 + 14 - max(e, -100)) << 23);
 }
 
+// Columns that the B fragments of a segment have room for: a power of two, so
+// that every offset in the inner loop is a constant.
+__device__ __forceinline__ int col_pitch(int ncol) {
+  return ncol <= 2 ? ncol : ncol <= 4 ? 4 : ncol <= 8 ? 8 : 16;
+}
+
 // B fragments of a segment's tokens.  Column c of block b and lane group t: 16
-// bytes at ((b * ncol + c) * 4 + t) * 16, the values 4t, 4t+2, 4t+1, 4t+3 of the
+// bytes at ((b * pitch + c) * 4 + t) * 16, the values 4t, 4t+2, 4t+1, 4t+3 of the
 // block and the same at +16.
 template <bool GATE_UP>
 __device__ void load_b(const MoeArgs& a, Plan& pl, const Seg& sg, int buf) {
-  const int ncol = a.two ? 2 * sg.n : sg.n;
+  const int pitch = col_pitch(a.two ? 2 * sg.n : sg.n);
   const int vecs = a.K / 8;
   auto row_of = [&](int c) -> int64_t {
     return GATE_UP ? static_cast<int64_t>(pl.order[sg.slot0 + c] / a.k) * a.K
@@ -243,7 +249,7 @@ __device__ void load_b(const MoeArgs& a, Plan& pl, const Seg& sg, int buf) {
         hv[j] = __float2half_rn(f);
         v[j] = f - __half2float(hv[j]);
       }
-      uint8_t* d = msm + a.b_off + (static_cast<uint32_t>(b * ncol + col + part) * 4 + t0) * 16 + (q >> 1) * 8;
+      uint8_t* d = msm + a.b_off + (static_cast<uint32_t>(b * pitch + col + part) * 4 + t0) * 16 + (q >> 1) * 8;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const __half2 lo = __halves2half2(hv[4 * u], hv[4 * u + 2]);
@@ -257,33 +263,6 @@ __device__ void load_b(const MoeArgs& a, Plan& pl, const Seg& sg, int buf) {
 }
 
 // ------------------------------------------------------------------ stages
-// Copy stage k of a row group into the ring slot at shared address dst.
-template <int FMT>
-__device__ __forceinline__ void copy_stage(uint32_t dst, const uint8_t* group, int k, int K, int lane) {
-  if constexpr (FMT == GQ_FMT_Q4_0) {
-    // tiles of 32 units (512 bytes of codes, 64 of scales); a stage is four
-    const int c = k >> 3, j = k & 7;
-    const int nu = min(32, (K >> 6) - 32 * c), n = min(4, nu - 4 * j);
-    const uint8_t* tile = group + static_cast<int64_t>(c) * 18432;
-    const uint8_t* src = tile + 2048 * j + 16 * lane;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) copy16(dst + 512 * i + 16 * lane, src + 512 * i);
-    if (lane < 4 * n) copy16(dst + kStageCodes + 16 * lane, tile + 512 * nu + 256 * j + 16 * lane);
-  } else {
-    // tiles of 8 super-blocks (2048 bytes of codes, 128 of sub-scales, 32 of S); a stage is one
-    const int c = k >> 3, j = k & 7;
-    const int ns = min(8, (K >> 8) - 8 * c);
-    const uint8_t* tile = group + static_cast<int64_t>(c) * 17664;
-    const uint8_t* src = tile + 2048 * j + 16 * lane;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) copy16(dst + 512 * i + 16 * lane, src + 512 * i);
-    if (lane < 10)
-      copy16(dst + kStageCodes + 16 * lane, lane < 8 ? tile + 2048 * ns + 128 * j + 16 * lane
-                                                     : tile + 2176 * ns + 32 * j + 16 * (lane - 8));
-  }
-}
-
 __device__ __forceinline__ uint32_t ld32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
 __device__ __forceinline__ uint4 ld128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ float2 halves(uint32_t v) {
@@ -310,54 +289,56 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t w) {
 
 // acc += one block of 32 weights: wa, wb this lane's code words of rows g and
 // g+8, da, db the rows' scales, xb this lane's B fragment of column tile 0.
-template <int NT>
-__device__ __forceinline__ void block_math(uint32_t wa, uint32_t wb, float da, float db, float acc[NT][4],
-                                           const uint8_t* xb, uint32_t xtile) {
+// With one column a lane keeps one sum for each row.
+template <int CP>
+__device__ __forceinline__ void block_math(uint32_t wa, uint32_t wb, float da, float db, float (*acc)[4],
+                                           const uint8_t* xb) {
   const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
   const uint32_t l0 = low_codes(wa), l1 = low_codes(wb), l2 = low_codes(wa8), l3 = low_codes(wb8);
   const uint32_t h0 = high_codes(wa), h1 = high_codes(wb), h2 = high_codes(wa8), h3 = high_codes(wb8);
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const uint4 xv = ld128(xb + j * xtile);
+  for (int j = 0; j < (CP + 7) / 8; ++j) {
+    const uint4 xv = ld128(xb + 512 * j);
     float c[4];
     mma_f16_z(c, l0, l1, l2, l3, xv.x, xv.y);
     mma_f16(c, h0, h1, h2, h3, xv.z, xv.w);
     acc[j][0] = fmaf(da, c[0], acc[j][0]);
-    acc[j][1] = fmaf(da, c[1], acc[j][1]);
+    if (CP > 1) acc[j][1] = fmaf(da, c[1], acc[j][1]);
     acc[j][2] = fmaf(db, c[2], acc[j][2]);
-    acc[j][3] = fmaf(db, c[3], acc[j][3]);
+    if (CP > 1) acc[j][3] = fmaf(db, c[3], acc[j][3]);
   }
 }
 
-// A stage of n units of two blocks (Q4_0) or of one super-block from its ring slot.
-template <int FMT, int NT>
-__device__ __forceinline__ void stage_math(const uint8_t* st, int n, int lane, float acc[NT][4],
-                                           const uint8_t* xb, uint32_t xpitch, uint32_t xtile) {
-  const int g8 = lane >> 2;
+// A stage from its ring slot: n units of two blocks (Q4_0) or one super-block.
+template <int FMT, int CP, bool FULL>
+__device__ __forceinline__ void stage_math(const uint8_t* st, int n, int lane, float (*acc)[4],
+                                           const uint8_t* xb) {
+  const uint8_t* code = st + (FMT == GQ_FMT_Q4_0 ? 16 : 32) * lane;
+  const uint8_t* sc = st + kStageCodes + 4 * (lane >> 2);
   if constexpr (FMT == GQ_FMT_Q4_0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (i < n) {
-        const uint4 v = ld128(st + 512 * i + 16 * lane);
-        const float2 da = halves(ld32(st + kStageCodes + 64 * i + 4 * g8));
-        const float2 db = halves(ld32(st + kStageCodes + 64 * i + 32 + 4 * g8));
-        block_math<NT>(v.x, v.y, da.x, db.x, acc, xb + (2 * i) * xpitch, xtile);
-        block_math<NT>(v.z, v.w, da.y, db.y, acc, xb + (2 * i + 1) * xpitch, xtile);
+      if (FULL || i < n) {
+        const uint4 v = ld128(code + 512 * i);
+        const float2 da = halves(ld32(sc + 64 * i));
+        const float2 db = halves(ld32(sc + 64 * i + 32));
+        block_math<CP>(v.x, v.y, da.x, db.x, acc, xb + (2 * i) * (64 * CP));
+        block_math<CP>(v.z, v.w, da.y, db.y, acc, xb + (2 * i + 1) * (64 * CP));
       }
     }
   } else {
-    const float sa = __half2float(*reinterpret_cast<const __half*>(st + kStageCodes + 128 + 2 * g8));
-    const float sb = __half2float(*reinterpret_cast<const __half*>(st + kStageCodes + 144 + 2 * g8));
+    const uint8_t* ss = st + kStageCodes + 128 + 2 * (lane >> 2);
+    const float sa = __half2float(*reinterpret_cast<const __half*>(ss));
+    const float sb = __half2float(*reinterpret_cast<const __half*>(ss + 16));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // half a super-block: lane-ordered 32 bytes of codes
-      const uint32_t qa = ld32(st + kStageCodes + 64 * i + 4 * g8) ^ 0x80808080u;
-      const uint32_t qb = ld32(st + kStageCodes + 64 * i + 32 + 4 * g8) ^ 0x80808080u;
-      const uint4 v = ld128(st + 1024 * i + 32 * lane), w = ld128(st + 1024 * i + 32 * lane + 16);
-      const uint8_t* x = xb + (4 * i) * xpitch;
-      block_math<NT>(v.x, v.y, sa * flipped_byte(qa, 0), sb * flipped_byte(qb, 0), acc, x, xtile);
-      block_math<NT>(v.z, v.w, sa * flipped_byte(qa, 1), sb * flipped_byte(qb, 1), acc, x + xpitch, xtile);
-      block_math<NT>(w.x, w.y, sa * flipped_byte(qa, 2), sb * flipped_byte(qb, 2), acc, x + 2 * xpitch, xtile);
-      block_math<NT>(w.z, w.w, sa * flipped_byte(qa, 3), sb * flipped_byte(qb, 3), acc, x + 3 * xpitch, xtile);
+      const uint32_t qa = ld32(sc + 64 * i) ^ 0x80808080u, qb = ld32(sc + 64 * i + 32) ^ 0x80808080u;
+      const uint4 v = ld128(code + 1024 * i), w = ld128(code + 1024 * i + 16);
+      const uint8_t* x = xb + (4 * i) * (64 * CP);
+      block_math<CP>(v.x, v.y, sa * flipped_byte(qa, 0), sb * flipped_byte(qb, 0), acc, x);
+      block_math<CP>(v.z, v.w, sa * flipped_byte(qa, 1), sb * flipped_byte(qb, 1), acc, x + 64 * CP);
+      block_math<CP>(w.x, w.y, sa * flipped_byte(qa, 2), sb * flipped_byte(qb, 2), acc, x + 128 * CP);
+      block_math<CP>(w.z, w.w, sa * flipped_byte(qa, 3), sb * flipped_byte(qb, 3), acc, x + 192 * CP);
     }
   }
 }
@@ -371,20 +352,54 @@ __device__ __forceinline__ const uint8_t* group_at(const MoeArgs& a, int e, int 
   return w + (static_cast<int64_t>(e) * a.groups + g) * a.group_bytes;
 }
 
-// A warp's next copy: stage k of row group q of the string, `left` stages in all.
-template <bool GATE_UP>
+// A warp's next copy: stage k of row group q of the string, `left` stages in
+// all; this lane's sources in it.
+template <int FMT, bool GATE_UP>
 struct Feed {
-  const uint8_t* group;
+  const uint8_t* code;
+  const uint8_t* scale;
   int e, q, k, left;
-  template <int FMT>
+
+  // Sources of stage k of a row group.
+  __device__ __forceinline__ void seek(const MoeArgs& a, int i0, int lane) {
+    const uint8_t* group = group_at<GATE_UP>(a, e, i0 + q);
+    const int c = k >> 3, j = k & 7;
+    if constexpr (FMT == GQ_FMT_Q4_0) {
+      // tiles of 32 units (512 bytes of codes, 64 of scales); a stage is four
+      const int nu = min(32, (a.K >> 6) - 32 * c);
+      const uint8_t* tile = group + static_cast<int64_t>(c) * 18432;
+      code = tile + 2048 * j + 16 * lane;
+      scale = tile + 512 * nu + 256 * j + 16 * lane;
+    } else {
+      // tiles of 8 super-blocks (2048 bytes of codes, 128 of sub-scales, 32 of S); a stage is one
+      const int ns = min(8, (a.K >> 8) - 8 * c);
+      const uint8_t* tile = group + static_cast<int64_t>(c) * 17664;
+      code = tile + 2048 * j + 16 * lane;
+      scale = lane < 8 ? tile + 2048 * ns + 128 * j + 16 * lane : tile + 2176 * ns + 32 * j + 16 * (lane - 8);
+    }
+  }
   __device__ __forceinline__ void step(const MoeArgs& a, int i0, int stages, uint32_t dst, int lane) {
     if (left > 0) {
-      copy_stage<FMT>(dst, group, k, a.K, lane);
+      dst += 16 * lane;
+      const int n = FMT == GQ_FMT_Q4_0 && k == stages - 1 ? (a.K >> 6) - 4 * k : 4;  // units
+      if (n == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) copy16(dst + 512 * i, code + 512 * i);
+      } else {
+        for (int i = 0; i < n; ++i) copy16(dst + 512 * i, code + 512 * i);
+      }
+      if (lane < (FMT == GQ_FMT_Q4_0 ? 4 * n : 10)) copy16(dst + kStageCodes, scale);
       --left;
-      if (++k == stages) {
-        k = 0;
-        ++q;
-        if (left > 0) group = group_at<GATE_UP>(a, e, i0 + q);
+      ++k;
+      if (k == stages || (k & 7) == 0) {  // another tile
+        if (k == stages) {
+          k = 0;
+          ++q;
+        }
+        if (left > 0) seek(a, i0, lane);
+      } else {
+        code += 2048;
+        scale += FMT == GQ_FMT_Q4_0 ? 256 : (lane < 8 ? 128 : 32);
       }
     }
     copies_commit();  // also an empty group: groups count stages
@@ -394,43 +409,52 @@ struct Feed {
 // This warp's stages [u, u1) of the string, the first kDepth of them under way:
 // partial sums to the table, part (row group + warp) for each row group that
 // the warp has stages of.
-template <int FMT, int NT, bool GATE_UP>
-__device__ __forceinline__ void stream(const MoeArgs& a, Feed<GATE_UP>& feed, int i0, int stages, int u,
-                                       int u1, int ncol, uint32_t ring, float* tab) {
+template <int FMT, int CP, bool GATE_UP>
+__device__ __forceinline__ void stream(const MoeArgs& a, Feed<FMT, GATE_UP>& feed, int i0, int stages, int u,
+                                       int u1, uint32_t ring, float* tab) {
+  constexpr int NT = (CP + 7) / 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
-  const int ncp = (ncol + 1) & ~1;
-  // columns past the last read an existing one; their sums are not used
-  const uint32_t xlane = static_cast<uint32_t>(min(g8, ncol - 1) * 64 + t * 16);
-  const uint32_t xtile = NT > 1 ? static_cast<uint32_t>(min(8 + g8, ncol - 1) * 64 + t * 16) - xlane : 0u;
-  const uint32_t xpitch = static_cast<uint32_t>(ncol) * 64;
-  const uint8_t* xb = msm + a.b_off + xlane;
+  // columns past the last repeat existing ones (or hold what was there); their sums are not used
+  const uint8_t* xb = msm + a.b_off + (g8 & (CP - 1)) * 64 + t * 16;
   const uint32_t sbase = smem_addr(msm);
+  const int last_n = FMT == GQ_FMT_Q4_0 ? (a.K >> 6) - 4 * (stages - 1) : 4;  // units of a row's last stage
   float acc[NT][4];
 #pragma unroll
   for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-  int q = u / stages, k = u - q * stages, slot = 0;
+  int q = u / stages, k = u - q * stages;
+  uint32_t st = ring;
+  const uint8_t* x = xb + k * (8 * 64 * CP);
   for (; u < u1; ++u) {
     copies_wait<kDepth - 1>();
     __syncwarp();  // every lane's copies of the stage
-    const uint32_t st = ring + slot * kStageBytes;
-    const int n = FMT == GQ_FMT_Q4_0 ? min(4, (a.K >> 6) - 4 * k) : 4;
-    stage_math<FMT, NT>(msm + st, n, lane, acc, xb + static_cast<uint32_t>(8 * k) * xpitch, xpitch, xtile);
+    const bool end = ++k == stages;
+    if (FMT == GQ_FMT_KSB || !end || last_n == 4)
+      stage_math<FMT, CP, true>(msm + st, 4, lane, acc, x);
+    else
+      stage_math<FMT, CP, false>(msm + st, last_n, lane, acc, x);
+    x += 8 * 64 * CP;
     __syncwarp();  // every lane has read the stage
-    feed.template step<FMT>(a, i0, stages, sbase + st, lane);
-    if (++slot == kDepth) slot = 0;
-    if (++k == stages || u + 1 == u1) {
-      float* d = tab + (q + warp) * 16 * ncp;
+    feed.step(a, i0, stages, sbase + st, lane);
+    st = st == ring + (kDepth - 1) * kStageBytes ? ring : st + kStageBytes;
+    if (end || u + 1 == u1) {
+      float* d = tab + (q + warp) * (16 * CP);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int c = 8 * j + 2 * t;
-        if (c < ncp) {
-          *reinterpret_cast<float2*>(d + g8 * ncp + c) = make_float2(acc[j][0], acc[j][1]);
-          *reinterpret_cast<float2*>(d + (g8 + 8) * ncp + c) = make_float2(acc[j][2], acc[j][3]);
+        if (CP == 1) {
+          if (t == 0) {
+            d[g8] = acc[j][0];
+            d[g8 + 8] = acc[j][2];
+          }
+        } else if (c < CP) {
+          *reinterpret_cast<float2*>(d + g8 * CP + c) = make_float2(acc[j][0], acc[j][1]);
+          *reinterpret_cast<float2*>(d + (g8 + 8) * CP + c) = make_float2(acc[j][2], acc[j][3]);
         }
         acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
       }
       k = 0;
       ++q;
+      x = xb;
     }
   }
 }
@@ -479,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs a) {
   String st;
   bool more = cur.next(st);
   const uint32_t ring = static_cast<uint32_t>(warp * kDepth * kStageBytes);
-  Feed<GATE_UP> feed;
+  Feed<FMT, GATE_UP> feed;
   // the first stages of this warp's share of a string
   auto fetch = [&](const String& s) {
     const int tu = s.n * stages;
@@ -488,17 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs a) {
     feed.q = u0 / stages;
     feed.k = u0 - feed.q * stages;
     feed.left = tu * (warp + 1) / kWarps - u0;
-    feed.group = group_at<GATE_UP>(a, feed.e, s.i0 + min(feed.q, s.n - 1));
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i)
-      feed.template step<FMT>(a, s.i0, stages, smem_addr(msm) + ring + i * kStageBytes, lane);
+    if (feed.left > 0) feed.seek(a, s.i0, lane);
+    for (int i = 0; i < kDepth; ++i) feed.step(a, s.i0, stages, smem_addr(msm) + ring + i * kStageBytes, lane);
   };
   if (more) fetch(st);
   if (!GATE_UP) pdl_wait();  // h and the slots' largest values are final
   int buf = 0, loaded = -1;
   while (more) {
     const Seg sg = pl.seg[st.seg];
-    const int ncol = a.two ? 2 * sg.n : sg.n, ncp = (ncol + 1) & ~1;
+    const int pitch = col_pitch(a.two ? 2 * sg.n : sg.n);
     if (loaded != st.seg) {
       load_b<GATE_UP>(a, pl, sg, st.seg & 1);
       loaded = st.seg;
@@ -506,10 +528,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs a) {
     float* tab = reinterpret_cast<float*>(msm + a.tab_off) + buf * a.tabfloats;
     const int tu = st.n * stages;
     const int u0 = tu * warp / kWarps, u1 = tu * (warp + 1) / kWarps;
-    if (ncol <= 8)
-      stream<FMT, 1, GATE_UP>(a, feed, st.i0, stages, u0, u1, ncol, ring, tab);
-    else
-      stream<FMT, 2, GATE_UP>(a, feed, st.i0, stages, u0, u1, ncol, ring, tab);
+    switch (pitch) {
+      case 1: stream<FMT, 1, GATE_UP>(a, feed, st.i0, stages, u0, u1, ring, tab); break;
+      case 2: stream<FMT, 2, GATE_UP>(a, feed, st.i0, stages, u0, u1, ring, tab); break;
+      case 4: stream<FMT, 4, GATE_UP>(a, feed, st.i0, stages, u0, u1, ring, tab); break;
+      case 8: stream<FMT, 8, GATE_UP>(a, feed, st.i0, stages, u0, u1, ring, tab); break;
+      default: stream<FMT, 16, GATE_UP>(a, feed, st.i0, stages, u0, u1, ring, tab);
+    }
     const String done = st;
     more = cur.next(st);
     if (more) fetch(st);
@@ -521,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs a) {
       float v = 0.f;
       for (int ww = w0; ww <= w1; ++ww) {
         if (tu * ww / kWarps == tu * (ww + 1) / kWarps) continue;  // no stages
-        const float* p = tab + (static_cast<int64_t>(q + ww) * 16 + row) * ncp + c;
+        const float* p = tab + (static_cast<int64_t>(q + ww) * 16 + row) * pitch + c;
         v += a.two ? p[0] + p[1] : p[0];
       }
       return v;
@@ -611,9 +636,9 @@ size_t shape_smem(MoeArgs& a) {
   const size_t left = kDynSmem - kRingBytes - plan;
   const size_t part = 2 * 16 * sizeof(float);  // of both tables, for each column
   const size_t most = left / (static_cast<size_t>(a.K) * 2 + kMinSlots * part);
-  int cols = static_cast<int>(most < kMaxCols ? most : kMaxCols) & ~1;
-  const int need = pairs * (a.two ? 2 : 1);
-  if (cols > need) cols = (need + 1) & ~1;
+  const size_t need = static_cast<size_t>(pairs) * (a.two ? 2 : 1);
+  int cols = 2;  // powers of two
+  while (cols < kMaxCols && static_cast<size_t>(2 * cols) <= most && static_cast<size_t>(cols) < need) cols *= 2;
   const size_t b = static_cast<size_t>(cols) * a.K * 2;
   const size_t slots = (left - b) / (part * cols);
   a.cap = a.two ? cols / 2 : cols;
