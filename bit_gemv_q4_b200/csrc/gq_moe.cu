@@ -8,9 +8,13 @@
 // post, section 2.3): every byte of them is read once, and nothing else is
 // large.
 //
-// Three launches joined by programmatic dependent launch: gate and up with the
-// activation between them (h, fp32, in the workspace), down (one fp32 row of
-// outputs for each token and slot), and the weighted sum over a token's slots.
+// One cooperative launch of one CTA per SM in three phases with a grid barrier
+// between them: gate and up with the activation (h, fp32, in the workspace),
+// down (one fp32 row of outputs for each token and slot), and the weighted sum
+// over a token's slots.  The first copies of down's weights are under way while
+// a CTA waits for the others.  (As three launches joined by programmatic
+// dependent launch the phases cost 8 us between the weight streams of the first
+// two: a CTA's shared memory keeps the next launch out of its SM.)
 //
 // Plan.  Every CTA reads the ids and builds the same plan in shared memory:
 // the (token, slot) pairs sorted by expert (stable), and segments of an expert
@@ -47,7 +51,7 @@
 namespace gq {
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 24;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxT = 64, kMaxTopK = 16, kMaxE = 1024;
 constexpr int kMaxPairs = kMaxT * kMaxTopK;
@@ -59,25 +63,36 @@ constexpr size_t kSmemBudget = 227 * 1024;
 // the end of a Q4_0 row group it may hold fewer (whole units of two blocks).
 constexpr int kStageCodes = 2048;
 constexpr int kStageBytes = 2304;   // codes, then scales
-constexpr int kDepth = 3;           // stages of a warp's ring
+constexpr int kDepth = 2;           // stages of a warp's ring
 constexpr size_t kRingBytes = static_cast<size_t>(kWarps) * kDepth * kStageBytes;
 
-struct MoeArgs {
+// One of the two products: gate and up, or down.
+struct Phase {
   const uint8_t* w0;        // gate, or down
-  const uint8_t* w1;        // up (gate-up launch only)
-  const void* x;            // x [T][H], or h [pairs][I] by slot
+  const uint8_t* w1;        // up
+  int K;                    // columns of the weights
+  int groups;               // row groups (16 rows) of one expert
+  int64_t group_bytes;
+  int two;                  // two columns for each token
+  int cap;                  // tokens of a segment at most
+};
+
+struct MoeArgs {
+  Phase ph[2];
+  const void* x;            // [T][H]
   const int32_t* ids;       // [T][k]
+  const float* weights;     // [T][k]
+  void* y;                  // [T][H]
   float* h;                 // [pairs][I], by slot
   float* out;               // [pairs][H], by pair
-  int* dev_status;
   unsigned* hmax;           // [pairs] largest |h| of a slot as bits, zero between calls
-  int T, k, E, K;           // K: columns of this launch's weights
-  int groups;               // row groups (16 rows) of one expert
-  int xtype, two;           // element type of x; two columns for each token
-  int cap;                  // tokens of a segment at most
+  unsigned long long* arrivals;  // at the grid barriers, a multiple of the grid between calls
+  int* dev_status;
+  long long budget;
+  int T, k, E, H;
+  int xtype, ytype;
   int tabslots;             // parts that one table holds
   int tabfloats;            // floats of one table
-  int64_t group_bytes;
   uint32_t b_off, tab_off, plan_off;  // dynamic shared memory, after the rings
 };
 
@@ -87,11 +102,13 @@ struct Seg {
 };
 
 struct Plan {
-  int nseg;
+  int nseg[2];
+  int go;                   // the grid barrier was passed
   float inv[2][kMaxCols];   // 1 / scale of a segment's tokens
-  unsigned amax[2][kMaxCols];
+  unsigned xmax[kMaxT];     // largest |x| of a token as bits
+  unsigned hmax[kMaxCols];  // of a string's tokens
   // in dynamic shared memory
-  Seg* seg;                 // [pairs]
+  Seg* seg[2];              // [pairs] of each phase
   short* order;             // [pairs] slot -> pair
   short* first;             // [E] pairs of an expert, then its first slot
   short* rank;              // [pairs] only while planning (in the rings' place)
@@ -110,61 +127,6 @@ __device__ __forceinline__ void copies_wait() {  // all but the newest N groups 
 }
 
 // ------------------------------------------------------------------- plan
-// Pairs sorted by expert (stable), and the segments.  ids outside [0, E) are
-// left out.  All threads call it.
-__device__ void make_plan(Plan& pl, const MoeArgs& a) {
-  const int P = a.T * a.k;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) pl.first[e] = 0;
-  __syncthreads();
-  if (warp == 0) {
-    // rank of each pair among its expert's, 32 pairs at a time
-    for (int p0 = 0; p0 < P; p0 += 32) {
-      const int p = p0 + lane;
-      const int id = p < P ? __ldcg(a.ids + p) : -1;
-      const bool ok = id >= 0 && id < a.E;
-      if (blockIdx.x == 0 && (id < -1 || id >= a.E)) report(a.dev_status, GQ_DEV_RANGE);
-      const unsigned peers = __match_any_sync(0xFFFFFFFFu, ok ? id : -1 - lane);
-      const int before = __popc(peers & ((1u << lane) - 1u));
-      const int base = ok ? pl.first[id] : 0;
-      __syncwarp();
-      if (ok && before == 0) pl.first[id] = static_cast<short>(base + __popc(peers));
-      if (p < P) pl.rank[p] = static_cast<short>(ok ? base + before : -1);
-      __syncwarp();
-    }
-    // counts -> first slots, and segments, in the order of the experts
-    int slots = 0, segs = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int n = e < a.E ? pl.first[e] : 0;
-      const int ns = (n + a.cap - 1) / a.cap;
-      int sn = n, ss = ns;  // inclusive sums over the lanes
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xFFFFFFFFu, sn, o), v = __shfl_up_sync(0xFFFFFFFFu, ss, o);
-        if (lane >= o) {
-          sn += u;
-          ss += v;
-        }
-      }
-      const int first = slots + sn - n, sfirst = segs + ss - ns;
-      if (e < a.E) pl.first[e] = static_cast<short>(first);
-      for (int i = 0; i < ns; ++i)
-        pl.seg[sfirst + i] = Seg{static_cast<short>(e), static_cast<short>(first + i * a.cap), min(a.cap, n - i * a.cap)};
-      slots += __shfl_sync(0xFFFFFFFFu, sn, 31);
-      segs += __shfl_sync(0xFFFFFFFFu, ss, 31);
-    }
-    if (lane == 0) pl.nseg = segs;
-  }
-  __syncthreads();
-  for (int p = threadIdx.x; p < P; p += kThreads) {
-    const int r = pl.rank[p];
-    if (r >= 0) pl.order[pl.first[__ldcg(a.ids + p)] + r] = static_cast<short>(p);
-  }
-  __syncthreads();
-}
-
-// ------------------------------------------------------------- activations
 // Eight consecutive values of an element type as floats.
 __device__ __forceinline__ void load8(const void* base, int64_t i, int type, float v[8]) {
   if (type == GQ_F32) {
@@ -187,6 +149,86 @@ __device__ __forceinline__ void load8(const void* base, int64_t i, int type, flo
   }
 }
 
+// Pairs sorted by expert (stable), and the segments of both phases (warp 0);
+// the tokens' largest |x| (the other warps).  ids outside [0, E) are left out.
+__device__ void make_plan(Plan& pl, const MoeArgs& a) {
+  const int P = a.T * a.k;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < a.E; e += kThreads) pl.first[e] = 0;
+  if (threadIdx.x < kMaxT) pl.xmax[threadIdx.x] = 0u;
+  const int id0 = warp == 0 && lane < P ? __ldcg(a.ids + lane) : -1;
+  __syncthreads();
+  if (warp == 0) {
+    // rank of each pair among its expert's, 32 pairs at a time
+    for (int p0 = 0; p0 < P; p0 += 32) {
+      const int p = p0 + lane;
+      const int id = p0 == 0 ? id0 : p < P ? __ldcg(a.ids + p) : -1;
+      const bool ok = id >= 0 && id < a.E;
+      if (blockIdx.x == 0 && (id < -1 || id >= a.E)) report(a.dev_status, GQ_DEV_RANGE);
+      const unsigned peers = __match_any_sync(0xFFFFFFFFu, ok ? id : -1 - lane);
+      const int before = __popc(peers & ((1u << lane) - 1u));
+      const int base = ok ? pl.first[id] : 0;
+      __syncwarp();
+      if (ok && before == 0) pl.first[id] = static_cast<short>(base + __popc(peers));
+      if (p < P) pl.rank[p] = static_cast<short>(ok ? base + before : -1);
+      __syncwarp();
+    }
+    // counts -> first slots, and segments, in the order of the experts
+    int slots = 0, segs[2] = {0, 0};
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int n = e < a.E ? pl.first[e] : 0;
+      if (!__any_sync(0xFFFFFFFFu, n)) continue;
+      int sn = n;  // inclusive sums over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, sn, o);
+        if (lane >= o) sn += u;
+      }
+      const int first = slots + sn - n;
+      if (e < a.E) pl.first[e] = static_cast<short>(first);
+      slots += __shfl_sync(0xFFFFFFFFu, sn, 31);
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int cap = a.ph[f].cap, ns = (n + cap - 1) / cap;
+        int ss = ns;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xFFFFFFFFu, ss, o);
+          if (lane >= o) ss += u;
+        }
+        for (int i = 0; i < ns; ++i)
+          pl.seg[f][segs[f] + ss - ns + i] =
+              Seg{static_cast<short>(e), static_cast<short>(first + i * cap), min(cap, n - i * cap)};
+        segs[f] += __shfl_sync(0xFFFFFFFFu, ss, 31);
+      }
+    }
+    if (lane < 2) pl.nseg[lane] = lane ? segs[1] : segs[0];
+  } else {
+    const int share = max(1, (kWarps - 1) / a.T), vecs = a.H / 8;  // warps for each token
+    for (int i = warp - 1; i < a.T * share; i += kWarps - 1) {
+      const int t = i / share;
+      unsigned m = 0;
+#pragma unroll 4
+      for (int r = (i - t * share) * 32 + lane; r < vecs; r += 32 * share) {
+        float v[8];
+        load8(a.x, static_cast<int64_t>(t) * a.H + 8 * r, a.xtype, v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(v[q]) & 0x7FFFFFFFu);
+      }
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      if (lane == 0) atomicMax(&pl.xmax[t], m);
+    }
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < P; p += kThreads) {
+    const int r = pl.rank[p];
+    if (r >= 0) pl.order[pl.first[__ldcg(a.ids + p)] + r] = static_cast<short>(p);
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------- activations
 // The power of two that brings the largest |value| (its bits) into [2^14,
 // 2^15); 1 for infinities and NaN, which stay what they are.
 __device__ __forceinline__ float scale_of(unsigned maxbits) {
@@ -205,43 +247,25 @@ __device__ __forceinline__ int col_pitch(int ncol) {
 // bytes at ((b * pitch + c) * 4 + t) * 16, the values 4t, 4t+2, 4t+1, 4t+3 of the
 // block and the same at +16.
 template <bool GATE_UP>
-__device__ void load_b(const MoeArgs& a, Plan& pl, const Seg& sg, int buf) {
-  const int pitch = col_pitch(a.two ? 2 * sg.n : sg.n);
-  const int vecs = a.K / 8;
-  auto row_of = [&](int c) -> int64_t {
-    return GATE_UP ? static_cast<int64_t>(pl.order[sg.slot0 + c] / a.k) * a.K
-                   : static_cast<int64_t>(sg.slot0 + c) * a.K;
-  };
-  if (threadIdx.x < sg.n)
-    pl.amax[buf][threadIdx.x] = GATE_UP ? 0u : __ldcg(a.hmax + sg.slot0 + threadIdx.x);
-  __syncthreads();
-  if (GATE_UP) {
-    for (int c = 0; c < sg.n; ++c) {
-      unsigned m = 0;
-      const int64_t row = row_of(c);
-      for (int i = threadIdx.x; i < vecs; i += kThreads) {
-        float v[8];
-        load8(a.x, row + 8 * i, a.xtype, v);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(v[q]) & 0x7FFFFFFFu);
-      }
-      m = __reduce_max_sync(0xFFFFFFFFu, m);
-      if ((threadIdx.x & 31) == 0 && m) atomicMax(&pl.amax[buf][c], m);
-    }
-    __syncthreads();
-  }
+__device__ void load_b(const MoeArgs& a, const Phase& ph, Plan& pl, const Seg& sg, int buf) {
+  const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
+  const int vecs = ph.K / 8;
+  auto row_of = [&](int c) { return GATE_UP ? pl.order[sg.slot0 + c] / a.k : sg.slot0 + c; };
+  auto max_of = [&](int c) { return GATE_UP ? pl.xmax[row_of(c)] : __ldcg(a.hmax + sg.slot0 + c); };
+  const int type = GATE_UP ? a.xtype : GQ_F32;
+  const void* src = GATE_UP ? a.x : a.h;
   if (threadIdx.x < sg.n)  // scale_of() is a power of two: the reciprocal is exact
-    pl.inv[buf][threadIdx.x] = 1.0f / scale_of(pl.amax[buf][threadIdx.x]);
+    pl.inv[buf][threadIdx.x] = 1.0f / scale_of(max_of(threadIdx.x));
   const int nvec = sg.n * vecs;
   for (int i = threadIdx.x; i < nvec; i += kThreads) {
     const int c = i / vecs, r = i - c * vecs;
     const int b = r >> 2, q = r & 3;
-    const float s = scale_of(pl.amax[buf][c]);
     float v[8];
-    load8(a.x, row_of(c) + 8 * r, a.xtype, v);
-    const int col = a.two ? 2 * c : c;
+    load8(src, static_cast<int64_t>(row_of(c)) * ph.K + 8 * r, type, v);
+    const float s = scale_of(max_of(c));
+    const int col = ph.two ? 2 * c : c;
     const int t0 = 2 * (q & 1);
-    for (int part = 0; part <= a.two; ++part) {
+    for (int part = 0; part <= ph.two; ++part) {
       __half hv[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -346,7 +370,7 @@ __device__ __forceinline__ void stage_math(const uint8_t* st, int n, int lane, f
 // A string of row groups [i0, i0 + n) of one expert (gate and up: row group i
 // is one of gate's, then the same of up's).
 template <bool GATE_UP>
-__device__ __forceinline__ const uint8_t* group_at(const MoeArgs& a, int e, int i) {
+__device__ __forceinline__ const uint8_t* group_at(const Phase& a, int e, int i) {
   const uint8_t* w = (GATE_UP && (i & 1)) ? a.w1 : a.w0;
   const int g = GATE_UP ? i >> 1 : i;
   return w + (static_cast<int64_t>(e) * a.groups + g) * a.group_bytes;
@@ -361,7 +385,7 @@ struct Feed {
   int e, q, k, left;
 
   // Sources of stage k of a row group.
-  __device__ __forceinline__ void seek(const MoeArgs& a, int i0, int lane) {
+  __device__ __forceinline__ void seek(const Phase& a, int i0, int lane) {
     const uint8_t* group = group_at<GATE_UP>(a, e, i0 + q);
     const int c = k >> 3, j = k & 7;
     if constexpr (FMT == GQ_FMT_Q4_0) {
@@ -378,7 +402,7 @@ struct Feed {
       scale = lane < 8 ? tile + 2048 * ns + 128 * j + 16 * lane : tile + 2176 * ns + 32 * j + 16 * (lane - 8);
     }
   }
-  __device__ __forceinline__ void step(const MoeArgs& a, int i0, int stages, uint32_t dst, int lane) {
+  __device__ __forceinline__ void step(const Phase& a, int i0, int stages, uint32_t dst, int lane) {
     if (left > 0) {
       dst += 16 * lane;
       const int n = FMT == GQ_FMT_Q4_0 && k == stages - 1 ? (a.K >> 6) - 4 * k : 4;  // units
@@ -410,12 +434,12 @@ struct Feed {
 // partial sums to the table, part (row group + warp) for each row group that
 // the warp has stages of.
 template <int FMT, int CP, bool GATE_UP>
-__device__ __forceinline__ void stream(const MoeArgs& a, Feed<FMT, GATE_UP>& feed, int i0, int stages, int u,
+__device__ __forceinline__ void stream(const Phase& a, uint32_t b_off, Feed<FMT, GATE_UP>& feed, int i0, int stages, int u,
                                        int u1, uint32_t ring, float* tab) {
   constexpr int NT = (CP + 7) / 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
   // columns past the last repeat existing ones (or hold what was there); their sums are not used
-  const uint8_t* xb = msm + a.b_off + (g8 & (CP - 1)) * 64 + t * 16;
+  const uint8_t* xb = msm + b_off + (g8 & (CP - 1)) * 64 + t * 16;
   const uint32_t sbase = smem_addr(msm);
   const int last_n = FMT == GQ_FMT_Q4_0 ? (a.K >> 6) - 4 * (stages - 1) : 4;  // units of a row's last stage
   float acc[NT][4];
@@ -464,156 +488,206 @@ __device__ __forceinline__ void stream(const MoeArgs& a, Feed<FMT, GATE_UP>& fee
 struct String {
   int seg, i0, n;  // segment, first row group (of the string's kind), how many
 };
-template <bool GATE_UP>
-struct Cursor {
-  int64_t r, r1;
-  int groups, most;  // row groups of an expert (pairs counted once), most in a string
-  __device__ __forceinline__ bool next(String& s) {
-    if (r >= r1) return false;
-    s.seg = static_cast<int>(r / groups);
-    const int g = static_cast<int>(r - static_cast<int64_t>(s.seg) * groups);
-    const int left = static_cast<int>(i64min(r1 - r, groups - g));
+template <int FMT, bool GATE_UP>
+struct Work {
+  int r, r1;    // row groups left (pairs of them for gate and up)
+  int stages;   // of a row group
+  bool more;
+  String st;
+  Feed<FMT, GATE_UP> feed;
+
+  __device__ __forceinline__ void next(const Phase& ph, int most) {
+    more = r < r1;
+    if (!more) return;
+    st.seg = r / ph.groups;
+    const int g = r - st.seg * ph.groups;
+    const int left = min(r1 - r, ph.groups - g);
     const int strings = (left + most - 1) / most;
     const int n = (left + strings - 1) / strings;  // even strings
-    s.i0 = GATE_UP ? 2 * g : g;
-    s.n = GATE_UP ? 2 * n : n;
+    st.i0 = GATE_UP ? 2 * g : g;
+    st.n = GATE_UP ? 2 * n : n;
     r += n;
-    return true;
   }
-};
-
-template <int FMT, bool GATE_UP>
-__global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs a) {
-  __shared__ Plan pl;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    pl.seg = reinterpret_cast<Seg*>(msm + a.plan_off);
-    pl.order = reinterpret_cast<short*>(pl.seg + a.T * a.k);
-    pl.first = pl.order + a.T * a.k;
-    pl.rank = reinterpret_cast<short*>(msm);
-  }
-  if (GATE_UP) pdl_wait();  // ids and x are final (the down launch starts after that)
-  pdl_launch_dependents();
-  __syncthreads();
-  make_plan(pl, a);
-  const int stages = FMT == GQ_FMT_Q4_0 ? (a.K + 255) / 256 : a.K / 256;  // of a row group
-  const int64_t total = static_cast<int64_t>(pl.nseg) * a.groups;
-  Cursor<GATE_UP> cur{total * blockIdx.x / gridDim.x, total * (blockIdx.x + 1) / gridDim.x, a.groups,
-                      (a.tabslots - kWarps) / (GATE_UP ? 2 : 1)};
-  String st;
-  bool more = cur.next(st);
-  const uint32_t ring = static_cast<uint32_t>(warp * kDepth * kStageBytes);
-  Feed<FMT, GATE_UP> feed;
-  // the first stages of this warp's share of a string
-  auto fetch = [&](const String& s) {
-    const int tu = s.n * stages;
+  // The first copies of this warp's share of the string.
+  __device__ __forceinline__ void fetch(const Phase& ph, const Plan& pl, uint32_t ring) {
+    if (!more) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tu = st.n * stages;
     const int u0 = tu * warp / kWarps;
-    feed.e = pl.seg[s.seg].e;
+    feed.e = pl.seg[!GATE_UP][st.seg].e;
     feed.q = u0 / stages;
     feed.k = u0 - feed.q * stages;
     feed.left = tu * (warp + 1) / kWarps - u0;
-    if (feed.left > 0) feed.seek(a, s.i0, lane);
-    for (int i = 0; i < kDepth; ++i) feed.step(a, s.i0, stages, smem_addr(msm) + ring + i * kStageBytes, lane);
-  };
-  if (more) fetch(st);
-  if (!GATE_UP) pdl_wait();  // h and the slots' largest values are final
+    if (feed.left > 0) feed.seek(ph, st.i0, lane);
+    for (int i = 0; i < kDepth; ++i) feed.step(ph, st.i0, stages, smem_addr(msm) + ring + i * kStageBytes, lane);
+  }
+  __device__ __forceinline__ void start(const MoeArgs& a, const Plan& pl, uint32_t ring) {
+    const Phase& ph = a.ph[!GATE_UP];
+    const unsigned total = static_cast<unsigned>(pl.nseg[!GATE_UP]) * ph.groups;  // at most 2^20
+    r = static_cast<int>(total * blockIdx.x / gridDim.x);
+    r1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+    stages = FMT == GQ_FMT_Q4_0 ? (ph.K + 255) / 256 : ph.K / 256;
+    next(ph, (a.tabslots - kWarps) / (GATE_UP ? 2 : 1));
+    fetch(ph, pl, ring);
+  }
+};
+
+// All strings of a phase.
+template <int FMT, bool GATE_UP>
+__device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, GATE_UP>& wk, uint32_t ring) {
+  const Phase& ph = a.ph[!GATE_UP];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = wk.stages;
   int buf = 0, loaded = -1;
-  while (more) {
-    const Seg sg = pl.seg[st.seg];
-    const int pitch = col_pitch(a.two ? 2 * sg.n : sg.n);
+  while (wk.more) {
+    const String st = wk.st;
+    const Seg sg = pl.seg[!GATE_UP][st.seg];
+    const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
     if (loaded != st.seg) {
-      load_b<GATE_UP>(a, pl, sg, st.seg & 1);
+      load_b<GATE_UP>(a, ph, pl, sg, st.seg & 1);
       loaded = st.seg;
     }
     float* tab = reinterpret_cast<float*>(msm + a.tab_off) + buf * a.tabfloats;
     const int tu = st.n * stages;
     const int u0 = tu * warp / kWarps, u1 = tu * (warp + 1) / kWarps;
     switch (pitch) {
-      case 1: stream<FMT, 1, GATE_UP>(a, feed, st.i0, stages, u0, u1, ring, tab); break;
-      case 2: stream<FMT, 2, GATE_UP>(a, feed, st.i0, stages, u0, u1, ring, tab); break;
-      case 4: stream<FMT, 4, GATE_UP>(a, feed, st.i0, stages, u0, u1, ring, tab); break;
-      case 8: stream<FMT, 8, GATE_UP>(a, feed, st.i0, stages, u0, u1, ring, tab); break;
-      default: stream<FMT, 16, GATE_UP>(a, feed, st.i0, stages, u0, u1, ring, tab);
+      case 1: stream<FMT, 1, GATE_UP>(ph, a.b_off, wk.feed, st.i0, stages, u0, u1, ring, tab); break;
+      case 2: stream<FMT, 2, GATE_UP>(ph, a.b_off, wk.feed, st.i0, stages, u0, u1, ring, tab); break;
+      case 4: stream<FMT, 4, GATE_UP>(ph, a.b_off, wk.feed, st.i0, stages, u0, u1, ring, tab); break;
+      case 8: stream<FMT, 8, GATE_UP>(ph, a.b_off, wk.feed, st.i0, stages, u0, u1, ring, tab); break;
+      default: stream<FMT, 16, GATE_UP>(ph, a.b_off, wk.feed, st.i0, stages, u0, u1, ring, tab);
     }
-    const String done = st;
-    more = cur.next(st);
-    if (more) fetch(st);
+    wk.next(ph, (a.tabslots - kWarps) / (GATE_UP ? 2 : 1));
+    wk.fetch(ph, pl, ring);
+    if (GATE_UP && threadIdx.x < kMaxCols) pl.hmax[threadIdx.x] = 0u;
     __syncthreads();  // the table is complete; B and the other table are free
-    // sums of the row groups, in warp order
-    auto sum = [&](int q, int row, int c) {
-      const int first = q * stages, last = first + stages - 1;
-      const int w0 = (16 * (first + 1) - 1) / tu, w1 = (16 * (last + 1) - 1) / tu;
-      float v = 0.f;
-      for (int ww = w0; ww <= w1; ++ww) {
-        if (tu * ww / kWarps == tu * (ww + 1) / kWarps) continue;  // no stages
-        const float* p = tab + (static_cast<int64_t>(q + ww) * 16 + row) * pitch + c;
-        v += a.two ? p[0] + p[1] : p[0];
+    // A warp takes two row groups (gate and up of the same rows, or two of
+    // down's), 16 lanes each, and adds their parts in warp order.
+    const float* inv = pl.inv[st.seg & 1];
+    const int row = lane & 15, half = lane >> 4;
+    for (int p = warp; p < (st.n + 1) / 2; p += kWarps) {
+      const int q = min(2 * p + half, st.n - 1);
+      const int lo = q * stages, hi = lo + stages - 1;
+      const int w0 = (kWarps * (lo + 1) - 1) / tu, w1 = (kWarps * (hi + 1) - 1) / tu;
+      for (int c = 0; c < sg.n; ++c) {
+        const int col = ph.two ? 2 * c : c;
+        float v = 0.f;
+        for (int w = w0; w <= w1; ++w) {
+          if (tu * w / kWarps == tu * (w + 1) / kWarps) continue;  // no stages
+          const float* t = tab + ((q + w) * 16 + row) * pitch + col;
+          v += ph.two ? t[0] + t[1] : t[0];
+        }
+        v *= inv[c];
+        if constexpr (GATE_UP) {
+          const float up = __shfl_down_sync(0xFFFFFFFFu, v, 16);
+          const float h = v / (1.0f + expf(-v)) * up;
+          unsigned m = 0;
+          if (half == 0) {
+            __stcg(a.h + static_cast<int64_t>(sg.slot0 + c) * (ph.groups * 16) + (st.i0 / 2 + p) * 16 + row, h);
+            m = __float_as_uint(h) & 0x7FFFFFFFu;
+          }
+          m = __reduce_max_sync(0xFFFFFFFFu, m);
+          if (lane == 0) atomicMax(&pl.hmax[c], m);
+        } else if (2 * p + half < st.n) {
+          const int pair = pl.order[sg.slot0 + c];
+          __stcg(a.out + static_cast<int64_t>(pair) * (ph.groups * 16) + (st.i0 + q) * 16 + row, v);
+        }
       }
-      return v;
-    };
-    const float* inv = pl.inv[done.seg & 1];
-    if constexpr (GATE_UP) {
-      const int cells = done.n / 2 * 16 * sg.n;
-      for (int i = threadIdx.x; i < cells; i += kThreads) {
-        const int row = i & 15, rest = i >> 4;
-        const int c = rest % sg.n, p = rest / sg.n;
-        const int col = a.two ? 2 * c : c;
-        const float g = sum(2 * p, row, col) * inv[c];
-        const float up = sum(2 * p + 1, row, col) * inv[c];
-        const float h = g / (1.0f + expf(-g)) * up;
-        const int slot = sg.slot0 + c;
-        a.h[static_cast<int64_t>(slot) * (a.groups * 16) + (done.i0 / 2 + p) * 16 + row] = h;
-        // the 16 rows of one token lie in one half of a warp
-        unsigned m = __float_as_uint(h) & 0x7FFFFFFFu;
-        const unsigned half = 0xFFFFu << (lane & 16);
-        m = __reduce_max_sync(half, m);
-        if (row == 0) atomicMax(a.hmax + slot, m);
-      }
-    } else {
-      const int cells = done.n * 16 * sg.n;
-      for (int i = threadIdx.x; i < cells; i += kThreads) {
-        const int row = i & 15, rest = i >> 4;
-        const int c = rest % sg.n, q = rest / sg.n;
-        const float v = sum(q, row, a.two ? 2 * c : c) * inv[c];
-        const int pair = pl.order[sg.slot0 + c];
-        a.out[static_cast<int64_t>(pair) * (a.groups * 16) + (done.i0 + q) * 16 + row] = v;
-      }
+    }
+    if (GATE_UP) {
+      __syncthreads();
+      if (threadIdx.x < sg.n) atomicMax(a.hmax + sg.slot0 + threadIdx.x, pl.hmax[threadIdx.x]);
     }
     buf ^= 1;
   }
 }
 
-// y[t] = sum_j w[t][j] * out[t][j] over the slots that name an expert; the
-// slots' largest values are cleared for the next call.
-__global__ void __launch_bounds__(256) moe_sum_kernel(const float* out, const int32_t* ids,
-                                                      const float* weights, unsigned* hmax, void* y,
-                                                      int T, int k, int E, int H, int ytype) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int64_t n = static_cast<int64_t>(T) * H;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i < T * k) hmax[i] = 0u;
-  if (i >= n) return;
-  const int t = static_cast<int>(i / H), c = static_cast<int>(i - static_cast<int64_t>(t) * H);
-  float v = 0.f;
-  for (int j = 0; j < k; ++j) {
-    const int id = __ldcg(ids + t * k + j);
-    if (id >= 0 && id < E)
-      v = fmaf(__ldcg(weights + t * k + j), __ldcg(out + (static_cast<int64_t>(t) * k + j) * H + c), v);
+// All CTAs of the grid arrive, and what each wrote before is seen by all after;
+// false once the budget has passed.  The arrivals only ever count up (in 64
+// bits), so nothing has to be cleared.
+__device__ __forceinline__ bool grid_barrier(const MoeArgs& a, Plan& pl) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const unsigned long long n = atomicAdd(a.arrivals, 1ull);
+    const unsigned long long target = (n / gridDim.x + 1) * gridDim.x;
+    const long long t0 = clock64();
+    int go = 1;
+    for (;;) {
+      unsigned long long v;
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(a.arrivals) : "memory");
+      if (v >= target) break;
+      if (clock64() - t0 > a.budget) {
+        go = 0;
+        break;
+      }
+    }
+    __threadfence();
+    pl.go = go;
   }
-  store_elem(y, i, v, ytype);
+  __syncthreads();
+  return pl.go != 0;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ MoeArgs a) {
+  __shared__ Plan pl;
+  if (threadIdx.x == 0) {
+    const int pairs = a.T * a.k;
+    pl.seg[0] = reinterpret_cast<Seg*>(msm + a.plan_off);
+    pl.seg[1] = pl.seg[0] + pairs;
+    pl.order = reinterpret_cast<short*>(pl.seg[1] + pairs);
+    pl.first = pl.order + pairs;
+    pl.rank = reinterpret_cast<short*>(msm);
+  }
+  pdl_wait();  // ids and x are final
+  pdl_launch_dependents();
+  __syncthreads();
+  make_plan(pl, a);
+  const uint32_t ring = static_cast<uint32_t>((threadIdx.x >> 5) * kDepth * kStageBytes);
+  Work<FMT, true> gate_up;
+  gate_up.start(a, pl, ring);
+  run_phase<FMT, true>(a, pl, gate_up, ring);
+  Work<FMT, false> down;
+  down.start(a, pl, ring);  // the first copies are under way while this CTA waits
+  bool ok = grid_barrier(a, pl);
+  if (ok) {
+    run_phase<FMT, false>(a, pl, down, ring);
+    ok = grid_barrier(a, pl);
+  }
+  if (!ok) {
+    copies_wait<0>();
+    if (threadIdx.x == 0) report(a.dev_status, GQ_DEV_TIMEOUT);
+    return;
+  }
+  // y[t] = sum_j w[t][j] * out[t][j] over the slots that name an expert; the
+  // slots' largest values are cleared for the next call
+  const int n = a.T * a.H;
+  const int i0 = static_cast<int>(blockIdx.x * kThreads + threadIdx.x);
+  if (i0 < a.T * a.k) a.hmax[i0] = 0u;
+  for (int i = i0; i < n; i += static_cast<int>(gridDim.x) * kThreads) {
+    const int t = i / a.H, c = i - t * a.H;
+    float v = 0.f;
+    for (int j = 0; j < a.k; ++j) {
+      const int id = __ldcg(a.ids + t * a.k + j);
+      if (id >= 0 && id < a.E)
+        v = fmaf(__ldcg(a.weights + t * a.k + j), __ldcg(a.out + static_cast<int64_t>(t * a.k + j) * a.H + c), v);
+    }
+    store_elem(a.y, i, v, a.ytype);
+  }
 }
 
 // ------------------------------------------------------------------- host
 size_t round256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 struct Ws {
-  size_t hmax, h, out, total;
+  size_t arrivals, hmax, h, out, total;
 };
 Ws ws_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
   Ws w;
-  w.hmax = 0;
-  w.h = kMaxPairs * 4;  // one size for every call, so that calls of any sizes may follow
+  w.arrivals = 0;
+  w.hmax = 256;
+  w.h = w.hmax + kMaxPairs * 4;  // one size for every call, so that calls of any sizes may follow
   w.out = w.h + round256(static_cast<size_t>(T * k * I) * 4);
   w.total = w.out + round256(static_cast<size_t>(T * k * H) * 4);
   return w;
@@ -624,35 +698,46 @@ bool moe_dims(int64_t T, int64_t k, int64_t E) {
 }
 bool moe_width(int fmt, int64_t K) { return K % (fmt == GQ_FMT_Q4_0 ? 64 : 256) == 0 && K <= kMaxK; }
 
-// Tokens of a segment and the layout of shared memory after the rings: the
-// plan, the B fragments (2 bytes for each value of a column), and two tables of
-// parts.  A table holds at least a string of 16 row groups.
+// Tokens of a segment and the layout of shared memory after the rings: the B
+// fragments (2 bytes for each value of a column), two tables of parts, and the
+// plan.  A table holds at least a string of 16 row groups.
 constexpr int kMinSlots = kWarps + 16, kMaxSlots = kWarps + 64;
 static_assert(sizeof(Plan) <= 1024, "the static part, up to the dynamic one's alignment");
 constexpr size_t kDynSmem = kSmemBudget - 1024;
 size_t shape_smem(MoeArgs& a) {
   const int pairs = a.T * a.k;
-  const size_t plan = (static_cast<size_t>(pairs) * (sizeof(Seg) + 2) + static_cast<size_t>(a.E) * 2 + 15) & ~size_t(15);
+  const size_t plan = (static_cast<size_t>(pairs) * (2 * sizeof(Seg) + 2) + static_cast<size_t>(a.E) * 2 + 15) & ~size_t(15);
   const size_t left = kDynSmem - kRingBytes - plan;
   const size_t part = 2 * 16 * sizeof(float);  // of both tables, for each column
-  const size_t most = left / (static_cast<size_t>(a.K) * 2 + kMinSlots * part);
-  const size_t need = static_cast<size_t>(pairs) * (a.two ? 2 : 1);
-  int cols = 2;  // powers of two
-  while (cols < kMaxCols && static_cast<size_t>(2 * cols) <= most && static_cast<size_t>(cols) < need) cols *= 2;
-  const size_t b = static_cast<size_t>(cols) * a.K * 2;
-  const size_t slots = (left - b) / (part * cols);
-  a.cap = a.two ? cols / 2 : cols;
-  a.tabslots = static_cast<int>(slots < kMaxSlots ? slots : kMaxSlots);
-  a.tabfloats = a.tabslots * 16 * cols;
+  size_t b = 0, cols = 2;
+  for (Phase& ph : a.ph) {
+    const size_t most = left / (static_cast<size_t>(ph.K) * 2 + kMinSlots * part);
+    const size_t need = static_cast<size_t>(pairs) * (ph.two ? 2 : 1);
+    size_t c = 2;  // powers of two
+    while (c < kMaxCols && 2 * c <= most && c < need) c *= 2;
+    ph.cap = static_cast<int>(ph.two ? c / 2 : c);
+    b = c * ph.K * 2 > b ? c * ph.K * 2 : b;
+    cols = c > cols ? c : cols;
+  }
+  // each phase alone leaves room for kMinSlots parts of its own columns
+  size_t slots = (left - b) / (part * cols);
+  while (slots < static_cast<size_t>(kMinSlots)) {
+    cols /= 2;
+    for (Phase& ph : a.ph)
+      if (static_cast<size_t>(ph.cap) * (ph.two ? 2 : 1) > cols) ph.cap = static_cast<int>(cols) / (ph.two ? 2 : 1);
+    slots = (left - b) / (part * cols);
+  }
+  a.tabslots = static_cast<int>(slots < static_cast<size_t>(kMaxSlots) ? slots : kMaxSlots);
+  a.tabfloats = a.tabslots * 16 * static_cast<int>(cols);
   a.b_off = kRingBytes;
   a.tab_off = a.b_off + static_cast<uint32_t>(b);
   a.plan_off = a.tab_off + 2 * a.tabfloats * 4;
   return a.plan_off + plan;
 }
 
-template <int FMT, bool GATE_UP>
+template <int FMT>
 gq_status launch_moe(MoeArgs& a, bool pdl, cudaStream_t s) {
-  auto kern = moe_kernel<FMT, GATE_UP>;
+  auto kern = moe_kernel<FMT>;
   thread_local unsigned long long configured_ctx = 0;  // per host thread and context
   const unsigned long long ctx = context_id();
   if (ctx == 0 || ctx != configured_ctx) {
@@ -662,7 +747,7 @@ gq_status launch_moe(MoeArgs& a, bool pdl, cudaStream_t s) {
     configured_ctx = ctx;
   }
   const size_t smem = shape_smem(a);
-  return launch(kern, dim3(sm_count()), dim3(kThreads), smem, s, pdl, a);
+  return launch_cooperative(kern, dim3(sm_count()), dim3(kThreads), smem, s, pdl, a);
 }
 
 template <int FMT>
@@ -692,41 +777,29 @@ gq_status moe_entry(const void* gate, const void* up, const void* down, int64_t 
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GQ_ERR_ALIGNMENT;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
 
+  const auto row_bytes = [](int64_t K) { return FMT == GQ_FMT_Q4_0 ? K / 32 * 18 : K / 256 * 138; };
   MoeArgs a{};
+  a.ph[0] = Phase{static_cast<const uint8_t*>(gate), static_cast<const uint8_t*>(up), static_cast<int>(H),
+                  static_cast<int>(I / 16), 16 * row_bytes(H), x_dtype == GQ_F32, 0};
+  a.ph[1] = Phase{static_cast<const uint8_t*>(down), nullptr, static_cast<int>(I), static_cast<int>(H / 16),
+                  16 * row_bytes(I), y_dtype == GQ_F32, 0};
+  a.x = x;
   a.ids = ids;
-  a.dev_status = dev_status;
-  a.hmax = reinterpret_cast<unsigned*>(ws + l.hmax);
+  a.weights = weights;
+  a.y = y;
   a.h = reinterpret_cast<float*>(ws + l.h);
   a.out = reinterpret_cast<float*>(ws + l.out);
+  a.hmax = reinterpret_cast<unsigned*>(ws + l.hmax);
+  a.arrivals = reinterpret_cast<unsigned long long*>(ws + l.arrivals);
+  a.dev_status = dev_status;
+  a.budget = kWaitBudget;
   a.T = static_cast<int>(T);
   a.k = static_cast<int>(k);
   a.E = static_cast<int>(E);
-  const auto row_bytes = [](int64_t K) { return FMT == GQ_FMT_Q4_0 ? K / 32 * 18 : K / 256 * 138; };
-
-  a.w0 = static_cast<const uint8_t*>(gate);
-  a.w1 = static_cast<const uint8_t*>(up);
-  a.x = x;
+  a.H = static_cast<int>(H);
   a.xtype = x_dtype;
-  a.two = x_dtype == GQ_F32;
-  a.K = static_cast<int>(H);
-  a.groups = static_cast<int>(I / 16);
-  a.group_bytes = 16 * row_bytes(H);
-  gq_status st = launch_moe<FMT, true>(a, (flags & GQ_GEMV_PDL) != 0, s);
-  if (st != GQ_OK) return st;
-
-  a.w0 = static_cast<const uint8_t*>(down);
-  a.w1 = nullptr;
-  a.x = a.h;
-  a.xtype = GQ_F32;
-  a.two = y_dtype == GQ_F32;
-  a.K = static_cast<int>(I);
-  a.groups = static_cast<int>(H / 16);
-  a.group_bytes = 16 * row_bytes(I);
-  st = launch_moe<FMT, false>(a, true, s);
-  if (st != GQ_OK) return st;
-
-  return launch(moe_sum_kernel, dim3(static_cast<unsigned>((T * H + 255) / 256)), dim3(256), 0, s, true,
-                a.out, ids, weights, a.hmax, y, a.T, a.k, a.E, static_cast<int>(H), y_dtype);
+  a.ytype = y_dtype;
+  return launch_moe<FMT>(a, (flags & GQ_GEMV_PDL) != 0, s);
 }
 
 }  // namespace
