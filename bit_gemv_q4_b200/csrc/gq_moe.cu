@@ -18,17 +18,18 @@
 //
 // Plan.  Every CTA reads the ids and builds the same plan in shared memory:
 // the (token, slot) pairs sorted by expert (stable), and segments of an expert
-// with at most `cap` of its pairs.  The work of all segments, 16 weight rows
-// at a time, is cut into even runs, one for each CTA; a run's row groups form
-// one string of stages (8 blocks of 32 weights x 16 rows, 2.3 KB), which its 16
-// warps share evenly, so that the split is even whatever the sizes are.  Each
-// warp copies its own stages to its own ring in shared memory (cp.async), a
-// few ahead: tiled storage is ordered by the lanes that multiply it, so the
-// copies are whole lines and a lane reads back its own codes, and warps wait
-// for nothing but their own copies.  (Reading units straight into registers,
-// eight ahead, ran at 1.5 TB/s: loads that share a scoreboard are waited for
-// together.)  Sums of a row group that several warps share meet in a shared
-// table and are added in warp order: results do not depend on scheduling.
+// with at most `cap` of its pairs.  The work of all segments, one item for 16
+// weight rows (of gate and of up, or of down), is cut into even runs, one for
+// each CTA.  A run is a string of stages (8 blocks of 32 weights x 16 rows, 2.3
+// KB) that its 24 warps share evenly, so that the split is even whatever the
+// sizes are.  Each warp copies its own stages to its own ring in shared memory
+// (cp.async), a few ahead: tiled storage is ordered by the lanes that multiply
+// it, so the copies are whole lines and a lane reads back its own codes, and
+// warps wait for nothing but their own copies.  (Reading units straight into
+// registers, eight ahead, ran at 1.5 TB/s: loads that share a scoreboard are
+// waited for together.)  A warp finishes the items that it has all of in its
+// registers; the parts of an item that several warps share meet in a table and
+// are added in warp order: results do not depend on scheduling.
 //
 // Arithmetic.  Codes become the fp16 values code - 8, exactly: the nibble goes
 // to the low mantissa bits of 1024, from which 1032 is subtracted, or stays in
@@ -56,7 +57,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxT = 64, kMaxTopK = 16, kMaxE = 1024;
 constexpr int kMaxPairs = kMaxT * kMaxTopK;
 constexpr int kMaxK = 16384;
-constexpr int kMaxCols = 16;                // columns of a segment: two n8 tiles
+constexpr int kMaxCols = 8;   // columns of a segment: the MMA's n
+constexpr int kMaxSegs = 16;  // segments of a string
 constexpr size_t kSmemBudget = 227 * 1024;
 
 // A stage: 8 blocks of 32 weights x 16 rows, what a warp copies at a time.  At
@@ -74,7 +76,8 @@ struct Phase {
   int groups;               // row groups (16 rows) of one expert
   int64_t group_bytes;
   int two;                  // two columns for each token
-  int cap;                  // tokens of a segment at most
+  int cap;                  // tokens of a segment at most, a power of two
+  int part;                 // floats of a part in the table
 };
 
 struct MoeArgs {
@@ -91,8 +94,7 @@ struct MoeArgs {
   long long budget;
   int T, k, E, H;
   int xtype, ytype;
-  int tabslots;             // parts that one table holds
-  int tabfloats;            // floats of one table
+  int bbytes;               // room for B fragments
   uint32_t b_off, tab_off, plan_off;  // dynamic shared memory, after the rings
 };
 
@@ -103,15 +105,15 @@ struct Seg {
 
 struct Plan {
   int nseg[2];
-  int go;                   // the grid barrier was passed
-  float inv[2][kMaxCols];   // 1 / scale of a segment's tokens
-  unsigned xmax[kMaxT];     // largest |x| of a token as bits
-  unsigned hmax[kMaxCols];  // of a string's tokens
+  int go;                              // the grid barrier was passed
+  unsigned xmax[kMaxT];                // largest |x| of a token as bits
+  // of a string's segments
+  int boff[kMaxSegs];                  // their B fragments
+  float inv[kMaxSegs][kMaxCols];       // 1 / scale of their tokens
+  unsigned hmax[kMaxSegs][kMaxCols];   // largest |h|
   // in dynamic shared memory
-  Seg* seg[2];              // [pairs] of each phase
-  short* order;             // [pairs] slot -> pair
-  short* first;             // [E] pairs of an expert, then its first slot
-  short* rank;              // [pairs] only while planning (in the rings' place)
+  Seg* seg[2];                         // [pairs] of each phase
+  short* order;                        // [pairs] slot -> pair
 };
 
 extern __shared__ __align__(1024) uint8_t msm[];
@@ -149,81 +151,73 @@ __device__ __forceinline__ void load8(const void* base, int64_t i, int type, flo
   }
 }
 
-// Pairs sorted by expert (stable), and the segments of both phases (warp 0);
-// the tokens' largest |x| (the other warps).  ids outside [0, E) are left out.
+// Pairs sorted by expert (stable), the segments of both phases, and the tokens'
+// largest |x|.  ids outside [0, E) are left out.  A pair's slot is the number of
+// pairs that go before it, counted by a thread of its own.
 __device__ void make_plan(Plan& pl, const MoeArgs& a) {
-  const int P = a.T * a.k;
+  const int P = a.T * a.k, P4 = (P + 3) & ~3;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) pl.first[e] = 0;
-  if (threadIdx.x < kMaxT) pl.xmax[threadIdx.x] = 0u;
-  const int id0 = warp == 0 && lane < P ? __ldcg(a.ids + lane) : -1;
-  __syncthreads();
-  if (warp == 0) {
-    // rank of each pair among its expert's, 32 pairs at a time
-    for (int p0 = 0; p0 < P; p0 += 32) {
-      const int p = p0 + lane;
-      const int id = p0 == 0 ? id0 : p < P ? __ldcg(a.ids + p) : -1;
-      const bool ok = id >= 0 && id < a.E;
-      if (blockIdx.x == 0 && (id < -1 || id >= a.E)) report(a.dev_status, GQ_DEV_RANGE);
-      const unsigned peers = __match_any_sync(0xFFFFFFFFu, ok ? id : -1 - lane);
-      const int before = __popc(peers & ((1u << lane) - 1u));
-      const int base = ok ? pl.first[id] : 0;
-      __syncwarp();
-      if (ok && before == 0) pl.first[id] = static_cast<short>(base + __popc(peers));
-      if (p < P) pl.rank[p] = static_cast<short>(ok ? base + before : -1);
-      __syncwarp();
+  int* ids = reinterpret_cast<int*>(msm);  // in the rings' place
+  short* rank = reinterpret_cast<short*>(ids + kMaxPairs);  // by slot: place among its expert's,
+  short* count = rank + kMaxPairs;                          // how many these are,
+  short* expert = count + kMaxPairs;                        // and the expert
+  for (int p = threadIdx.x; p < P4; p += kThreads) {
+    const int id = p < P ? __ldcg(a.ids + p) : -1;
+    if (blockIdx.x == 0 && (id < -1 || id >= a.E)) report(a.dev_status, GQ_DEV_RANGE);
+    ids[p] = id >= 0 && id < a.E ? id : 0x7FFFFFFF;
+  }
+  const int share = max(1, kWarps / a.T), vecs = a.H / 8;  // warps for each token
+  for (int i = warp; i < a.T * share; i += kWarps) {
+    const int t = i / share;
+    unsigned m = 0;
+#pragma unroll 2
+    for (int r = (i - t * share) * 32 + lane; r < vecs; r += 32 * share) {
+      float v[8];
+      load8(a.x, static_cast<int64_t>(t) * a.H + 8 * r, a.xtype, v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(v[q]) & 0x7FFFFFFFu);
     }
-    // counts -> first slots, and segments, in the order of the experts
-    int slots = 0, segs[2] = {0, 0};
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int n = e < a.E ? pl.first[e] : 0;
-      if (!__any_sync(0xFFFFFFFFu, n)) continue;
-      int sn = n;  // inclusive sums over the lanes
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xFFFFFFFFu, sn, o);
-        if (lane >= o) sn += u;
-      }
-      const int first = slots + sn - n;
-      if (e < a.E) pl.first[e] = static_cast<short>(first);
-      slots += __shfl_sync(0xFFFFFFFFu, sn, 31);
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int cap = a.ph[f].cap, ns = (n + cap - 1) / cap;
-        int ss = ns;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int u = __shfl_up_sync(0xFFFFFFFFu, ss, o);
-          if (lane >= o) ss += u;
-        }
-        for (int i = 0; i < ns; ++i)
-          pl.seg[f][segs[f] + ss - ns + i] =
-              Seg{static_cast<short>(e), static_cast<short>(first + i * cap), min(cap, n - i * cap)};
-        segs[f] += __shfl_sync(0xFFFFFFFFu, ss, 31);
-      }
-    }
-    if (lane < 2) pl.nseg[lane] = lane ? segs[1] : segs[0];
-  } else {
-    const int share = max(1, (kWarps - 1) / a.T), vecs = a.H / 8;  // warps for each token
-    for (int i = warp - 1; i < a.T * share; i += kWarps - 1) {
-      const int t = i / share;
-      unsigned m = 0;
-#pragma unroll 4
-      for (int r = (i - t * share) * 32 + lane; r < vecs; r += 32 * share) {
-        float v[8];
-        load8(a.x, static_cast<int64_t>(t) * a.H + 8 * r, a.xtype, v);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(v[q]) & 0x7FFFFFFFu);
-      }
-      m = __reduce_max_sync(0xFFFFFFFFu, m);
-      if (lane == 0) atomicMax(&pl.xmax[t], m);
-    }
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (lane == 0) atomicMax(&pl.xmax[t], m);
   }
   __syncthreads();
-  for (int p = threadIdx.x; p < P; p += kThreads) {
-    const int r = pl.rank[p];
-    if (r >= 0) pl.order[pl.first[__ldcg(a.ids + p)] + r] = static_cast<short>(p);
+  int slots = 0;
+  for (int p0 = 0; p0 < P; p0 += kThreads) {
+    const int p = p0 + threadIdx.x;
+    const int id = p < P ? ids[p] : 0x7FFFFFFF;
+    const bool ok = id != 0x7FFFFFFF;
+    if (ok) {
+      int less = 0, same = 0, before = 0;
+      for (int q = 0; q < P4; q += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(ids + q);
+        less += (v.x < id) + (v.y < id) + (v.z < id) + (v.w < id);
+        const int eq = (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
+        same += eq;
+        if (q + 3 < p) before += eq;
+        else if (q <= p) before += (v.x == id && q < p) + (v.y == id && q + 1 < p) + (v.z == id && q + 2 < p);
+      }
+      const int slot = less + before;
+      pl.order[slot] = static_cast<short>(p);
+      rank[slot] = static_cast<short>(before);
+      count[slot] = static_cast<short>(same);
+      expert[slot] = static_cast<short>(id);
+    }
+    slots += __syncthreads_count(ok);
+  }
+  if (warp < 2) {  // a segment begins at every cap-th pair of an expert
+    const int cap = a.ph[warp].cap;  // a power of two
+    Seg* seg = pl.seg[warp];
+    int n = 0;
+    for (int s0 = 0; s0 < slots; s0 += 32) {
+      const int s = s0 + lane;
+      const bool begins = s < slots && (rank[s] & (cap - 1)) == 0;
+      const unsigned b = __ballot_sync(0xFFFFFFFFu, begins);
+      if (begins)
+        seg[n + __popc(b & ((1u << lane) - 1u))] =
+            Seg{expert[s], static_cast<short>(s), min(cap, count[s] - rank[s])};
+      n += __popc(b);
+    }
+    if (lane == 0) pl.nseg[warp] = n;
   }
   __syncthreads();
 }
@@ -240,22 +234,26 @@ __device__ __forceinline__ float scale_of(unsigned maxbits) {
 // Columns that the B fragments of a segment have room for: a power of two, so
 // that every offset in the inner loop is a constant.
 __device__ __forceinline__ int col_pitch(int ncol) {
-  return ncol <= 2 ? ncol : ncol <= 4 ? 4 : ncol <= 8 ? 8 : 16;
+  return ncol <= 2 ? ncol : ncol <= 4 ? 4 : 8;
 }
 
-// B fragments of a segment's tokens.  Column c of block b and lane group t: 16
-// bytes at ((b * pitch + c) * 4 + t) * 16, the values 4t, 4t+2, 4t+1, 4t+3 of the
-// block and the same at +16.
+// B fragments of a segment's tokens at shared offset b_off.  Column c of block b
+// and lane group t: 16 bytes at ((b * pitch + c) * 4 + t) * 16, the values 4t,
+// 4t+2, 4t+1, 4t+3 of the block and the same at +16.
 template <bool GATE_UP>
-__device__ void load_b(const MoeArgs& a, const Phase& ph, Plan& pl, const Seg& sg, int buf) {
+__device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& pl, const Seg& sg, int local,
+                                       int b_off) {
   const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
   const int vecs = ph.K / 8;
   auto row_of = [&](int c) { return GATE_UP ? pl.order[sg.slot0 + c] / a.k : sg.slot0 + c; };
   auto max_of = [&](int c) { return GATE_UP ? pl.xmax[row_of(c)] : __ldcg(a.hmax + sg.slot0 + c); };
   const int type = GATE_UP ? a.xtype : GQ_F32;
   const void* src = GATE_UP ? a.x : a.h;
-  if (threadIdx.x < sg.n)  // scale_of() is a power of two: the reciprocal is exact
-    pl.inv[buf][threadIdx.x] = 1.0f / scale_of(max_of(threadIdx.x));
+  if (threadIdx.x < sg.n) {  // scale_of() is a power of two: the reciprocal is exact
+    pl.inv[local][threadIdx.x] = 1.0f / scale_of(max_of(threadIdx.x));
+    pl.hmax[local][threadIdx.x] = 0u;
+  }
+  if (threadIdx.x == 0) pl.boff[local] = b_off;
   const int nvec = sg.n * vecs;
   for (int i = threadIdx.x; i < nvec; i += kThreads) {
     const int c = i / vecs, r = i - c * vecs;
@@ -273,7 +271,7 @@ __device__ void load_b(const MoeArgs& a, const Phase& ph, Plan& pl, const Seg& s
         hv[j] = __float2half_rn(f);
         v[j] = f - __half2float(hv[j]);
       }
-      uint8_t* d = msm + a.b_off + (static_cast<uint32_t>(b * pitch + col + part) * 4 + t0) * 16 + (q >> 1) * 8;
+      uint8_t* d = msm + b_off + (static_cast<uint32_t>(b * pitch + col + part) * 4 + t0) * 16 + (q >> 1) * 8;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const __half2 lo = __halves2half2(hv[4 * u], hv[4 * u + 2]);
@@ -283,7 +281,6 @@ __device__ void load_b(const MoeArgs& a, const Phase& ph, Plan& pl, const Seg& s
       }
     }
   }
-  __syncthreads();
 }
 
 // ------------------------------------------------------------------ stages
@@ -312,30 +309,25 @@ __device__ __forceinline__ uint32_t high_codes(uint32_t w) {
 }
 
 // acc += one block of 32 weights: wa, wb this lane's code words of rows g and
-// g+8, da, db the rows' scales, xb this lane's B fragment of column tile 0.
-// With one column a lane keeps one sum for each row.
+// g+8, da, db the rows' scales, xb this lane's B fragment.  With one column a
+// lane keeps one sum for each row.
 template <int CP>
-__device__ __forceinline__ void block_math(uint32_t wa, uint32_t wb, float da, float db, float (*acc)[4],
+__device__ __forceinline__ void block_math(uint32_t wa, uint32_t wb, float da, float db, float acc[4],
                                            const uint8_t* xb) {
   const uint32_t wa8 = wa >> 8, wb8 = wb >> 8;
-  const uint32_t l0 = low_codes(wa), l1 = low_codes(wb), l2 = low_codes(wa8), l3 = low_codes(wb8);
-  const uint32_t h0 = high_codes(wa), h1 = high_codes(wb), h2 = high_codes(wa8), h3 = high_codes(wb8);
-#pragma unroll
-  for (int j = 0; j < (CP + 7) / 8; ++j) {
-    const uint4 xv = ld128(xb + 512 * j);
-    float c[4];
-    mma_f16_z(c, l0, l1, l2, l3, xv.x, xv.y);
-    mma_f16(c, h0, h1, h2, h3, xv.z, xv.w);
-    acc[j][0] = fmaf(da, c[0], acc[j][0]);
-    if (CP > 1) acc[j][1] = fmaf(da, c[1], acc[j][1]);
-    acc[j][2] = fmaf(db, c[2], acc[j][2]);
-    if (CP > 1) acc[j][3] = fmaf(db, c[3], acc[j][3]);
-  }
+  const uint4 xv = ld128(xb);
+  float c[4];
+  mma_f16_z(c, low_codes(wa), low_codes(wb), low_codes(wa8), low_codes(wb8), xv.x, xv.y);
+  mma_f16(c, high_codes(wa), high_codes(wb), high_codes(wa8), high_codes(wb8), xv.z, xv.w);
+  acc[0] = fmaf(da, c[0], acc[0]);
+  if (CP > 1) acc[1] = fmaf(da, c[1], acc[1]);
+  acc[2] = fmaf(db, c[2], acc[2]);
+  if (CP > 1) acc[3] = fmaf(db, c[3], acc[3]);
 }
 
 // A stage from its ring slot: n units of two blocks (Q4_0) or one super-block.
 template <int FMT, int CP, bool FULL>
-__device__ __forceinline__ void stage_math(const uint8_t* st, int n, int lane, float (*acc)[4],
+__device__ __forceinline__ void stage_math(const uint8_t* st, int n, int lane, float acc[4],
                                            const uint8_t* xb) {
   const uint8_t* code = st + (FMT == GQ_FMT_Q4_0 ? 16 : 32) * lane;
   const uint8_t* sc = st + kStageCodes + 4 * (lane >> 2);
@@ -367,45 +359,46 @@ __device__ __forceinline__ void stage_math(const uint8_t* st, int n, int lane, f
   }
 }
 
-// A string of row groups [i0, i0 + n) of one expert (gate and up: row group i
-// is one of gate's, then the same of up's).
-template <bool GATE_UP>
-__device__ __forceinline__ const uint8_t* group_at(const Phase& a, int e, int i) {
-  const uint8_t* w = (GATE_UP && (i & 1)) ? a.w1 : a.w0;
-  const int g = GATE_UP ? i >> 1 : i;
-  return w + (static_cast<int64_t>(e) * a.groups + g) * a.group_bytes;
-}
+// Items [ra, rb) of all segments' (item r is row group r % groups of segment r /
+// groups) whose B fragments are in shared memory together.
+struct String {
+  int ra, rb, seg0, segs;
+};
 
-// A warp's next copy: stage k of row group q of the string, `left` stages in
-// all; this lane's sources in it.
+// A warp's next copy: stage k of row group g of segment s (gate's stages, then
+// up's), `left` stages in all; this lane's sources in it.
 template <int FMT, bool GATE_UP>
 struct Feed {
   const uint8_t* code;
   const uint8_t* scale;
-  int e, q, k, left;
+  int s, g, k, left;
 
-  // Sources of stage k of a row group.
-  __device__ __forceinline__ void seek(const Phase& a, int i0, int lane) {
-    const uint8_t* group = group_at<GATE_UP>(a, e, i0 + q);
-    const int c = k >> 3, j = k & 7;
+  __device__ __forceinline__ void seek(const Phase& ph, const Plan& pl, int stages, int lane) {
+    const bool up = GATE_UP && k >= stages;
+    const int kk = up ? k - stages : k;
+    const uint8_t* group = (up ? ph.w1 : ph.w0) +
+                           (static_cast<int64_t>(pl.seg[!GATE_UP][s].e) * ph.groups + g) * ph.group_bytes;
+    const int c = kk >> 3, j = kk & 7;
     if constexpr (FMT == GQ_FMT_Q4_0) {
       // tiles of 32 units (512 bytes of codes, 64 of scales); a stage is four
-      const int nu = min(32, (a.K >> 6) - 32 * c);
+      const int nu = min(32, (ph.K >> 6) - 32 * c);
       const uint8_t* tile = group + static_cast<int64_t>(c) * 18432;
       code = tile + 2048 * j + 16 * lane;
       scale = tile + 512 * nu + 256 * j + 16 * lane;
     } else {
       // tiles of 8 super-blocks (2048 bytes of codes, 128 of sub-scales, 32 of S); a stage is one
-      const int ns = min(8, (a.K >> 8) - 8 * c);
+      const int ns = min(8, (ph.K >> 8) - 8 * c);
       const uint8_t* tile = group + static_cast<int64_t>(c) * 17664;
       code = tile + 2048 * j + 16 * lane;
       scale = lane < 8 ? tile + 2048 * ns + 128 * j + 16 * lane : tile + 2176 * ns + 32 * j + 16 * (lane - 8);
     }
   }
-  __device__ __forceinline__ void step(const Phase& a, int i0, int stages, uint32_t dst, int lane) {
+  __device__ __forceinline__ void step(const Phase& ph, const Plan& pl, int stages, uint32_t dst, int lane) {
     if (left > 0) {
       dst += 16 * lane;
-      const int n = FMT == GQ_FMT_Q4_0 && k == stages - 1 ? (a.K >> 6) - 4 * k : 4;  // units
+      const int kk = GATE_UP && k >= stages ? k - stages : k;
+      const bool end = kk == stages - 1;
+      const int n = FMT == GQ_FMT_Q4_0 && end ? (ph.K >> 6) - 4 * kk : 4;  // units
       if (n == 4) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) copy16(dst + 512 * i, code + 512 * i);
@@ -415,12 +408,15 @@ struct Feed {
       if (lane < (FMT == GQ_FMT_Q4_0 ? 4 * n : 10)) copy16(dst + kStageCodes, scale);
       --left;
       ++k;
-      if (k == stages || (k & 7) == 0) {  // another tile
-        if (k == stages) {
+      if (end || ((kk + 1) & 7) == 0) {  // another tile
+        if (k == (GATE_UP ? 2 * stages : stages)) {
           k = 0;
-          ++q;
+          if (++g == ph.groups) {
+            g = 0;
+            ++s;
+          }
         }
-        if (left > 0) seek(a, i0, lane);
+        if (left > 0) seek(ph, pl, stages, lane);
       } else {
         code += 2048;
         scale += FMT == GQ_FMT_Q4_0 ? 256 : (lane < 8 ? 128 : 32);
@@ -430,96 +426,79 @@ struct Feed {
   }
 };
 
-// This warp's stages [u, u1) of the string, the first kDepth of them under way:
-// partial sums to the table, part (row group + warp) for each row group that
-// the warp has stages of.
-template <int FMT, int CP, bool GATE_UP>
-__device__ __forceinline__ void stream(const Phase& a, uint32_t b_off, Feed<FMT, GATE_UP>& feed, int i0, int stages, int u,
-                                       int u1, uint32_t ring, float* tab) {
-  constexpr int NT = (CP + 7) / 8;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
-  // columns past the last repeat existing ones (or hold what was there); their sums are not used
-  const uint8_t* xb = msm + b_off + (g8 & (CP - 1)) * 64 + t * 16;
-  const uint32_t sbase = smem_addr(msm);
-  const int last_n = FMT == GQ_FMT_Q4_0 ? (a.K >> 6) - 4 * (stages - 1) : 4;  // units of a row's last stage
-  float acc[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-  int q = u / stages, k = u - q * stages;
-  uint32_t st = ring;
-  const uint8_t* x = xb + k * (8 * 64 * CP);
-  for (; u < u1; ++u) {
-    copies_wait<kDepth - 1>();
-    __syncwarp();  // every lane's copies of the stage
-    const bool end = ++k == stages;
-    if (FMT == GQ_FMT_KSB || !end || last_n == 4)
-      stage_math<FMT, CP, true>(msm + st, 4, lane, acc, x);
-    else
-      stage_math<FMT, CP, false>(msm + st, last_n, lane, acc, x);
-    x += 8 * 64 * CP;
-    __syncwarp();  // every lane has read the stage
-    feed.step(a, i0, stages, sbase + st, lane);
-    st = st == ring + (kDepth - 1) * kStageBytes ? ring : st + kStageBytes;
-    if (end || u + 1 == u1) {
-      float* d = tab + (q + warp) * (16 * CP);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int c = 8 * j + 2 * t;
-        if (CP == 1) {
-          if (t == 0) {
-            d[g8] = acc[j][0];
-            d[g8 + 8] = acc[j][2];
-          }
-        } else if (c < CP) {
-          *reinterpret_cast<float2*>(d + g8 * CP + c) = make_float2(acc[j][0], acc[j][1]);
-          *reinterpret_cast<float2*>(d + (g8 + 8) * CP + c) = make_float2(acc[j][2], acc[j][3]);
-        }
-        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-      }
-      k = 0;
-      ++q;
-      x = xb;
+// The parts of items that warps share: two for each warp, of both matrices for
+// gate and up.  Part 0 belongs to an item that an earlier warp began, part 1 to
+// one that this warp began and a later one ends.
+__device__ __forceinline__ float* part_at(const MoeArgs& a, const Phase& ph, int warp, int which) {
+  return reinterpret_cast<float*>(msm + a.tab_off) + (2 * warp + which) * ph.part;
+}
+template <int CP>
+__device__ __forceinline__ void store_part(float* d, const float acc[4], int lane) {
+  const int g8 = lane >> 2, t = lane & 3;
+  if (CP == 1) {
+    if (t == 0) {
+      d[g8] = acc[0];
+      d[g8 + 8] = acc[2];
     }
+  } else if (2 * t < CP) {
+    *reinterpret_cast<float2*>(d + g8 * CP + 2 * t) = make_float2(acc[0], acc[1]);
+    *reinterpret_cast<float2*>(d + (g8 + 8) * CP + 2 * t) = make_float2(acc[2], acc[3]);
   }
 }
 
-// The run of this CTA: row groups (pairs of them for gate and up) [r0, r1) of
-// all segments', cut into strings of one segment that the table holds.
-struct String {
-  int seg, i0, n;  // segment, first row group (of the string's kind), how many
-};
+// Token c's row of a finished item: h (whose size it returns, as bits), or the
+// pair's output.
+template <bool GATE_UP>
+__device__ __forceinline__ unsigned put(const MoeArgs& a, const Phase& ph, const Plan& pl, const Seg& sg, int c,
+                                        int row, float v, float up) {
+  if constexpr (GATE_UP) {
+    const float h = v / (1.0f + expf(-v)) * up;
+    __stcg(a.h + static_cast<int64_t>(sg.slot0 + c) * (ph.groups * 16) + row, h);
+    return __float_as_uint(h) & 0x7FFFFFFFu;
+  } else {
+    __stcg(a.out + static_cast<int64_t>(pl.order[sg.slot0 + c]) * (ph.groups * 16) + row, v);
+    return 0u;
+  }
+}
+
 template <int FMT, bool GATE_UP>
 struct Work {
-  int r, r1;    // row groups left (pairs of them for gate and up)
-  int stages;   // of a row group
+  int r, r1;      // items left to this CTA
+  int stages;     // of a row group of one matrix
   bool more;
   String st;
+  int u0, u1;     // this warp's stages of the string
   Feed<FMT, GATE_UP> feed;
 
-  __device__ __forceinline__ void next(const Phase& ph, int most) {
+  __device__ __forceinline__ int item_stages() const { return GATE_UP ? 2 * stages : stages; }
+
+  // The next string, and the first copies of this warp's share of it.
+  __device__ __forceinline__ void next(const MoeArgs& a, const Phase& ph, const Plan& pl, uint32_t ring) {
     more = r < r1;
     if (!more) return;
-    st.seg = r / ph.groups;
-    const int g = r - st.seg * ph.groups;
-    const int left = min(r1 - r, ph.groups - g);
-    const int strings = (left + most - 1) / most;
-    const int n = (left + strings - 1) / strings;  // even strings
-    st.i0 = GATE_UP ? 2 * g : g;
-    st.n = GATE_UP ? 2 * n : n;
-    r += n;
-  }
-  // The first copies of this warp's share of the string.
-  __device__ __forceinline__ void fetch(const Phase& ph, const Plan& pl, uint32_t ring) {
-    if (!more) return;
+    st.ra = r;
+    st.seg0 = r / ph.groups;
+    st.segs = 0;
+    int bytes = 0;
+    while (r < r1 && st.segs < kMaxSegs) {
+      const int s = st.seg0 + st.segs;
+      bytes += col_pitch(ph.two ? 2 * pl.seg[!GATE_UP][s].n : pl.seg[!GATE_UP][s].n) * ph.K * 2;
+      if (bytes > a.bbytes && st.segs) break;  // (one segment always fits)
+      r = min(r1, (s + 1) * ph.groups);
+      ++st.segs;
+    }
+    st.rb = r;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tu = st.n * stages;
-    const int u0 = tu * warp / kWarps;
-    feed.e = pl.seg[!GATE_UP][st.seg].e;
-    feed.q = u0 / stages;
-    feed.k = u0 - feed.q * stages;
-    feed.left = tu * (warp + 1) / kWarps - u0;
-    if (feed.left > 0) feed.seek(ph, st.i0, lane);
-    for (int i = 0; i < kDepth; ++i) feed.step(ph, st.i0, stages, smem_addr(msm) + ring + i * kStageBytes, lane);
+    const int tu = (st.rb - st.ra) * item_stages();
+    u0 = tu * warp / kWarps;
+    u1 = tu * (warp + 1) / kWarps;
+    const int i = st.ra + u0 / item_stages();
+    feed.k = u0 % item_stages();
+    feed.s = i / ph.groups;
+    feed.g = i - feed.s * ph.groups;
+    feed.left = u1 - u0;
+    if (feed.left > 0) feed.seek(ph, pl, stages, lane);
+    for (int d = 0; d < kDepth; ++d) feed.step(ph, pl, stages, smem_addr(msm) + ring + d * kStageBytes, lane);
   }
   __device__ __forceinline__ void start(const MoeArgs& a, const Plan& pl, uint32_t ring) {
     const Phase& ph = a.ph[!GATE_UP];
@@ -527,78 +506,178 @@ struct Work {
     r = static_cast<int>(total * blockIdx.x / gridDim.x);
     r1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
     stages = FMT == GQ_FMT_Q4_0 ? (ph.K + 255) / 256 : ph.K / 256;
-    next(ph, (a.tabslots - kWarps) / (GATE_UP ? 2 : 1));
-    fetch(ph, pl, ring);
+    next(a, ph, pl, ring);
   }
 };
 
-// All strings of a phase.
-template <int FMT, bool GATE_UP>
-__device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, GATE_UP>& wk, uint32_t ring) {
+// This warp's stages [u, ue) of the string, all of one segment, from stage k of
+// row group g on; the copies are under way.  `whole`: the warp has its item from
+// the first stage on.
+template <int FMT, int CP, bool GATE_UP>
+__device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& pl, Work<FMT, GATE_UP>& wk,
+                                       const Seg& sg, int local, int u, int ue, int g, int k, bool& whole,
+                                       uint32_t ring, uint32_t& st) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
+  // columns past the last repeat existing ones (or hold what was there); their sums are not used
+  const uint8_t* xb = msm + pl.boff[local] + (g8 & (CP - 1)) * 64 + t * 16;
+  const uint32_t sbase = smem_addr(msm);
+  const int stages = wk.stages, all = wk.item_stages();
+  const int last_n = FMT == GQ_FMT_Q4_0 ? (ph.K >> 6) - 4 * (stages - 1) : 4;  // units of a row's last stage
+  float acc[4] = {}, gate[4] = {};
+  unsigned top[2] = {0u, 0u};  // largest |h| of this lane's tokens
+  int kk = GATE_UP && k >= stages ? k - stages : k;
+  const uint8_t* x = xb + kk * (8 * 64 * CP);
+  for (; u < ue; ++u) {
+    copies_wait<kDepth - 1>();
+    __syncwarp();  // every lane's copies of the stage
+    ++k;
+    const bool end = ++kk == stages;
+    if (FMT == GQ_FMT_KSB || !end || last_n == 4)
+      stage_math<FMT, CP, true>(msm + st, 4, lane, acc, x);
+    else
+      stage_math<FMT, CP, false>(msm + st, last_n, lane, acc, x);
+    x += 8 * 64 * CP;
+    __syncwarp();  // every lane has read the stage
+    wk.feed.step(ph, pl, stages, sbase + st, lane);
+    st = st == ring + (kDepth - 1) * kStageBytes ? ring : st + kStageBytes;
+    if (!end) continue;
+    kk = 0;
+    x = xb;
+    if (GATE_UP && k == stages) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        gate[i] = acc[i];
+        acc[i] = 0.f;
+      }
+      continue;
+    }
+    if (whole) {
+      // columns 2t and 2t+1, rows g8 and g8 + 8: two tokens, or one in two columns
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = ph.two ? t : 2 * t + i;
+        if (c < sg.n && !(ph.two && i)) {
+          const float f = pl.inv[local][c];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float v = ph.two ? acc[2 * half] + acc[2 * half + 1] : acc[2 * half + i];
+            const float w = ph.two ? gate[2 * half] + gate[2 * half + 1] : gate[2 * half + i];
+            const unsigned m = put<GATE_UP>(a, ph, pl, sg, c, 16 * g + g8 + 8 * half, (GATE_UP ? w : v) * f, v * f);
+            top[i] = max(top[i], m);
+          }
+        }
+      }
+    } else {
+      float* d = part_at(a, ph, warp, 0);
+      if (GATE_UP) store_part<CP>(d, gate, lane);
+      store_part<CP>(d + (GATE_UP ? 16 * CP : 0), acc, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = gate[i] = 0.f;
+    whole = true;
+    k = 0;
+    ++g;
+  }
+  if (k > 0 && k < all && u == wk.u1 && wk.u1 > wk.u0) {  // the run ends inside an item
+    float* d = part_at(a, ph, warp, whole);
+    if (GATE_UP) {
+      store_part<CP>(d, k < stages ? acc : gate, lane);
+      if (k < stages) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = 0.f;
+      }
+    }
+    store_part<CP>(d + (GATE_UP ? 16 * CP : 0), acc, lane);
+  }
+  if (GATE_UP) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // over the lanes of a token
+      unsigned m = top[i];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      const int c = ph.two ? t : 2 * t + i;
+      if (g8 == 0 && c < sg.n && !(ph.two && i) && m) atomicMax(&pl.hmax[local][c], m);
+    }
+  }
+}
+
+// All strings of a phase; after(): called once this warp has no more copies to
+// issue for it.
+template <int FMT, bool GATE_UP, class After>
+__device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, GATE_UP>& wk, uint32_t ring,
+                                          After after) {
   const Phase& ph = a.ph[!GATE_UP];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stages = wk.stages;
-  int buf = 0, loaded = -1;
+  const int all = wk.item_stages();
+  if (!wk.more) after();
   while (wk.more) {
     const String st = wk.st;
-    const Seg sg = pl.seg[!GATE_UP][st.seg];
-    const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
-    if (loaded != st.seg) {
-      load_b<GATE_UP>(a, ph, pl, sg, st.seg & 1);
-      loaded = st.seg;
+    const int u0 = wk.u0, u1 = wk.u1, tu = (st.rb - st.ra) * all;
+    int b_off = a.b_off;
+    for (int i = 0; i < st.segs; ++i) {
+      const Seg sg = pl.seg[!GATE_UP][st.seg0 + i];
+      load_b<GATE_UP>(a, ph, pl, sg, i, b_off);
+      b_off += col_pitch(ph.two ? 2 * sg.n : sg.n) * ph.K * 2;
     }
-    float* tab = reinterpret_cast<float*>(msm + a.tab_off) + buf * a.tabfloats;
-    const int tu = st.n * stages;
-    const int u0 = tu * warp / kWarps, u1 = tu * (warp + 1) / kWarps;
-    switch (pitch) {
-      case 1: stream<FMT, 1, GATE_UP>(ph, a.b_off, wk.feed, st.i0, stages, u0, u1, ring, tab); break;
-      case 2: stream<FMT, 2, GATE_UP>(ph, a.b_off, wk.feed, st.i0, stages, u0, u1, ring, tab); break;
-      case 4: stream<FMT, 4, GATE_UP>(ph, a.b_off, wk.feed, st.i0, stages, u0, u1, ring, tab); break;
-      case 8: stream<FMT, 8, GATE_UP>(ph, a.b_off, wk.feed, st.i0, stages, u0, u1, ring, tab); break;
-      default: stream<FMT, 16, GATE_UP>(ph, a.b_off, wk.feed, st.i0, stages, u0, u1, ring, tab);
+    __syncthreads();
+    const int i0 = st.ra + u0 / all, k0 = u0 % all;
+    bool whole = k0 == 0;
+    uint32_t slot = ring;
+    int u = u0, r = i0, k = k0;
+    while (u < u1) {
+      const int s = r / ph.groups, local = s - st.seg0;
+      const Seg sg = pl.seg[!GATE_UP][s];
+      const int ue = min(u1, (min(st.rb, (s + 1) * ph.groups) - st.ra) * all);
+      const int g = r - s * ph.groups;
+      switch (col_pitch(ph.two ? 2 * sg.n : sg.n)) {
+        case 1: stream<FMT, 1, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, ring, slot); break;
+        case 2: stream<FMT, 2, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, ring, slot); break;
+        case 4: stream<FMT, 4, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, ring, slot); break;
+        default: stream<FMT, 8, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, ring, slot);
+      }
+      u = ue;
+      r = (s + 1) * ph.groups;
+      k = 0;
     }
-    wk.next(ph, (a.tabslots - kWarps) / (GATE_UP ? 2 : 1));
-    wk.fetch(ph, pl, ring);
-    if (GATE_UP && threadIdx.x < kMaxCols) pl.hmax[threadIdx.x] = 0u;
-    __syncthreads();  // the table is complete; B and the other table are free
-    // A warp takes two row groups (gate and up of the same rows, or two of
-    // down's), 16 lanes each, and adds their parts in warp order.
-    const float* inv = pl.inv[st.seg & 1];
-    const int row = lane & 15, half = lane >> 4;
-    for (int p = warp; p < (st.n + 1) / 2; p += kWarps) {
-      const int q = min(2 * p + half, st.n - 1);
-      const int lo = q * stages, hi = lo + stages - 1;
-      const int w0 = (kWarps * (lo + 1) - 1) / tu, w1 = (kWarps * (hi + 1) - 1) / tu;
-      for (int c = 0; c < sg.n; ++c) {
-        const int col = ph.two ? 2 * c : c;
+    wk.next(a, ph, pl, ring);
+    if (!wk.more) after();
+    __syncthreads();  // the parts are there; nobody reads B any more
+    // An item that this warp began and did not end: the later warps' parts in order.
+    const int last = st.ra + (u1 - 1) / all;  // this warp's last item
+    const int begin = (last - st.ra) * all;
+    if (u1 > u0 && begin >= u0 && u1 < begin + all) {
+      const int s = last / ph.groups, local = s - st.seg0;
+      const Seg sg = pl.seg[!GATE_UP][s];
+      const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
+      const int row = lane & 15, half = lane >> 4;
+      // gate and up: each half of the warp one matrix; down: every other token
+      for (int c0 = 0; c0 < sg.n; c0 += GATE_UP ? 1 : 2) {
+        const int c = GATE_UP ? c0 : min(c0 + half, sg.n - 1);
+        const int at = ((GATE_UP ? half * 16 : 0) + row) * pitch + (ph.two ? 2 * c : c);
         float v = 0.f;
-        for (int w = w0; w <= w1; ++w) {
+        for (int w = warp; w < kWarps && tu * w / kWarps < begin + all; ++w) {
           if (tu * w / kWarps == tu * (w + 1) / kWarps) continue;  // no stages
-          const float* t = tab + ((q + w) * 16 + row) * pitch + col;
-          v += ph.two ? t[0] + t[1] : t[0];
+          const float* d = part_at(a, ph, w, w == warp) + at;
+          v += ph.two ? d[0] + d[1] : d[0];
         }
-        v *= inv[c];
-        if constexpr (GATE_UP) {
-          const float up = __shfl_down_sync(0xFFFFFFFFu, v, 16);
-          const float h = v / (1.0f + expf(-v)) * up;
-          unsigned m = 0;
-          if (half == 0) {
-            __stcg(a.h + static_cast<int64_t>(sg.slot0 + c) * (ph.groups * 16) + (st.i0 / 2 + p) * 16 + row, h);
-            m = __float_as_uint(h) & 0x7FFFFFFFu;
-          }
+        v *= pl.inv[local][c];
+        const float up = __shfl_down_sync(0xFFFFFFFFu, v, 16);
+        unsigned m = 0;
+        if (GATE_UP ? half == 0 : c0 + half < sg.n)
+          m = put<GATE_UP>(a, ph, pl, sg, c, 16 * (last - s * ph.groups) + row, v, up);
+        if (GATE_UP) {
           m = __reduce_max_sync(0xFFFFFFFFu, m);
-          if (lane == 0) atomicMax(&pl.hmax[c], m);
-        } else if (2 * p + half < st.n) {
-          const int pair = pl.order[sg.slot0 + c];
-          __stcg(a.out + static_cast<int64_t>(pair) * (ph.groups * 16) + (st.i0 + q) * 16 + row, v);
+          if (lane == 0) atomicMax(&pl.hmax[local][c], m);
         }
       }
     }
-    if (GATE_UP) {
-      __syncthreads();
-      if (threadIdx.x < sg.n) atomicMax(a.hmax + sg.slot0 + threadIdx.x, pl.hmax[threadIdx.x]);
+    __syncthreads();
+    if (GATE_UP && threadIdx.x < st.segs * kMaxCols) {
+      const int i = threadIdx.x / kMaxCols, c = threadIdx.x % kMaxCols;
+      const Seg sg = pl.seg[0][st.seg0 + i];
+      if (c < sg.n) atomicMax(a.hmax + sg.slot0 + c, pl.hmax[i][c]);
     }
-    buf ^= 1;
+    if (wk.more) __syncthreads();  // before the next string's values
   }
 }
 
@@ -637,22 +716,21 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     pl.seg[0] = reinterpret_cast<Seg*>(msm + a.plan_off);
     pl.seg[1] = pl.seg[0] + pairs;
     pl.order = reinterpret_cast<short*>(pl.seg[1] + pairs);
-    pl.first = pl.order + pairs;
-    pl.rank = reinterpret_cast<short*>(msm);
   }
+  if (threadIdx.x < kMaxT) pl.xmax[threadIdx.x] = 0u;
+  __syncthreads();
   pdl_wait();  // ids and x are final
   pdl_launch_dependents();
-  __syncthreads();
   make_plan(pl, a);
   const uint32_t ring = static_cast<uint32_t>((threadIdx.x >> 5) * kDepth * kStageBytes);
   Work<FMT, true> gate_up;
-  gate_up.start(a, pl, ring);
-  run_phase<FMT, true>(a, pl, gate_up, ring);
   Work<FMT, false> down;
-  down.start(a, pl, ring);  // the first copies are under way while this CTA waits
+  gate_up.start(a, pl, ring);
+  // down's first copies are under way while this CTA waits for the others
+  run_phase<FMT, true>(a, pl, gate_up, ring, [&] { down.start(a, pl, ring); });
   bool ok = grid_barrier(a, pl);
   if (ok) {
-    run_phase<FMT, false>(a, pl, down, ring);
+    run_phase<FMT, false>(a, pl, down, ring, [] {});
     ok = grid_barrier(a, pl);
   }
   if (!ok) {
@@ -699,39 +777,43 @@ bool moe_dims(int64_t T, int64_t k, int64_t E) {
 bool moe_width(int fmt, int64_t K) { return K % (fmt == GQ_FMT_Q4_0 ? 64 : 256) == 0 && K <= kMaxK; }
 
 // Tokens of a segment and the layout of shared memory after the rings: the B
-// fragments (2 bytes for each value of a column), two tables of parts, and the
-// plan.  A table holds at least a string of 16 row groups.
-constexpr int kMinSlots = kWarps + 16, kMaxSlots = kWarps + 64;
-static_assert(sizeof(Plan) <= 1024, "the static part, up to the dynamic one's alignment");
-constexpr size_t kDynSmem = kSmemBudget - 1024;
+// fragments (2 bytes for each value of a column), the table of parts, and the
+// plan.  Segments are as wide as both phases' columns and parts fit; what is
+// left takes more segments of a string.
+static_assert(sizeof(Plan) <= 2048, "the static part");
+constexpr size_t kDynSmem = kSmemBudget - 2048;
 size_t shape_smem(MoeArgs& a) {
   const int pairs = a.T * a.k;
-  const size_t plan = (static_cast<size_t>(pairs) * (2 * sizeof(Seg) + 2) + static_cast<size_t>(a.E) * 2 + 15) & ~size_t(15);
+  const size_t plan = (static_cast<size_t>(pairs) * (2 * sizeof(Seg) + 2) + 15) & ~size_t(15);
   const size_t left = kDynSmem - kRingBytes - plan;
-  const size_t part = 2 * 16 * sizeof(float);  // of both tables, for each column
-  size_t b = 0, cols = 2;
-  for (Phase& ph : a.ph) {
-    const size_t most = left / (static_cast<size_t>(ph.K) * 2 + kMinSlots * part);
+  size_t tab = 0, b = 0;
+  for (int f = 0; f < 2; ++f) {
+    Phase& ph = a.ph[f];
+    const size_t part = 2 * kWarps * (f == 0 ? 2 : 1) * 16 * sizeof(float);  // for each column
     const size_t need = static_cast<size_t>(pairs) * (ph.two ? 2 : 1);
-    size_t c = 2;  // powers of two
-    while (c < kMaxCols && 2 * c <= most && c < need) c *= 2;
+    size_t c = ph.two ? 2 : 1;  // powers of two
+    while (c < kMaxCols && c < need && 2 * c * (static_cast<size_t>(ph.K) * 2 + part) <= left) c *= 2;
     ph.cap = static_cast<int>(ph.two ? c / 2 : c);
+    tab = c * part > tab ? c * part : tab;
     b = c * ph.K * 2 > b ? c * ph.K * 2 : b;
-    cols = c > cols ? c : cols;
   }
-  // each phase alone leaves room for kMinSlots parts of its own columns
-  size_t slots = (left - b) / (part * cols);
-  while (slots < static_cast<size_t>(kMinSlots)) {
-    cols /= 2;
-    for (Phase& ph : a.ph)
-      if (static_cast<size_t>(ph.cap) * (ph.two ? 2 : 1) > cols) ph.cap = static_cast<int>(cols) / (ph.two ? 2 : 1);
-    slots = (left - b) / (part * cols);
+  // the phases use the same room one after the other: narrower segments if both do not fit
+  while (b + tab > left) {
+    const size_t c0 = static_cast<size_t>(a.ph[0].cap) * (a.ph[0].two ? 2 : 1);
+    const size_t c1 = static_cast<size_t>(a.ph[1].cap) * (a.ph[1].two ? 2 : 1);
+    const size_t t0 = c0 * 4 * kWarps * 16 * sizeof(float), t1 = c1 * 2 * kWarps * 16 * sizeof(float);
+    const size_t b0 = c0 * a.ph[0].K * 2, b1 = c1 * a.ph[1].K * 2;
+    tab = t0 > t1 ? t0 : t1;
+    b = b0 > b1 ? b0 : b1;
+    if (b + tab <= left) break;
+    Phase& ph = t0 >= t1 && a.ph[0].cap > 1 ? a.ph[0] : a.ph[1].cap > 1 ? a.ph[1] : a.ph[0];
+    ph.cap /= 2;
   }
-  a.tabslots = static_cast<int>(slots < static_cast<size_t>(kMaxSlots) ? slots : kMaxSlots);
-  a.tabfloats = a.tabslots * 16 * static_cast<int>(cols);
+  for (int f = 0; f < 2; ++f) a.ph[f].part = (f == 0 ? 2 : 1) * 16 * a.ph[f].cap * (a.ph[f].two ? 2 : 1);
   a.b_off = kRingBytes;
-  a.tab_off = a.b_off + static_cast<uint32_t>(b);
-  a.plan_off = a.tab_off + 2 * a.tabfloats * 4;
+  a.bbytes = static_cast<int>((left - tab) & ~size_t(15));
+  a.tab_off = a.b_off + a.bbytes;
+  a.plan_off = a.tab_off + static_cast<uint32_t>(tab);
   return a.plan_off + plan;
 }
 
@@ -780,9 +862,9 @@ gq_status moe_entry(const void* gate, const void* up, const void* down, int64_t 
   const auto row_bytes = [](int64_t K) { return FMT == GQ_FMT_Q4_0 ? K / 32 * 18 : K / 256 * 138; };
   MoeArgs a{};
   a.ph[0] = Phase{static_cast<const uint8_t*>(gate), static_cast<const uint8_t*>(up), static_cast<int>(H),
-                  static_cast<int>(I / 16), 16 * row_bytes(H), x_dtype == GQ_F32, 0};
+                  static_cast<int>(I / 16), 16 * row_bytes(H), x_dtype == GQ_F32, 0, 0};
   a.ph[1] = Phase{static_cast<const uint8_t*>(down), nullptr, static_cast<int>(I), static_cast<int>(H / 16),
-                  16 * row_bytes(I), y_dtype == GQ_F32, 0};
+                  16 * row_bytes(I), y_dtype == GQ_F32, 0, 0};
   a.x = x;
   a.ids = ids;
   a.weights = weights;
