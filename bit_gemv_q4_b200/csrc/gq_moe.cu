@@ -23,10 +23,10 @@
 // each CTA.  A run is a string of stages (8 blocks of 32 weights x 16 rows, 2.3
 // KB) that its 24 warps share evenly, so that the split is even whatever the
 // sizes are.  Each warp copies its own stages to its own ring in shared memory
-// (cp.async), a few ahead: tiled storage is ordered by the lanes that multiply
-// it, so the copies are whole lines and a lane reads back its own codes, and
-// warps wait for nothing but their own copies.  (Reading units straight into
-// registers, eight ahead, ran at 1.5 TB/s: loads that share a scoreboard are
+// (cp.async): tiled storage is ordered by the lanes that multiply it, so the
+// copies are whole lines and a lane reads back its own codes, and warps wait
+// for nothing but their own copies.  (Reading stages straight into registers,
+// one or two ahead, ran at half the rate: loads that share a scoreboard are
 // waited for together.)  A warp finishes the items that it has all of in its
 // registers; the parts of an item that several warps share meet in a table and
 // are added in warp order: results do not depend on scheduling.
@@ -158,9 +158,9 @@ __device__ void make_plan(Plan& pl, const MoeArgs& a) {
   const int P = a.T * a.k, P4 = (P + 3) & ~3;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* ids = reinterpret_cast<int*>(msm);  // in the rings' place
-  short* rank = reinterpret_cast<short*>(ids + kMaxPairs);  // by slot: place among its expert's,
-  short* count = rank + kMaxPairs;                          // how many these are,
-  short* expert = count + kMaxPairs;                        // and the expert
+  short* rank = reinterpret_cast<short*>(ids + P4);  // by slot: place among its expert's,
+  short* count = rank + P4;                          // how many these are,
+  short* expert = count + P4;                        // and the expert
   for (int p = threadIdx.x; p < P4; p += kThreads) {
     const int id = p < P ? __ldcg(a.ids + p) : -1;
     if (blockIdx.x == 0 && (id < -1 || id >= a.E)) report(a.dev_status, GQ_DEV_RANGE);
@@ -239,12 +239,14 @@ __device__ __forceinline__ int col_pitch(int ncol) {
 
 // B fragments of a segment's tokens at shared offset b_off.  Column c of block b
 // and lane group t: 16 bytes at ((b * pitch + c) * 4 + t) * 16, the values 4t,
-// 4t+2, 4t+1, 4t+3 of the block and the same at +16.
+// 4t+2, 4t+1, 4t+3 of the block and the same at +16; zeros up to whole stages.
+__host__ __device__ __forceinline__ int padded(int K) { return (K + 255) & ~255; }
+
 template <bool GATE_UP>
 __device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& pl, const Seg& sg, int local,
                                        int b_off) {
   const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
-  const int vecs = ph.K / 8;
+  const int vecs = padded(ph.K) / 8, real = ph.K / 8;
   auto row_of = [&](int c) { return GATE_UP ? pl.order[sg.slot0 + c] / a.k : sg.slot0 + c; };
   auto max_of = [&](int c) { return GATE_UP ? pl.xmax[row_of(c)] : __ldcg(a.hmax + sg.slot0 + c); };
   const int type = GATE_UP ? a.xtype : GQ_F32;
@@ -258,8 +260,8 @@ __device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& 
   for (int i = threadIdx.x; i < nvec; i += kThreads) {
     const int c = i / vecs, r = i - c * vecs;
     const int b = r >> 2, q = r & 3;
-    float v[8];
-    load8(src, static_cast<int64_t>(row_of(c)) * ph.K + 8 * r, type, v);
+    float v[8] = {};
+    if (r < real) load8(src, static_cast<int64_t>(row_of(c)) * ph.K + 8 * r, type, v);
     const float s = scale_of(max_of(c));
     const int col = ph.two ? 2 * c : c;
     const int t0 = 2 * (q & 1);
@@ -325,22 +327,19 @@ __device__ __forceinline__ void block_math(uint32_t wa, uint32_t wb, float da, f
   if (CP > 1) acc[3] = fmaf(db, c[3], acc[3]);
 }
 
-// A stage from its ring slot: n units of two blocks (Q4_0) or one super-block.
-template <int FMT, int CP, bool FULL>
-__device__ __forceinline__ void stage_math(const uint8_t* st, int n, int lane, float acc[4],
-                                           const uint8_t* xb) {
+// acc += the stage in ring slot st: four units of two blocks (Q4_0) or one super-block.
+template <int FMT, int CP>
+__device__ __forceinline__ void stage_math(const uint8_t* st, int lane, float acc[4], const uint8_t* xb) {
   const uint8_t* code = st + (FMT == GQ_FMT_Q4_0 ? 16 : 32) * lane;
   const uint8_t* sc = st + kStageCodes + 4 * (lane >> 2);
   if constexpr (FMT == GQ_FMT_Q4_0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (FULL || i < n) {
-        const uint4 v = ld128(code + 512 * i);
-        const float2 da = halves(ld32(sc + 64 * i));
-        const float2 db = halves(ld32(sc + 64 * i + 32));
-        block_math<CP>(v.x, v.y, da.x, db.x, acc, xb + (2 * i) * (64 * CP));
-        block_math<CP>(v.z, v.w, da.y, db.y, acc, xb + (2 * i + 1) * (64 * CP));
-      }
+      const uint4 v = ld128(code + 512 * i);
+      const float2 da = halves(ld32(sc + 64 * i));
+      const float2 db = halves(ld32(sc + 64 * i + 32));
+      block_math<CP>(v.x, v.y, da.x, db.x, acc, xb + (2 * i) * (64 * CP));
+      block_math<CP>(v.z, v.w, da.y, db.y, acc, xb + (2 * i + 1) * (64 * CP));
     }
   } else {
     const uint8_t* ss = st + kStageCodes + 128 + 2 * (lane >> 2);
@@ -393,9 +392,10 @@ struct Feed {
       scale = lane < 8 ? tile + 2048 * ns + 128 * j + 16 * lane : tile + 2176 * ns + 32 * j + 16 * (lane - 8);
     }
   }
-  __device__ __forceinline__ void step(const Phase& ph, const Plan& pl, int stages, uint32_t dst, int lane) {
+  // Copies it to ring slot `slot` (a byte offset); always a group, so that groups count stages.
+  __device__ __forceinline__ void step(const Phase& ph, const Plan& pl, int stages, uint32_t slot, int lane) {
     if (left > 0) {
-      dst += 16 * lane;
+      const uint32_t dst = smem_addr(msm) + slot + 16 * lane;
       const int kk = GATE_UP && k >= stages ? k - stages : k;
       const bool end = kk == stages - 1;
       const int n = FMT == GQ_FMT_Q4_0 && end ? (ph.K >> 6) - 4 * kk : 4;  // units
@@ -404,6 +404,8 @@ struct Feed {
         for (int i = 0; i < 4; ++i) copy16(dst + 512 * i, code + 512 * i);
       } else {
         for (int i = 0; i < n; ++i) copy16(dst + 512 * i, code + 512 * i);
+        // units that are not there: scales of zero (and their activations are zeros)
+        if (lane >= 4 * n && lane < 16) *reinterpret_cast<uint4*>(msm + slot + kStageCodes + 16 * lane) = uint4{};
       }
       if (lane < (FMT == GQ_FMT_Q4_0 ? 4 * n : 10)) copy16(dst + kStageCodes, scale);
       --left;
@@ -422,7 +424,7 @@ struct Feed {
         scale += FMT == GQ_FMT_Q4_0 ? 256 : (lane < 8 ? 128 : 32);
       }
     }
-    copies_commit();  // also an empty group: groups count stages
+    copies_commit();
   }
 };
 
@@ -470,10 +472,11 @@ struct Work {
   int u0, u1;     // this warp's stages of the string
   Feed<FMT, GATE_UP> feed;
 
+  __device__ __forceinline__ static uint32_t ring() { return (threadIdx.x >> 5) * (kDepth * kStageBytes); }
   __device__ __forceinline__ int item_stages() const { return GATE_UP ? 2 * stages : stages; }
 
-  // The next string, and the first copies of this warp's share of it.
-  __device__ __forceinline__ void next(const MoeArgs& a, const Phase& ph, const Plan& pl, uint32_t ring) {
+  // The next string, and the first copy of this warp's share of it.
+  __device__ __forceinline__ void next(const MoeArgs& a, const Phase& ph, const Plan& pl) {
     more = r < r1;
     if (!more) return;
     st.ra = r;
@@ -482,7 +485,7 @@ struct Work {
     int bytes = 0;
     while (r < r1 && st.segs < kMaxSegs) {
       const int s = st.seg0 + st.segs;
-      bytes += col_pitch(ph.two ? 2 * pl.seg[!GATE_UP][s].n : pl.seg[!GATE_UP][s].n) * ph.K * 2;
+      bytes += col_pitch(ph.two ? 2 * pl.seg[!GATE_UP][s].n : pl.seg[!GATE_UP][s].n) * padded(ph.K) * 2;
       if (bytes > a.bbytes && st.segs) break;  // (one segment always fits)
       r = min(r1, (s + 1) * ph.groups);
       ++st.segs;
@@ -498,49 +501,34 @@ struct Work {
     feed.g = i - feed.s * ph.groups;
     feed.left = u1 - u0;
     if (feed.left > 0) feed.seek(ph, pl, stages, lane);
-    for (int d = 0; d < kDepth; ++d) feed.step(ph, pl, stages, smem_addr(msm) + ring + d * kStageBytes, lane);
+    feed.step(ph, pl, stages, ring(), lane);
   }
-  __device__ __forceinline__ void start(const MoeArgs& a, const Plan& pl, uint32_t ring) {
+  __device__ __forceinline__ void start(const MoeArgs& a, const Plan& pl) {
     const Phase& ph = a.ph[!GATE_UP];
     const unsigned total = static_cast<unsigned>(pl.nseg[!GATE_UP]) * ph.groups;  // at most 2^20
     r = static_cast<int>(total * blockIdx.x / gridDim.x);
     r1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
     stages = FMT == GQ_FMT_Q4_0 ? (ph.K + 255) / 256 : ph.K / 256;
-    next(a, ph, pl, ring);
+    next(a, ph, pl);
   }
 };
 
 // This warp's stages [u, ue) of the string, all of one segment, from stage k of
-// row group g on; the copies are under way.  `whole`: the warp has its item from
-// the first stage on.
+// row group g on.  `whole`: the warp has its item from the first stage on.
 template <int FMT, int CP, bool GATE_UP>
 __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& pl, Work<FMT, GATE_UP>& wk,
                                        const Seg& sg, int local, int u, int ue, int g, int k, bool& whole,
-                                       uint32_t ring, uint32_t& st) {
+                                       uint32_t& slot) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
   // columns past the last repeat existing ones (or hold what was there); their sums are not used
   const uint8_t* xb = msm + pl.boff[local] + (g8 & (CP - 1)) * 64 + t * 16;
-  const uint32_t sbase = smem_addr(msm);
   const int stages = wk.stages, all = wk.item_stages();
-  const int last_n = FMT == GQ_FMT_Q4_0 ? (ph.K >> 6) - 4 * (stages - 1) : 4;  // units of a row's last stage
   float acc[4] = {}, gate[4] = {};
   unsigned top[2] = {0u, 0u};  // largest |h| of this lane's tokens
   int kk = GATE_UP && k >= stages ? k - stages : k;
   const uint8_t* x = xb + kk * (8 * 64 * CP);
-  for (; u < ue; ++u) {
-    copies_wait<kDepth - 1>();
-    __syncwarp();  // every lane's copies of the stage
-    ++k;
-    const bool end = ++kk == stages;
-    if (FMT == GQ_FMT_KSB || !end || last_n == 4)
-      stage_math<FMT, CP, true>(msm + st, 4, lane, acc, x);
-    else
-      stage_math<FMT, CP, false>(msm + st, last_n, lane, acc, x);
-    x += 8 * 64 * CP;
-    __syncwarp();  // every lane has read the stage
-    wk.feed.step(ph, pl, stages, sbase + st, lane);
-    st = st == ring + (kDepth - 1) * kStageBytes ? ring : st + kStageBytes;
-    if (!end) continue;
+  // the row group ends: the gate's sums wait for up's, or the item is done
+  auto row_end = [&]() {
     kk = 0;
     x = xb;
     if (GATE_UP && k == stages) {
@@ -549,7 +537,7 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
         gate[i] = acc[i];
         acc[i] = 0.f;
       }
-      continue;
+      return;
     }
     if (whole) {
       // columns 2t and 2t+1, rows g8 and g8 + 8: two tokens, or one in two columns
@@ -577,6 +565,17 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
     whole = true;
     k = 0;
     ++g;
+  };
+  for (; u < ue; ++u) {
+    copies_wait<kDepth - 1>();
+    __syncwarp();  // every lane's copies of the stage
+    stage_math<FMT, CP>(msm + slot, lane, acc, x);
+    x += 8 * 64 * CP;
+    __syncwarp();  // every lane has read the stage
+    wk.feed.step(ph, pl, stages, slot, lane);
+    slot = slot == wk.ring() + (kDepth - 1) * kStageBytes ? wk.ring() : slot + kStageBytes;
+    ++k;
+    if (++kk == stages) row_end();
   }
   if (k > 0 && k < all && u == wk.u1 && wk.u1 > wk.u0) {  // the run ends inside an item
     float* d = part_at(a, ph, warp, whole);
@@ -601,95 +600,108 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
   }
 }
 
-// All strings of a phase; after(): called once this warp has no more copies to
-// issue for it.
-template <int FMT, bool GATE_UP, class After>
-__device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, GATE_UP>& wk, uint32_t ring,
-                                          After after) {
+// After the last stage of a string: an item that this warp began and did not
+// end takes the later warps' parts in order; then the sizes of h.
+template <int FMT, bool GATE_UP>
+__device__ __noinline__ void join_parts(const MoeArgs& a, Plan& pl, const String st, int u0, int u1, int all) {
   const Phase& ph = a.ph[!GATE_UP];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tu = (st.rb - st.ra) * all;
+  __syncthreads();  // the parts are there; nobody reads B any more
+  const int last = st.ra + (u1 - 1) / all;  // this warp's last item
+  const int begin = (last - st.ra) * all;
+  if (u1 > u0 && begin >= u0 && u1 < begin + all) {
+    const int s = last / ph.groups, local = s - st.seg0;
+    const Seg sg = pl.seg[!GATE_UP][s];
+    const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
+    const int row = lane & 15, half = lane >> 4;
+    // gate and up: each half of the warp one matrix; down: every other token
+    for (int c0 = 0; c0 < sg.n; c0 += GATE_UP ? 1 : 2) {
+      const int c = GATE_UP ? c0 : min(c0 + half, sg.n - 1);
+      const int at = ((GATE_UP ? half * 16 : 0) + row) * pitch + (ph.two ? 2 * c : c);
+      float v = 0.f;
+      for (int w = warp; w < kWarps && tu * w / kWarps < begin + all; ++w) {
+        if (tu * w / kWarps == tu * (w + 1) / kWarps) continue;  // no stages
+        const float* d = part_at(a, ph, w, w == warp) + at;
+        v += ph.two ? d[0] + d[1] : d[0];
+      }
+      v *= pl.inv[local][c];
+      const float up = __shfl_down_sync(0xFFFFFFFFu, v, 16);
+      unsigned m = 0;
+      if (GATE_UP ? half == 0 : c0 + half < sg.n)
+        m = put<GATE_UP>(a, ph, pl, sg, c, 16 * (last - s * ph.groups) + row, v, up);
+      if (GATE_UP) {
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if (lane == 0) atomicMax(&pl.hmax[local][c], m);
+      }
+    }
+  }
+  __syncthreads();
+  if (GATE_UP && threadIdx.x < st.segs * kMaxCols) {
+    const int i = threadIdx.x / kMaxCols, c = threadIdx.x % kMaxCols;
+    const Seg sg = pl.seg[0][st.seg0 + i];
+    if (c < sg.n) atomicMax(a.hmax + sg.slot0 + c, pl.hmax[i][c]);
+  }
+}
+
+// The strings of a phase, up to the last one's parts; that string is left in
+// (st, u0, u1) for join_parts().
+template <int FMT, bool GATE_UP>
+__device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, GATE_UP>& wk, String& st, int& u0,
+                                          int& u1) {
+  const Phase& ph = a.ph[!GATE_UP];
   const int all = wk.item_stages();
-  if (!wk.more) after();
   while (wk.more) {
-    const String st = wk.st;
-    const int u0 = wk.u0, u1 = wk.u1, tu = (st.rb - st.ra) * all;
+    st = wk.st;
+    u0 = wk.u0;
+    u1 = wk.u1;
     int b_off = a.b_off;
     for (int i = 0; i < st.segs; ++i) {
       const Seg sg = pl.seg[!GATE_UP][st.seg0 + i];
       load_b<GATE_UP>(a, ph, pl, sg, i, b_off);
-      b_off += col_pitch(ph.two ? 2 * sg.n : sg.n) * ph.K * 2;
+      b_off += col_pitch(ph.two ? 2 * sg.n : sg.n) * padded(ph.K) * 2;
     }
+    // the rest of the ring (the first copies went ahead of B: a full ring of them would hold it up)
+    for (int d = 1; d < kDepth; ++d)
+      wk.feed.step(ph, pl, wk.stages, wk.ring() + d * kStageBytes, threadIdx.x & 31);
     __syncthreads();
-    const int i0 = st.ra + u0 / all, k0 = u0 % all;
-    bool whole = k0 == 0;
-    uint32_t slot = ring;
-    int u = u0, r = i0, k = k0;
+    bool whole = u0 % all == 0;
+    uint32_t slot = wk.ring();
+    int u = u0, r = st.ra + u0 / all, k = u0 % all;
     while (u < u1) {
       const int s = r / ph.groups, local = s - st.seg0;
       const Seg sg = pl.seg[!GATE_UP][s];
       const int ue = min(u1, (min(st.rb, (s + 1) * ph.groups) - st.ra) * all);
       const int g = r - s * ph.groups;
       switch (col_pitch(ph.two ? 2 * sg.n : sg.n)) {
-        case 1: stream<FMT, 1, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, ring, slot); break;
-        case 2: stream<FMT, 2, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, ring, slot); break;
-        case 4: stream<FMT, 4, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, ring, slot); break;
-        default: stream<FMT, 8, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, ring, slot);
+        case 1: stream<FMT, 1, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, slot); break;
+        case 2: stream<FMT, 2, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, slot); break;
+        case 4: stream<FMT, 4, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, slot); break;
+        default: stream<FMT, 8, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, slot);
       }
       u = ue;
       r = (s + 1) * ph.groups;
       k = 0;
     }
-    wk.next(a, ph, pl, ring);
-    if (!wk.more) after();
-    __syncthreads();  // the parts are there; nobody reads B any more
-    // An item that this warp began and did not end: the later warps' parts in order.
-    const int last = st.ra + (u1 - 1) / all;  // this warp's last item
-    const int begin = (last - st.ra) * all;
-    if (u1 > u0 && begin >= u0 && u1 < begin + all) {
-      const int s = last / ph.groups, local = s - st.seg0;
-      const Seg sg = pl.seg[!GATE_UP][s];
-      const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
-      const int row = lane & 15, half = lane >> 4;
-      // gate and up: each half of the warp one matrix; down: every other token
-      for (int c0 = 0; c0 < sg.n; c0 += GATE_UP ? 1 : 2) {
-        const int c = GATE_UP ? c0 : min(c0 + half, sg.n - 1);
-        const int at = ((GATE_UP ? half * 16 : 0) + row) * pitch + (ph.two ? 2 * c : c);
-        float v = 0.f;
-        for (int w = warp; w < kWarps && tu * w / kWarps < begin + all; ++w) {
-          if (tu * w / kWarps == tu * (w + 1) / kWarps) continue;  // no stages
-          const float* d = part_at(a, ph, w, w == warp) + at;
-          v += ph.two ? d[0] + d[1] : d[0];
-        }
-        v *= pl.inv[local][c];
-        const float up = __shfl_down_sync(0xFFFFFFFFu, v, 16);
-        unsigned m = 0;
-        if (GATE_UP ? half == 0 : c0 + half < sg.n)
-          m = put<GATE_UP>(a, ph, pl, sg, c, 16 * (last - s * ph.groups) + row, v, up);
-        if (GATE_UP) {
-          m = __reduce_max_sync(0xFFFFFFFFu, m);
-          if (lane == 0) atomicMax(&pl.hmax[local][c], m);
-        }
-      }
-    }
-    __syncthreads();
-    if (GATE_UP && threadIdx.x < st.segs * kMaxCols) {
-      const int i = threadIdx.x / kMaxCols, c = threadIdx.x % kMaxCols;
-      const Seg sg = pl.seg[0][st.seg0 + i];
-      if (c < sg.n) atomicMax(a.hmax + sg.slot0 + c, pl.hmax[i][c]);
-    }
-    if (wk.more) __syncthreads();  // before the next string's values
+    wk.next(a, ph, pl);
+    if (!wk.more) break;
+    join_parts<FMT, GATE_UP>(a, pl, st, u0, u1, all);
+    __syncthreads();  // before the next string's values
   }
 }
 
-// All CTAs of the grid arrive, and what each wrote before is seen by all after;
-// false once the budget has passed.  The arrivals only ever count up (in 64
-// bits), so nothing has to be cleared.
-__device__ __forceinline__ bool grid_barrier(const MoeArgs& a, Plan& pl) {
+// A barrier of the grid in two halves: what each CTA wrote before it arrives is
+// seen by all after the wait, which gives up (false) once the budget has passed.
+// The arrivals only ever count up (in 64 bits), so nothing has to be cleared.
+// arrive() returns the count to wait for, in thread 0.
+__device__ __forceinline__ unsigned long long grid_arrive(const MoeArgs& a) {
   __threadfence();
   __syncthreads();
+  if (threadIdx.x) return 0;
+  return (atomicAdd(a.arrivals, 1ull) / gridDim.x + 1) * gridDim.x;
+}
+__device__ __forceinline__ bool grid_wait(const MoeArgs& a, Plan& pl, unsigned long long target) {
   if (threadIdx.x == 0) {
-    const unsigned long long n = atomicAdd(a.arrivals, 1ull);
-    const unsigned long long target = (n / gridDim.x + 1) * gridDim.x;
     const long long t0 = clock64();
     int go = 1;
     for (;;) {
@@ -722,16 +734,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   pdl_wait();  // ids and x are final
   pdl_launch_dependents();
   make_plan(pl, a);
-  const uint32_t ring = static_cast<uint32_t>((threadIdx.x >> 5) * kDepth * kStageBytes);
-  Work<FMT, true> gate_up;
+  String st{0, 0, 0, 0};
+  int u0 = 0, u1 = 0;
+  {
+    Work<FMT, true> gate_up;
+    gate_up.start(a, pl);
+    run_phase<FMT, true>(a, pl, gate_up, st, u0, u1);
+  }
+  join_parts<FMT, true>(a, pl, st, u0, u1, 2 * (FMT == GQ_FMT_Q4_0 ? (a.ph[0].K + 255) / 256 : a.ph[0].K / 256));
+  unsigned long long target = grid_arrive(a);
   Work<FMT, false> down;
-  gate_up.start(a, pl, ring);
-  // down's first copies are under way while this CTA waits for the others
-  run_phase<FMT, true>(a, pl, gate_up, ring, [&] { down.start(a, pl, ring); });
-  bool ok = grid_barrier(a, pl);
+  down.start(a, pl);  // its first copies are under way while this CTA waits for the others
+  bool ok = grid_wait(a, pl, target);
   if (ok) {
-    run_phase<FMT, false>(a, pl, down, ring, [] {});
-    ok = grid_barrier(a, pl);
+    st.segs = u0 = u1 = 0;
+    run_phase<FMT, false>(a, pl, down, st, u0, u1);
+    join_parts<FMT, false>(a, pl, st, u0, u1, down.item_stages());
+    target = grid_arrive(a);
+    ok = grid_wait(a, pl, target);
   }
   if (!ok) {
     copies_wait<0>();
@@ -792,17 +812,17 @@ size_t shape_smem(MoeArgs& a) {
     const size_t part = 2 * kWarps * (f == 0 ? 2 : 1) * 16 * sizeof(float);  // for each column
     const size_t need = static_cast<size_t>(pairs) * (ph.two ? 2 : 1);
     size_t c = ph.two ? 2 : 1;  // powers of two
-    while (c < kMaxCols && c < need && 2 * c * (static_cast<size_t>(ph.K) * 2 + part) <= left) c *= 2;
+    while (c < kMaxCols && c < need && 2 * c * (static_cast<size_t>(padded(ph.K)) * 2 + part) <= left) c *= 2;
     ph.cap = static_cast<int>(ph.two ? c / 2 : c);
     tab = c * part > tab ? c * part : tab;
-    b = c * ph.K * 2 > b ? c * ph.K * 2 : b;
+    b = c * padded(ph.K) * 2 > b ? c * padded(ph.K) * 2 : b;
   }
   // the phases use the same room one after the other: narrower segments if both do not fit
   while (b + tab > left) {
     const size_t c0 = static_cast<size_t>(a.ph[0].cap) * (a.ph[0].two ? 2 : 1);
     const size_t c1 = static_cast<size_t>(a.ph[1].cap) * (a.ph[1].two ? 2 : 1);
     const size_t t0 = c0 * 4 * kWarps * 16 * sizeof(float), t1 = c1 * 2 * kWarps * 16 * sizeof(float);
-    const size_t b0 = c0 * a.ph[0].K * 2, b1 = c1 * a.ph[1].K * 2;
+    const size_t b0 = c0 * padded(a.ph[0].K) * 2, b1 = c1 * padded(a.ph[1].K) * 2;
     tab = t0 > t1 ? t0 : t1;
     b = b0 > b1 ? b0 : b1;
     if (b + tab <= left) break;
