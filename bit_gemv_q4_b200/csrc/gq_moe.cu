@@ -153,7 +153,7 @@ __device__ __forceinline__ void load8(const void* base, int64_t i, int type, flo
 
 // Pairs sorted by expert (stable), the segments of both phases, and the tokens'
 // largest |x|.  ids outside [0, E) are left out.  A pair's slot is the number of
-// pairs that go before it, counted by a thread of its own.
+// pairs that go before it, counted by one or more lanes of its own.
 __device__ void make_plan(Plan& pl, const MoeArgs& a) {
   const int P = a.T * a.k, P4 = (P + 3) & ~3;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -181,21 +181,28 @@ __device__ void make_plan(Plan& pl, const MoeArgs& a) {
     if (lane == 0) atomicMax(&pl.xmax[t], m);
   }
   __syncthreads();
+  int share_log = 0;  // 2^share_log lanes for each pair
+  while (share_log < 5 && (P << (share_log + 1)) <= kThreads) ++share_log;
+  const int lanes = 1 << share_log, sub = lane & (lanes - 1);
   int slots = 0;
-  for (int p0 = 0; p0 < P; p0 += kThreads) {
-    const int p = p0 + threadIdx.x;
+  for (int p0 = 0; p0 < P; p0 += kThreads >> share_log) {
+    const int p = p0 + (threadIdx.x >> share_log);
     const int id = p < P ? ids[p] : 0x7FFFFFFF;
-    const bool ok = id != 0x7FFFFFFF;
+    int less = 0, same = 0, before = 0;
+    for (int q = 4 * sub; q < P4; q += 4 * lanes) {
+      const int4 v = *reinterpret_cast<const int4*>(ids + q);
+      less += (v.x < id) + (v.y < id) + (v.z < id) + (v.w < id);
+      const int eq = (v.x == id) | (v.y == id) << 1 | (v.z == id) << 2 | (v.w == id) << 3;
+      same += __popc(eq);
+      before += __popc(eq & ((1 << min(max(p - q, 0), 4)) - 1));
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+      less += __shfl_xor_sync(0xFFFFFFFFu, less, o);
+      same += __shfl_xor_sync(0xFFFFFFFFu, same, o);
+      before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+    }
+    const bool ok = sub == 0 && id != 0x7FFFFFFF;
     if (ok) {
-      int less = 0, same = 0, before = 0;
-      for (int q = 0; q < P4; q += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(ids + q);
-        less += (v.x < id) + (v.y < id) + (v.z < id) + (v.w < id);
-        const int eq = (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
-        same += eq;
-        if (q + 3 < p) before += eq;
-        else if (q <= p) before += (v.x == id && q < p) + (v.y == id && q + 1 < p) + (v.z == id && q + 2 < p);
-      }
       const int slot = less + before;
       pl.order[slot] = static_cast<short>(p);
       rank[slot] = static_cast<short>(before);
@@ -603,8 +610,8 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
 // After the last stage of a string: an item that this warp began and did not
 // end takes the later warps' parts in order; then the sizes of h.
 template <int FMT, bool GATE_UP>
-__device__ __noinline__ void join_parts(const MoeArgs& a, Plan& pl, const String st, int u0, int u1, int all) {
-  const Phase& ph = a.ph[!GATE_UP];
+__device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Plan& pl, const String& st, int u0,
+                                           int u1, int all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tu = (st.rb - st.ra) * all;
   __syncthreads();  // the parts are there; nobody reads B any more
@@ -644,17 +651,14 @@ __device__ __noinline__ void join_parts(const MoeArgs& a, Plan& pl, const String
   }
 }
 
-// The strings of a phase, up to the last one's parts; that string is left in
-// (st, u0, u1) for join_parts().
+// All strings of a phase.
 template <int FMT, bool GATE_UP>
-__device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, GATE_UP>& wk, String& st, int& u0,
-                                          int& u1) {
+__device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, GATE_UP>& wk) {
   const Phase& ph = a.ph[!GATE_UP];
   const int all = wk.item_stages();
   while (wk.more) {
-    st = wk.st;
-    u0 = wk.u0;
-    u1 = wk.u1;
+    const String st = wk.st;
+    const int u0 = wk.u0, u1 = wk.u1;
     int b_off = a.b_off;
     for (int i = 0; i < st.segs; ++i) {
       const Seg sg = pl.seg[!GATE_UP][st.seg0 + i];
@@ -684,9 +688,8 @@ __device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, 
       k = 0;
     }
     wk.next(a, ph, pl);
-    if (!wk.more) break;
-    join_parts<FMT, GATE_UP>(a, pl, st, u0, u1, all);
-    __syncthreads();  // before the next string's values
+    join_parts<FMT, GATE_UP>(a, ph, pl, st, u0, u1, all);
+    if (wk.more) __syncthreads();  // before the next string's values
   }
 }
 
@@ -734,22 +737,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   pdl_wait();  // ids and x are final
   pdl_launch_dependents();
   make_plan(pl, a);
-  String st{0, 0, 0, 0};
-  int u0 = 0, u1 = 0;
   {
     Work<FMT, true> gate_up;
     gate_up.start(a, pl);
-    run_phase<FMT, true>(a, pl, gate_up, st, u0, u1);
+    run_phase<FMT, true>(a, pl, gate_up);
   }
-  join_parts<FMT, true>(a, pl, st, u0, u1, 2 * (FMT == GQ_FMT_Q4_0 ? (a.ph[0].K + 255) / 256 : a.ph[0].K / 256));
   unsigned long long target = grid_arrive(a);
   Work<FMT, false> down;
   down.start(a, pl);  // its first copies are under way while this CTA waits for the others
   bool ok = grid_wait(a, pl, target);
   if (ok) {
-    st.segs = u0 = u1 = 0;
-    run_phase<FMT, false>(a, pl, down, st, u0, u1);
-    join_parts<FMT, false>(a, pl, st, u0, u1, down.item_stages());
+    run_phase<FMT, false>(a, pl, down);
     target = grid_arrive(a);
     ok = grid_wait(a, pl, target);
   }
