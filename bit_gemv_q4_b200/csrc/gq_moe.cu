@@ -68,12 +68,24 @@ constexpr int kStageBytes = 2304;   // codes, then scales
 constexpr int kDepth = 2;           // stages of a warp's ring
 constexpr size_t kRingBytes = static_cast<size_t>(kWarps) * kDepth * kStageBytes;
 
+// n / d for n * d < 2^32, d known to the host.  (Every warp divides a few times
+// at each phase; as the compiler's division these cost 1 us a phase.)
+struct Div {
+  unsigned d, m;
+  __device__ __forceinline__ int operator()(int n) const {
+    return m ? static_cast<int>(__umulhi(static_cast<unsigned>(n), m)) : n;
+  }
+};
+Div make_div(unsigned d) { return Div{d, d > 1 ? static_cast<unsigned>((1ull << 32) / d + 1) : 0u}; }
+
 // One of the two products: gate and up, or down.
 struct Phase {
   const uint8_t* w0;        // gate, or down
   const uint8_t* w1;        // up
   int K;                    // columns of the weights
   int groups;               // row groups (16 rows) of one expert
+  int stages;               // of a row group
+  Div by_groups, by_item, by_vecs;  // row groups, stages of an item, 8-value pieces of a padded row
   int64_t group_bytes;
   int two;                  // two columns for each token
   int cap;                  // tokens of a segment at most, a power of two
@@ -93,6 +105,7 @@ struct MoeArgs {
   int* dev_status;
   long long budget;
   int T, k, E, H;
+  Div by_grid;
   int xtype, ytype;
   int bbytes;               // room for B fragments
   uint32_t b_off, tab_off, plan_off;  // dynamic shared memory, after the rings
@@ -170,7 +183,7 @@ __device__ void make_plan(Plan& pl, const MoeArgs& a) {
   for (int i = warp; i < a.T * share; i += kWarps) {
     const int t = i / share;
     unsigned m = 0;
-#pragma unroll 2
+#pragma unroll 4
     for (int r = (i - t * share) * 32 + lane; r < vecs; r += 32 * share) {
       float v[8];
       load8(a.x, static_cast<int64_t>(t) * a.H + 8 * r, a.xtype, v);
@@ -265,7 +278,7 @@ __device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& 
   if (threadIdx.x == 0) pl.boff[local] = b_off;
   const int nvec = sg.n * vecs;
   for (int i = threadIdx.x; i < nvec; i += kThreads) {
-    const int c = i / vecs, r = i - c * vecs;
+    const int c = ph.by_vecs(i), r = i - c * vecs;
     const int b = r >> 2, q = r & 3;
     float v[8] = {};
     if (r < real) load8(src, static_cast<int64_t>(row_of(c)) * ph.K + 8 * r, type, v);
@@ -461,7 +474,8 @@ template <bool GATE_UP>
 __device__ __forceinline__ unsigned put(const MoeArgs& a, const Phase& ph, const Plan& pl, const Seg& sg, int c,
                                         int row, float v, float up) {
   if constexpr (GATE_UP) {
-    const float h = v / (1.0f + expf(-v)) * up;
+    // within 2 steps; a quotient by an infinity is zero
+    const float h = __fdividef(v, 1.0f + expf(-v)) * up;
     __stcg(a.h + static_cast<int64_t>(sg.slot0 + c) * (ph.groups * 16) + row, h);
     return __float_as_uint(h) & 0x7FFFFFFFu;
   } else {
@@ -473,21 +487,19 @@ __device__ __forceinline__ unsigned put(const MoeArgs& a, const Phase& ph, const
 template <int FMT, bool GATE_UP>
 struct Work {
   int r, r1;      // items left to this CTA
-  int stages;     // of a row group of one matrix
   bool more;
   String st;
   int u0, u1;     // this warp's stages of the string
+  int s0, g0, k0; // where they begin
   Feed<FMT, GATE_UP> feed;
 
   __device__ __forceinline__ static uint32_t ring() { return (threadIdx.x >> 5) * (kDepth * kStageBytes); }
-  __device__ __forceinline__ int item_stages() const { return GATE_UP ? 2 * stages : stages; }
-
   // The next string, and the first copy of this warp's share of it.
   __device__ __forceinline__ void next(const MoeArgs& a, const Phase& ph, const Plan& pl) {
     more = r < r1;
     if (!more) return;
     st.ra = r;
-    st.seg0 = r / ph.groups;
+    st.seg0 = ph.by_groups(r);
     st.segs = 0;
     int bytes = 0;
     while (r < r1 && st.segs < kMaxSegs) {
@@ -499,23 +511,24 @@ struct Work {
     }
     st.rb = r;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tu = (st.rb - st.ra) * item_stages();
-    u0 = tu * warp / kWarps;
-    u1 = tu * (warp + 1) / kWarps;
-    const int i = st.ra + u0 / item_stages();
-    feed.k = u0 % item_stages();
-    feed.s = i / ph.groups;
-    feed.g = i - feed.s * ph.groups;
+    const unsigned tu = (st.rb - st.ra) * ph.by_item.d;
+    u0 = static_cast<int>(tu * warp / kWarps);
+    u1 = static_cast<int>(tu * (warp + 1) / kWarps);
+    const int i = ph.by_item(u0);
+    feed.k = k0 = u0 - i * ph.by_item.d;
+    feed.s = s0 = ph.by_groups(st.ra + i);
+    feed.g = g0 = st.ra + i - s0 * ph.groups;
     feed.left = u1 - u0;
-    if (feed.left > 0) feed.seek(ph, pl, stages, lane);
-    feed.step(ph, pl, stages, ring(), lane);
+    if (feed.left > 0) feed.seek(ph, pl, ph.stages, lane);
+    feed.step(ph, pl, ph.stages, ring(), lane);
   }
   __device__ __forceinline__ void start(const MoeArgs& a, const Plan& pl) {
     const Phase& ph = a.ph[!GATE_UP];
-    const unsigned total = static_cast<unsigned>(pl.nseg[!GATE_UP]) * ph.groups;  // at most 2^20
-    r = static_cast<int>(total * blockIdx.x / gridDim.x);
-    r1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
-    stages = FMT == GQ_FMT_Q4_0 ? (ph.K + 255) / 256 : ph.K / 256;
+    const int total = pl.nseg[!GATE_UP] * ph.groups;  // at most 2^20
+    const int each = a.by_grid(total), rest = total - each * static_cast<int>(gridDim.x);
+    const int b = static_cast<int>(blockIdx.x);
+    r = each * b + a.by_grid(rest * b);
+    r1 = each * (b + 1) + a.by_grid(rest * (b + 1));
     next(a, ph, pl);
   }
 };
@@ -529,7 +542,7 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
   // columns past the last repeat existing ones (or hold what was there); their sums are not used
   const uint8_t* xb = msm + pl.boff[local] + (g8 & (CP - 1)) * 64 + t * 16;
-  const int stages = wk.stages, all = wk.item_stages();
+  const int stages = ph.stages, all = ph.by_item.d;
   float acc[4] = {}, gate[4] = {};
   unsigned top[2] = {0u, 0u};  // largest |h| of this lane's tokens
   int kk = GATE_UP && k >= stages ? k - stages : k;
@@ -607,47 +620,48 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
   }
 }
 
-// After the last stage of a string: an item that this warp began and did not
-// end takes the later warps' parts in order; then the sizes of h.
+// After the last stage of a string (stage `u1` of the string would follow): the
+// item that this warp began and did not end (`cut`: row group g of segment sg,
+// `end` its last stage + 1) takes the later warps' parts in order.
 template <int FMT, bool GATE_UP>
-__device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Plan& pl, const String& st, int u0,
-                                           int u1, int all) {
+__device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Plan& pl, const String& st, bool cut,
+                                           const Seg& sg, int local, int g, unsigned u1, unsigned end) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tu = (st.rb - st.ra) * all;
+  const unsigned tu = (st.rb - st.ra) * ph.by_item.d;
   __syncthreads();  // the parts are there; nobody reads B any more
-  const int last = st.ra + (u1 - 1) / all;  // this warp's last item
-  const int begin = (last - st.ra) * all;
-  if (u1 > u0 && begin >= u0 && u1 < begin + all) {
-    const int s = last / ph.groups, local = s - st.seg0;
-    const Seg sg = pl.seg[!GATE_UP][s];
+  if (cut) {
     const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
     const int row = lane & 15, half = lane >> 4;
     // gate and up: each half of the warp one matrix; down: every other token
     for (int c0 = 0; c0 < sg.n; c0 += GATE_UP ? 1 : 2) {
       const int c = GATE_UP ? c0 : min(c0 + half, sg.n - 1);
-      const int at = ((GATE_UP ? half * 16 : 0) + row) * pitch + (ph.two ? 2 * c : c);
-      float v = 0.f;
-      for (int w = warp; w < kWarps && tu * w / kWarps < begin + all; ++w) {
-        if (tu * w / kWarps == tu * (w + 1) / kWarps) continue;  // no stages
-        const float* d = part_at(a, ph, w, w == warp) + at;
-        v += ph.two ? d[0] + d[1] : d[0];
+      const float* d = part_at(a, ph, warp, 1) + ((GATE_UP ? half * 16 : 0) + row) * pitch + (ph.two ? 2 * c : c);
+      float v = ph.two ? d[0] + d[1] : d[0];
+      d += ph.part;  // the next warp's part 0
+      unsigned begin = u1;
+      for (unsigned w = warp + 1; begin < end; ++w) {
+        const unsigned next = tu * (w + 1) / kWarps;
+        if (next > begin) v += ph.two ? d[0] + d[1] : d[0];  // (a warp without stages has no part)
+        begin = next;
+        d += 2 * ph.part;
       }
       v *= pl.inv[local][c];
       const float up = __shfl_down_sync(0xFFFFFFFFu, v, 16);
       unsigned m = 0;
-      if (GATE_UP ? half == 0 : c0 + half < sg.n)
-        m = put<GATE_UP>(a, ph, pl, sg, c, 16 * (last - s * ph.groups) + row, v, up);
+      if (GATE_UP ? half == 0 : c0 + half < sg.n) m = put<GATE_UP>(a, ph, pl, sg, c, 16 * g + row, v, up);
       if (GATE_UP) {
         m = __reduce_max_sync(0xFFFFFFFFu, m);
         if (lane == 0) atomicMax(&pl.hmax[local][c], m);
       }
     }
   }
-  __syncthreads();
-  if (GATE_UP && threadIdx.x < st.segs * kMaxCols) {
-    const int i = threadIdx.x / kMaxCols, c = threadIdx.x % kMaxCols;
-    const Seg sg = pl.seg[0][st.seg0 + i];
-    if (c < sg.n) atomicMax(a.hmax + sg.slot0 + c, pl.hmax[i][c]);
+  if (GATE_UP) {
+    __syncthreads();
+    if (threadIdx.x < st.segs * kMaxCols) {
+      const int i = threadIdx.x / kMaxCols, c = threadIdx.x % kMaxCols;
+      const Seg sh = pl.seg[0][st.seg0 + i];
+      if (c < sh.n) atomicMax(a.hmax + sh.slot0 + c, pl.hmax[i][c]);
+    }
   }
 }
 
@@ -655,10 +669,9 @@ __device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Pl
 template <int FMT, bool GATE_UP>
 __device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, GATE_UP>& wk) {
   const Phase& ph = a.ph[!GATE_UP];
-  const int all = wk.item_stages();
+  const int all = ph.by_item.d;
   while (wk.more) {
     const String st = wk.st;
-    const int u0 = wk.u0, u1 = wk.u1;
     int b_off = a.b_off;
     for (int i = 0; i < st.segs; ++i) {
       const Seg sg = pl.seg[!GATE_UP][st.seg0 + i];
@@ -667,28 +680,36 @@ __device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, 
     }
     // the rest of the ring (the first copies went ahead of B: a full ring of them would hold it up)
     for (int d = 1; d < kDepth; ++d)
-      wk.feed.step(ph, pl, wk.stages, wk.ring() + d * kStageBytes, threadIdx.x & 31);
+      wk.feed.step(ph, pl, ph.stages, wk.ring() + d * kStageBytes, threadIdx.x & 31);
     __syncthreads();
-    bool whole = u0 % all == 0;
+    int u = wk.u0, s = wk.s0, g = wk.g0, k = wk.k0;
+    const int u1 = wk.u1;
+    int base = u - k - g * all;  // the stage of the string that segment s begins with
+    bool whole = k == 0;
     uint32_t slot = wk.ring();
-    int u = u0, r = st.ra + u0 / all, k = u0 % all;
+    Seg sg{0, 0, 0};
+    int last_base = 0, last_s = 0;
     while (u < u1) {
-      const int s = r / ph.groups, local = s - st.seg0;
-      const Seg sg = pl.seg[!GATE_UP][s];
-      const int ue = min(u1, (min(st.rb, (s + 1) * ph.groups) - st.ra) * all);
-      const int g = r - s * ph.groups;
+      sg = pl.seg[!GATE_UP][s];
+      const int ue = min(u1, base + ph.groups * all);
       switch (col_pitch(ph.two ? 2 * sg.n : sg.n)) {
-        case 1: stream<FMT, 1, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, slot); break;
-        case 2: stream<FMT, 2, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, slot); break;
-        case 4: stream<FMT, 4, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, slot); break;
-        default: stream<FMT, 8, GATE_UP>(a, ph, pl, wk, sg, local, u, ue, g, k, whole, slot);
+        case 1: stream<FMT, 1, GATE_UP>(a, ph, pl, wk, sg, s - st.seg0, u, ue, g, k, whole, slot); break;
+        case 2: stream<FMT, 2, GATE_UP>(a, ph, pl, wk, sg, s - st.seg0, u, ue, g, k, whole, slot); break;
+        case 4: stream<FMT, 4, GATE_UP>(a, ph, pl, wk, sg, s - st.seg0, u, ue, g, k, whole, slot); break;
+        default: stream<FMT, 8, GATE_UP>(a, ph, pl, wk, sg, s - st.seg0, u, ue, g, k, whole, slot);
       }
       u = ue;
-      r = (s + 1) * ph.groups;
-      k = 0;
+      last_base = base;
+      last_s = s;
+      base += ph.groups * all;
+      ++s;
+      g = k = 0;
     }
+    // the item that the warp's last stage is of
+    const int li = ph.by_item(max(u1 - 1 - last_base, 0)), begin = last_base + li * all;
+    const bool cut = u1 > wk.u0 && begin >= wk.u0 && u1 < begin + all;
     wk.next(a, ph, pl);
-    join_parts<FMT, GATE_UP>(a, ph, pl, st, u0, u1, all);
+    join_parts<FMT, GATE_UP>(a, ph, pl, st, cut, sg, last_s - st.seg0, li, u1, begin + all);
     if (wk.more) __syncthreads();  // before the next string's values
   }
 }
@@ -827,6 +848,11 @@ size_t shape_smem(MoeArgs& a) {
     Phase& ph = t0 >= t1 && a.ph[0].cap > 1 ? a.ph[0] : a.ph[1].cap > 1 ? a.ph[1] : a.ph[0];
     ph.cap /= 2;
   }
+  for (Phase& ph : a.ph) {
+    ph.by_groups = make_div(ph.groups);
+    ph.by_item = make_div((&ph == a.ph ? 2 : 1) * ph.stages);
+    ph.by_vecs = make_div(padded(ph.K) / 8);
+  }
   for (int f = 0; f < 2; ++f) a.ph[f].part = (f == 0 ? 2 : 1) * 16 * a.ph[f].cap * (a.ph[f].two ? 2 : 1);
   a.b_off = kRingBytes;
   a.bbytes = static_cast<int>((left - tab) & ~size_t(15));
@@ -877,12 +903,21 @@ gq_status moe_entry(const void* gate, const void* up, const void* down, int64_t 
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GQ_ERR_ALIGNMENT;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
 
-  const auto row_bytes = [](int64_t K) { return FMT == GQ_FMT_Q4_0 ? K / 32 * 18 : K / 256 * 138; };
   MoeArgs a{};
-  a.ph[0] = Phase{static_cast<const uint8_t*>(gate), static_cast<const uint8_t*>(up), static_cast<int>(H),
-                  static_cast<int>(I / 16), 16 * row_bytes(H), x_dtype == GQ_F32, 0, 0};
-  a.ph[1] = Phase{static_cast<const uint8_t*>(down), nullptr, static_cast<int>(I), static_cast<int>(H / 16),
-                  16 * row_bytes(I), y_dtype == GQ_F32, 0, 0};
+  auto phase = [](const void* w0, const void* w1, int64_t rows, int64_t K, bool two) {
+    Phase ph{};
+    ph.w0 = static_cast<const uint8_t*>(w0);
+    ph.w1 = static_cast<const uint8_t*>(w1);
+    ph.K = static_cast<int>(K);
+    ph.groups = static_cast<int>(rows / 16);
+    ph.stages = static_cast<int>((K + 255) / 256);
+    ph.group_bytes = 16 * (FMT == GQ_FMT_Q4_0 ? K / 32 * 18 : K / 256 * 138);
+    ph.two = two;
+    return ph;
+  };
+  a.ph[0] = phase(gate, up, I, H, x_dtype == GQ_F32);
+  a.ph[1] = phase(down, nullptr, H, I, y_dtype == GQ_F32);
+  a.by_grid = make_div(static_cast<unsigned>(sm_count()));
   a.x = x;
   a.ids = ids;
   a.weights = weights;
