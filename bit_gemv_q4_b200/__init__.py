@@ -509,17 +509,19 @@ def gq_gemv_ksb_tiled_grouped(Ts, Ms, K: int, x: torch.Tensor, y_dtype=torch.flo
 _call_ws: dict = {}
 
 
-def _auto_workspace(name: str, need: int, device: torch.device, stream: int) -> torch.Tensor:
+def _auto_workspace(name: str, need: int, device: torch.device, stream: int):
+    """(tensor, address, bytes) of the call's workspace on `stream`."""
     key = (name, device.index, stream)
     ws = _call_ws.get(key)
-    if ws is None or ws.numel() < need:
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-            ws = torch.zeros(need, dtype=torch.uint8, device=device)
-            # a captured call keeps a workspace of its own, which its graph clears
-            if not torch.cuda.is_current_stream_capturing():
-                _call_ws[key] = ws
-    elif torch.cuda.is_current_stream_capturing():
-        ws = torch.zeros(need, dtype=torch.uint8, device=device)
+    if ws is not None and ws[2] >= need and not torch.cuda.is_current_stream_capturing():
+        return ws
+    # cleared on the call's own stream; a captured call keeps a workspace of its own, which its
+    # graph clears
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        t = torch.zeros(need, dtype=torch.uint8, device=device)
+        ws = (t, t.data_ptr() or None, need)
+        if not torch.cuda.is_current_stream_capturing():
+            _call_ws[key] = ws
     return ws
 
 
@@ -527,12 +529,18 @@ def _on_device(call):
     """Run the call with its first tensor's device as the current one."""
     @functools.wraps(call)
     def wrapped(first, *args, **kw):
-        dev = first.device
-        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-            with torch.cuda.device(dev):
+        if first.is_cuda and first.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
                 return call(first, *args, **kw)
         return call(first, *args, **kw)
     return wrapped
+
+
+@functools.lru_cache(maxsize=4096)
+def _size(name: str, *args) -> int:
+    """A size function of the library, its answers kept (they depend on the arguments and the GPU
+    model alone)."""
+    return int(getattr(lib, name)(*args))
 
 
 def _raw_stream(stream, device: torch.device) -> int:
@@ -545,7 +553,7 @@ def _workspace(name: str, workspace, need: int, device: torch.device, stream: in
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a uint8 CUDA tensor")
-        workspace = _auto_workspace(name, need, device, stream)
+        return _auto_workspace(name, need, device, stream)[1:]
     if workspace is None:
         return None, 0
     return _ptr(workspace), workspace.numel() * workspace.element_size()
@@ -578,14 +586,14 @@ def gq_moe_route(x: torch.Tensor, Wr: torch.Tensor, k: int, bias: torch.Tensor |
         raise ValueError("bias holds E fp32 values")
     s = _raw_stream(stream, x.device)
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
+        ids = x.new_empty((T, k), dtype=torch.int32)
     elif ids.dtype != torch.int32 or ids.numel() != T * k:
         raise ValueError("ids holds T * k int32 values")
     if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=x.device)
+        weights = x.new_empty((T, k), dtype=torch.float32)
     elif weights.dtype != torch.float32 or weights.numel() != T * k:
         raise ValueError("weights holds T * k fp32 values")
-    ws, ws_bytes = _workspace("route", workspace, lib.gq_moe_route_workspace_bytes(T, E), x.device, s)
+    ws, ws_bytes = _workspace("route", workspace, _size("gq_moe_route_workspace_bytes", T, E), x.device, s)
     _check(lib.gq_moe_route(_ptr(x), _DTYPE_CODE[x.dtype], T, H, _ptr(Wr), _DTYPE_CODE[Wr.dtype], E,
                             _ptr(bias), k, scale, _ptr(ids), _ptr(weights), ws, ws_bytes, flags,
                             _ptr(dev_status), s), "gq_moe_route")
@@ -606,15 +614,15 @@ def _moe(name: str, fmt: int, gate, up, down, E: int, I: int, x: torch.Tensor, i
         raise TypeError("ids must be int32 and weights fp32")
     T, H = x.shape
     k = ids.shape[1]
-    gu, dn = lib.gq_tiled_bytes(fmt, E * I, H), lib.gq_tiled_bytes(fmt, E * H, I)
+    gu, dn = _size("gq_tiled_bytes", fmt, E * I, H), _size("gq_tiled_bytes", fmt, E * H, I)
     if gate.numel() < gu or up.numel() < gu or down.numel() < dn:
         raise ValueError("gate, up or down is smaller than the tiled storage of E experts")
     s = _raw_stream(stream, x.device)
     if out is None:
-        out = torch.empty((T, H), dtype=y_dtype, device=x.device)
+        out = x.new_empty((T, H), dtype=y_dtype)
     elif out.dtype not in _DTYPE_CODE or out.numel() != T * H:
         raise ValueError("out holds T * H values")
-    ws, ws_bytes = _workspace(name, workspace, lib.gq_moe_workspace_bytes(fmt, H, I, T, k), x.device, s)
+    ws, ws_bytes = _workspace(name, workspace, _size("gq_moe_workspace_bytes", fmt, H, I, T, k), x.device, s)
     _check(getattr(lib, name)(_ptr(gate), _ptr(up), _ptr(down), E, H, I, _ptr(x), _DTYPE_CODE[x.dtype],
                               T, _ptr(ids), _ptr(weights), k, _ptr(out), _DTYPE_CODE[out.dtype], ws,
                               ws_bytes, flags, _ptr(dev_status), s), name)
@@ -679,9 +687,9 @@ def gq_quantize_fp8(x: torch.Tensor, rows: int, out: torch.Tensor | None = None,
         raise ValueError("rows is 1 or 128")
     R, K = x.shape
     if out is None:
-        out = torch.empty((R, K), dtype=torch.float8_e4m3fn, device=x.device)
+        out = x.new_empty((R, K), dtype=torch.float8_e4m3fn)
     if scales is None:
-        scales = torch.empty((-(-R // rows), -(-K // 128)), dtype=torch.float32, device=x.device)
+        scales = x.new_empty((-(-R // rows), -(-K // 128)), dtype=torch.float32)
     if _fp8_pair(out, scales, rows, "out") != (R, K):
         raise ValueError("out has another shape than x")
     _check(lib.gq_quantize_fp8(_ptr(x), _DTYPE_CODE[x.dtype], R, K, rows, _ptr(out), _ptr(scales),
@@ -697,7 +705,7 @@ def gq_dequantize_fp8(q: torch.Tensor, scales: torch.Tensor, rows: int, dtype=to
     if dtype not in _DTYPE_CODE:
         raise TypeError("outputs must be float32, float16 or bfloat16")
     if out is None:
-        out = torch.empty((R, K), dtype=dtype, device=q.device)
+        out = q.new_empty((R, K), dtype=dtype)
     elif out.dtype not in _DTYPE_CODE or out.numel() != R * K:
         raise ValueError("out holds R * K values")
     _check(lib.gq_dequantize_fp8(_ptr(q), _ptr(scales), R, K, rows, _ptr(out), _DTYPE_CODE[out.dtype],
@@ -725,10 +733,10 @@ def gq_gemm_fp8(W: torch.Tensor, w_scales: torch.Tensor, X: torch.Tensor, x_scal
         raise TypeError("outputs must be float32, float16 or bfloat16")
     s = _raw_stream(stream, X.device)
     if out is None:
-        out = torch.empty((B, M), dtype=y_dtype, device=X.device)
+        out = X.new_empty((B, M), dtype=y_dtype)
     elif out.dtype not in _DTYPE_CODE or out.numel() != B * M:
         raise ValueError("out holds B * M values")
-    ws, ws_bytes = _workspace("gq_gemm_fp8", workspace, lib.gq_gemm_fp8_workspace_bytes(M, K, B), X.device, s)
+    ws, ws_bytes = _workspace("gq_gemm_fp8", workspace, _size("gq_gemm_fp8_workspace_bytes", M, K, B), X.device, s)
     _check(lib.gq_gemm_fp8(_ptr(W), _ptr(w_scales), M, K, _ptr(X), _ptr(x_scales), B, _ptr(out),
                            _DTYPE_CODE[out.dtype], ws, ws_bytes, flags, _ptr(dev_status), s), "gq_gemm_fp8")
     return out
