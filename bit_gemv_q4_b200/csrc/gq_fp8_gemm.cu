@@ -46,10 +46,12 @@ constexpr int kTileX = kBM * kBK;
 constexpr int kMaxCut = 4096;            // tiles of a split call at most
 constexpr size_t kCountBytes = kMaxCut * sizeof(int);
 
-// Unit u of T * S: k-step u % S of tile u / S.  CTA i of P takes [U i / P, U (i + 1) / P).
+// Unit u of T * S: k-step u % S of tile u / S.  CTA i of P takes units [U i / P, U (i + 1) / P),
+// or with `whole` the tiles i, i + P, ...
 struct Split {
   int64_t U;
   int S, T, P;
+  int whole;
   int tm;  // tiles along M; tile t covers tokens 128 (t / tm) and weight rows BN (t % tm)
 };
 
@@ -144,10 +146,17 @@ __device__ __forceinline__ int unit_owner(const Split& sp, int64_t u) {
 // The tiles of a CTA's run and the k-steps of each: a cut first or last tile
 // before the whole ones between them, so that cut tiles complete early.
 struct Run {
-  int ta, tb, S;
+  int ta, tb, S, stride;
   int64_t u0, u1;
-  __device__ __forceinline__ int count() const { return tb - ta + 1; }
+  __device__ __forceinline__ int count() const { return (tb - ta) / stride + 1; }
+  __device__ __forceinline__ int64_t steps() const { return stride > 1 ? static_cast<int64_t>(count()) * S : u1 - u0; }
   __device__ __forceinline__ void get(int k, int& t, int& k0, int& k1) const {
+    if (stride > 1) {
+      t = ta + k * stride;
+      k0 = 0;
+      k1 = S;
+      return;
+    }
     t = (k == 0) ? ta : (k == 1) ? tb : ta + k - 1;
     k0 = (t == ta) ? static_cast<int>(u0 - static_cast<int64_t>(ta) * S) : 0;
     k1 = (t == tb) ? static_cast<int>(u1 - static_cast<int64_t>(tb) * S) : S;
@@ -156,6 +165,14 @@ struct Run {
 __device__ __forceinline__ Run run_of(const Split& sp, int i) {
   Run r;
   r.S = sp.S;
+  r.stride = 1;
+  if (sp.whole) {  // at least two CTAs
+    r.ta = i;
+    r.tb = sp.T - 1;
+    r.stride = sp.P;
+    r.u0 = r.u1 = 0;
+    return r;
+  }
   r.u0 = unit_begin(sp, i);
   r.u1 = unit_begin(sp, i + 1);
   r.ta = static_cast<int>(r.u0 / sp.S);
@@ -257,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_e4m3(kBM, BN);
       bool ok = true;
-      const int64_t steps = run.u1 - run.u0;
+      const int64_t steps = run.steps();
       for (int64_t g = 0; g < steps; ++g) {
         const int s = static_cast<int>(g % kStages), buf = static_cast<int>(g & 1);
         if (!mbar_wait(&full[s], static_cast<uint32_t>(g / kStages) & 1u, a.budget) ||
@@ -304,32 +321,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* sx = a.sx + static_cast<int64_t>(row_ok ? row : 0) * a.kblocks;
       const int64_t wb = min((m0 + cols0) / 128, (a.M - 1) / 128);  // this half's weight block
       const float* sw = a.sw + wb * a.kblocks;
-      float acc[kHalf];
+      float2 acc2[kHalf / 2];
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
-      float f = __ldg(sx + k0) * __ldg(sw + k0);
+      for (int i = 0; i < kHalf / 2; ++i) acc2[i] = make_float2(0.f, 0.f);
+      float* acc = reinterpret_cast<float*>(acc2);
+      // the scales of this step and the next two (their loads take longer than a step)
+      const int kl = k1 - 1;
+      float sx0 = __ldg(sx + k0), sw0 = __ldg(sw + k0);
+      float sx1 = __ldg(sx + min(k0 + 1, kl)), sw1 = __ldg(sw + min(k0 + 1, kl));
       for (int ks = k0; ks < k1; ++ks, ++g) {
         const int buf = g & 1;
-        const float fnext = ks + 1 < k1 ? __ldg(sx + ks + 1) * __ldg(sw + ks + 1) : 0.f;
+        const float sx2 = __ldg(sx + min(ks + 2, kl)), sw2 = __ldg(sw + min(ks + 2, kl));
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&d_full[buf], (g >> 1) & 1u, a.budget)) || aborted()) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (any) {
+          // 16 columns at a time: the next ones are on their way while these are added
+          const float2 f = make_float2(sx0 * sw0, sx0 * sw0);
+          const uint32_t src = tmem + lane_base + static_cast<uint32_t>(buf * BN + cols0);
+          uint32_t v[2][16];
+          tmem_ld16(src, v[0]);
 #pragma unroll
-          for (int c = 0; c < kHalf; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(tmem + lane_base + static_cast<uint32_t>(buf * BN + cols0 + c), v);
+          for (int c = 0; c < kHalf / 16; ++c) {
             tmem_wait_ld();
+            if (c + 1 < kHalf / 16) {
+              tmem_ld16(src + 16 * (c + 1), v[(c + 1) & 1]);
+            } else {  // the buffer is free
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&d_empty[buf]);
+            }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(f, __uint_as_float(v[i]), acc[c + i]);
+            for (int i = 0; i < 8; ++i)
+              acc2[8 * c + i] = __ffma2_rn(f, make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])),
+                                           acc2[8 * c + i]);
           }
+        } else if (lane == 0) {
+          mbar_arrive(&d_empty[buf]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&d_empty[buf]);
-        f = fnext;
+        sx0 = sx1, sw0 = sw1;
+        sx1 = sx2, sw1 = sw2;
       }
       if (!ok) break;
       if (k1 - k0 == a.sp.S) {
@@ -400,24 +433,25 @@ struct Choice {
 Choice choose(int64_t M, int64_t K, int64_t B) {
   const int64_t sms = sm_count();
   const int64_t tb = (B + kBM - 1) / kBM, S = (K + kBK - 1) / kBK;
-  auto split = [&](int bn, int64_t p) {
+  auto split = [&](int bn, bool whole) {
     Split s;
     s.S = static_cast<int>(S);
     s.tm = static_cast<int>((M + bn - 1) / bn);
     s.T = static_cast<int>(tb * s.tm);
     s.U = tb * s.tm * S;
-    s.P = static_cast<int>(i64min(p, s.U));
+    s.P = static_cast<int>(i64min(sms, whole ? s.T : s.U));
+    s.whole = whole && s.P > 1;
     return s;
   };
   const int64_t t256 = tb * ((M + 255) / 256), t128 = tb * ((M + 127) / 128);
-  if (t256 >= 2 * sms) return Choice{256, split(256, t256)};
-  if (t128 > sms) return Choice{128, split(128, t128)};
-  if (10 * t128 >= 8 * sms && B > 64) return Choice{128, split(128, t128)};
-  return Choice{128, split(128, sms)};
+  if (t256 >= 2 * sms) return Choice{256, split(256, true)};
+  if (t128 > sms) return Choice{128, split(128, true)};
+  if (10 * t128 >= 8 * sms && B > 64) return Choice{128, split(128, true)};
+  return Choice{128, split(128, false)};
 }
 
 size_t ws_bytes_of(const Choice& c, int64_t B) {
-  if (c.sp.P == c.sp.T) return kCountBytes;  // whole tiles: no parts
+  if (c.sp.whole || c.sp.T == 1 && c.sp.P == 1) return kCountBytes;  // no parts
   const int64_t rows = B < kBM ? B : kBM;
   return kCountBytes + static_cast<size_t>(c.sp.P) * 2 * static_cast<size_t>(rows) * c.bn * sizeof(float);
 }
