@@ -80,6 +80,17 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
       : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B (both K-major), fp32 D.
 constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
@@ -271,25 +282,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kEpiWarps + 1) {
     // --------------------------------------------------------------- MMA
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(kBM, BN);
-      bool ok = true;
-      const int64_t steps = run.steps();
-      for (int64_t g = 0; g < steps; ++g) {
-        const int s = static_cast<int>(g % kStages), buf = static_cast<int>(g & 1);
-        if (!mbar_wait(&full[s], static_cast<uint32_t>(g / kStages) & 1u, a.budget) ||
-            !mbar_wait(&d_empty[buf], (static_cast<uint32_t>(g >> 1) & 1u) ^ 1u, a.budget) || aborted()) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t xs = base + ring + s * C::kStageBytes, wsm = xs + kTileX;
+    // The whole warp runs the loop and one elected lane issues: the
+    // descriptors are then warp-uniform for the compiler, too.  (In a branch of
+    // one lane each MMA took about 160 cycles to issue.)
+    constexpr uint32_t idesc = idesc_e4m3(kBM, BN);
+    bool ok = true;
+    const int64_t steps = run.steps();
+    int s = 0;
+    uint32_t phase = 0;
+    for (int64_t g = 0; g < steps; ++g) {
+      const int buf = static_cast<int>(g & 1);
+      ok = mbar_wait(&full[s], phase, a.budget) &&
+           mbar_wait(&d_empty[buf], (static_cast<uint32_t>(g >> 1) & 1u) ^ 1u, a.budget) && !aborted();
+      if (!__all_sync(0xFFFFFFFFu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint64_t xd = umma_desc_sw128(base + ring + s * C::kStageBytes);
+      const uint64_t wd = umma_desc_sw128(base + ring + s * C::kStageBytes + kTileX);
+      if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < kBK / 32; ++i)
-          umma_e4m3(tmem + buf * BN, umma_desc_sw128(xs + 32 * i), umma_desc_sw128(wsm + 32 * i), idesc, i != 0);
+        for (int i = 0; i < kBK / 32; ++i) umma_e4m3(tmem + buf * BN, xd + 2 * i, wd + 2 * i, idesc, i != 0);
         umma_commit(&empty[s]);
         umma_commit(&d_full[buf]);
       }
+      __syncwarp();
+      if (++s == kStages) {
+        s = 0;
+        phase ^= 1u;
+      }
+    }
+    if (elect_one()) {
       if (!ok) fail();
       umma_commit(done);  // also on the abort path: tensor memory is quiet before exit
     }
