@@ -14,6 +14,8 @@
 //  * warp 8 (producer): both operands' 128-byte rows by TMA, 128-byte swizzle;
 //  * warp 9 (MMA): four tcgen05.mma (K = 32) to a k-step, into one of two
 //    accumulator buffers in tensor memory;
+//  * warp 10 (scales): the factors of four k-steps at a time, ahead of their
+//    use, into shared memory;
 //  * warps 0..7: read the buffer back and add it, times the factor, to sums in
 //    registers (a thread holds one token and BN / 2 columns); at the end of a
 //    tile they round once and store.
@@ -41,7 +43,10 @@ namespace {
 constexpr int kBM = 128;                 // tokens of a tile
 constexpr int kBK = 128;                 // bytes of K in a step: one group of scales
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kThreads = 32 * (kEpiWarps + 3);
+constexpr int kFactorSteps = 4;          // k-steps of a slot of factors
+constexpr int kFactorSlots = 3;
+constexpr int kFactorBytes = kFactorSlots * kFactorSteps * 2 * kBM * 4;  // for each half of the columns
 constexpr int kTileX = kBM * kBK;
 constexpr int kMaxCut = 4096;            // tiles of a split call at most
 constexpr size_t kCountBytes = kMaxCut * sizeof(int);
@@ -195,7 +200,7 @@ template <int BN>
 struct Cfg {
   static constexpr int kStageBytes = kTileX + BN * kBK;
   static constexpr int kStages = BN == 256 ? 4 : 6;
-  static constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
+  static constexpr int kSmem = kStages * kStageBytes + kFactorBytes + 1024 + 256;
 };
 
 template <int BN>
@@ -206,12 +211,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kStages = C::kStages, kHalf = BN / 2;
   const uint32_t base = smem_addr(fsm);
   const uint32_t ring = ((base + 1023u) & ~1023u) - base;
-  uint64_t* full = reinterpret_cast<uint64_t*>(fsm + ring + kStages * C::kStageBytes);
+  float* factors = reinterpret_cast<float*>(fsm + ring + kStages * C::kStageBytes);  // [slot][step][half][token]
+  uint64_t* full = reinterpret_cast<uint64_t*>(fsm + ring + kStages * C::kStageBytes + kFactorBytes);
   uint64_t* empty = full + kStages;
   uint64_t* d_full = empty + kStages;  // [2] a group's sums are in the buffer
   uint64_t* d_empty = d_full + 2;      // [2] they have been read
   uint64_t* done = d_empty + 2;        // every MMA of the CTA has finished
-  uint64_t* e_bar = done + 1;
+  uint64_t* f_full = done + 1;         // [slots] factors
+  uint64_t* f_empty = f_full + kFactorSlots;
+  uint64_t* e_bar = f_empty + kFactorSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(e_bar + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   int* last_flag = abort_flag + 1;
@@ -227,6 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&d_full[i], 1);
       mbar_init(&d_empty[i], kEpiWarps);
+    }
+    for (int i = 0; i < kFactorSlots; ++i) {
+      mbar_init(&f_full[i], 1);
+      mbar_init(&f_empty[i], kEpiWarps);
     }
     mbar_init(done, 1);
     mbar_init(e_bar, kEpiWarps);
@@ -318,6 +330,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit(done);  // also on the abort path: tensor memory is quiet before exit
     }
     __syncwarp();
+  } else if (warp == kEpiWarps + 2) {
+    // ------------------------------------------------------------- scales
+    // Four k-steps of a tile at a time; a lane has four tokens.
+    bool ok = true;
+    int q = 0;  // slots filled
+    for (int k = 0; k < nrun && ok; ++k) {
+      int t, k0, k1;
+      run.get(k, t, k0, k1);
+      const int row0 = (t / a.sp.tm) * kBM;
+      const int64_t m0 = static_cast<int64_t>(t % a.sp.tm) * BN, last = (a.M - 1) / 128;
+      const float* swl = a.sw + min(m0 / 128, last) * a.kblocks;
+      const float* swh = a.sw + min((m0 + BN / 2) / 128, last) * a.kblocks;
+      for (int ks = k0; ks < k1; ks += kFactorSteps, ++q) {
+        float x[4][kFactorSteps], lo[kFactorSteps], hi[kFactorSteps];
+#pragma unroll
+        for (int j = 0; j < kFactorSteps; ++j) {
+          const int kj = min(ks + j, k1 - 1);
+          lo[j] = __ldg(swl + kj);
+          hi[j] = __ldg(swh + kj);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = min(row0 + lane + 32 * i, a.B - 1);
+            x[i][j] = __ldg(a.sx + static_cast<int64_t>(row) * a.kblocks + kj);
+          }
+        }
+        const int slot = q % kFactorSlots;
+        ok = mbar_wait(&f_empty[slot], ((q / kFactorSlots) & 1u) ^ 1u, a.budget) && !aborted();
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        float* f = factors + slot * (kFactorSteps * 2 * kBM) + lane;
+#pragma unroll
+        for (int j = 0; j < kFactorSteps; ++j) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[(2 * j) * kBM + 32 * i] = x[i][j] * lo[j];
+            f[(2 * j + 1) * kBM + 32 * i] = x[i][j] * hi[j];
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&f_full[slot]);
+      }
+    }
+    if (!ok && lane == 0) fail();
   } else {
     // ---------------------------------------------------------- epilogue
     const int quarter = warp & 3, half = warp >> 2;
@@ -333,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return r;
     };
     bool ok = true;
-    uint32_t g = 0;
+    uint32_t g = 0, fq = 0;  // k-steps and slots of factors done
     for (int k = 0; k < nrun && ok; ++k) {
       int t, k0, k1;
       run.get(k, t, k0, k1);
@@ -342,28 +399,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = row0 + 32 * quarter + lane;
       const bool row_ok = row < a.B;
       const bool any = row0 + 32 * quarter < a.B;  // some lane of the warp has a token
-      const float* sx = a.sx + static_cast<int64_t>(row_ok ? row : 0) * a.kblocks;
-      const int64_t wb = min((m0 + cols0) / 128, (a.M - 1) / 128);  // this half's weight block
-      const float* sw = a.sw + wb * a.kblocks;
       float2 acc2[kHalf / 2];
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) acc2[i] = make_float2(0.f, 0.f);
       float* acc = reinterpret_cast<float*>(acc2);
-      // the scales of this step and the next two (their loads take longer than a step)
-      const int kl = k1 - 1;
-      float sx0 = __ldg(sx + k0), sw0 = __ldg(sw + k0);
-      float sx1 = __ldg(sx + min(k0 + 1, kl)), sw1 = __ldg(sw + min(k0 + 1, kl));
       for (int ks = k0; ks < k1; ++ks, ++g) {
         const int buf = g & 1;
-        const float sx2 = __ldg(sx + min(ks + 2, kl)), sw2 = __ldg(sw + min(ks + 2, kl));
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&d_full[buf], (g >> 1) & 1u, a.budget)) || aborted()) {
+        const int fs = fq % kFactorSlots, fj = (ks - k0) % kFactorSteps;
+        bool got = fj != 0 || mbar_wait(&f_full[fs], (fq / kFactorSlots) & 1u, a.budget);
+        const float fac = factors[((fs * kFactorSteps + fj) * 2 + half) * kBM + 32 * quarter + lane];
+        got = got && mbar_wait(&d_full[buf], (g >> 1) & 1u, a.budget);
+        if (!__all_sync(0xFFFFFFFFu, got) || aborted()) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (any) {
           // 16 columns at a time: the next ones are on their way while these are added
-          const float2 f = make_float2(sx0 * sw0, sx0 * sw0);
+          const float2 f = make_float2(fac, fac);
           const uint32_t src = tmem + lane_base + static_cast<uint32_t>(buf * BN + cols0);
           uint32_t v[2][16];
           tmem_ld16(src, v[0]);
@@ -385,8 +438,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (lane == 0) {
           mbar_arrive(&d_empty[buf]);
         }
-        sx0 = sx1, sw0 = sw1;
-        sx1 = sx2, sw1 = sw2;
+        if (fj == kFactorSteps - 1 || ks + 1 == k1) {
+          __syncwarp();  // every lane has its factor
+          if (lane == 0) mbar_arrive(&f_empty[fs]);
+          ++fq;
+        }
       }
       if (!ok) break;
       if (k1 - k0 == a.sp.S) {
