@@ -21,6 +21,13 @@
 //    tile they round once and store.
 // While the warps add one group the MMAs fill the other buffer.
 //
+// With many tiles two CTAs of a cluster share one of 256 tokens x 256 weight
+// rows (cta_group::2): each holds its 128 tokens and half of the weight rows, so
+// that a k-step takes 64 KB of shared-memory traffic in each instead of 96 KB
+// (writes and the MMAs' reads at 128 bytes a cycle, beside 512 cycles of MMA).
+// The leader's MMA warp issues for both; loads of both count on its barriers,
+// commits arrive at both CTAs', and both epilogues release its buffers.
+//
 // When tiles are few, the k-steps of all tiles are divided evenly over the SMs
 // and a tile cut between CTAs is joined through fp32 partial sums in the
 // workspace: the CTA that completes it adds the parts in CTA order, so results
@@ -196,18 +203,83 @@ __device__ __forceinline__ Run run_of(const Split& sp, int i) {
   return r;
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 struct Cfg {
-  static constexpr int kStageBytes = kTileX + BN * kBK;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kRowsW = PAIR ? BN / 2 : BN;  // weight rows in this CTA's shared memory
+  static constexpr int kStageBytes = kTileX + kRowsW * kBK;
+  static constexpr int kStages = kRowsW == 256 ? 4 : 6;
   static constexpr int kSmem = kStages * kStageBytes + kFactorBytes + 1024 + 256;
 };
 
-template <int BN>
+// ------------------------------------------------------------ pairs of CTAs
+// The pair's forms of the tensor-core and TMA operations (no multicast loads).
+template <bool PAIR>
+__device__ __forceinline__ void acc_alloc(uint32_t* dst, uint32_t ncols) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)),
+                 "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst, ncols);
+    tmem_relinquish();
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void acc_dealloc(uint32_t taddr, uint32_t ncols) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+  else
+    tmem_dealloc(taddr, ncols);
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    umma_e4m3(d, a, b, idesc, accumulate);
+}
+// Arrives at `bar` (of both CTAs) when the MMAs issued so far have finished.
+template <bool PAIR>
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    umma_commit(bar);
+}
+// Loads a box into this CTA's shared memory, counted on the leader's barrier.
+template <bool PAIR>
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(cluster_map(smem_addr(bar), 0))
+        : "memory");
+  else
+    tma_load_2d(dst, map, x, y, bar);
+}
+
+// Arrives on the leader's barrier.  Only tensor-memory reads are ordered by it
+// (tcgen05 fences on both sides), so the release stays at CTA scope: at cluster
+// scope it waited for the warp's stores, 1000 cycles a k-step.
+__device__ __forceinline__ void leader_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_map(smem_addr(bar), 0)) : "memory");
+}
+
+template <int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                     const Args a) {
-  using C = Cfg<BN>;
+  using C = Cfg<BN, PAIR>;
   constexpr int kStages = C::kStages, kHalf = BN / 2;
   const uint32_t base = smem_addr(fsm);
   const uint32_t ring = ((base + 1023u) & ~1023u) - base;
@@ -225,7 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* last_flag = abort_flag + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Run run = run_of(a.sp, blockIdx.x);
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const Run run = run_of(a.sp, PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x));
+  constexpr int kRows = PAIR ? 2 * kBM : kBM;  // tokens of a tile
   const int nrun = run.count();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -234,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], kEpiWarps);
+      mbar_init(&d_empty[i], PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     for (int i = 0; i < kFactorSlots; ++i) {
       mbar_init(&f_full[i], 1);
@@ -246,11 +320,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   if (warp == kEpiWarps + 1) {
-    tmem_alloc(tmem_slot, 2 * BN);
-    tmem_relinquish();
+    acc_alloc<PAIR>(tmem_slot, 2 * BN);
   }
   tc_fence_before();
-  __syncthreads();
+  if (PAIR) cluster_sync_all();  // both CTAs' barriers are there
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   auto aborted = [&]() { return *reinterpret_cast<volatile int*>(abort_flag) != 0; };
@@ -266,11 +340,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       bool ok = true;
       int g = 0;
-      const uint32_t bytes = static_cast<uint32_t>(a.xrows * kBK + BN * kBK);
+      const uint32_t bytes = static_cast<uint32_t>(a.xrows * kBK + C::kRowsW * kBK) * (PAIR ? 2 : 1);
       for (int k = 0; k < nrun && ok; ++k) {
         int t, k0, k1;
         run.get(k, t, k0, k1);
-        const int row0 = (t / a.sp.tm) * kBM, m0 = (t % a.sp.tm) * BN;
+        const int row0 = (t / a.sp.tm) * kRows + rank * kBM, m0 = (t % a.sp.tm) * BN + rank * C::kRowsW;
         for (int ks = k0; ks < k1; ++ks, ++g) {
           const int s = g % kStages;
           if (!mbar_wait(&empty[s], ((g / kStages) & 1u) ^ 1u, a.budget) || aborted()) {
@@ -278,14 +352,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           uint8_t* st = fsm + ring + s * C::kStageBytes;
-          mbar_arrive_expect_tx(&full[s], bytes);
-          tma_load_2d(st, &xmap, ks * kBK, row0, &full[s]);
-          tma_load_2d(st + kTileX, &wmap, ks * kBK, m0, &full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+          load_box<PAIR>(st, &xmap, ks * kBK, row0, &full[s]);
+          load_box<PAIR>(st + kTileX, &wmap, ks * kBK, m0, &full[s]);
         }
       }
       if (!ok) fail();
-      // every issued copy lands before shared memory is released
-      for (int i = max(0, g - kStages); i < g; ++i)
+      // every issued copy lands before shared memory is released (a pair's count in the leader)
+      for (int i = max(0, g - kStages); i < g && rank == 0; ++i)
         if (!mbar_wait(&full[i % kStages], (i / kStages) & 1u, a.budget)) {
           report(a.dev_status, GQ_DEV_TIMEOUT);
           break;
@@ -297,15 +371,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The whole warp runs the loop and one elected lane issues: the
     // descriptors are then warp-uniform for the compiler, too.  (In a branch of
     // one lane each MMA took about 160 cycles to issue.)
-    constexpr uint32_t idesc = idesc_e4m3(kBM, BN);
+    constexpr uint32_t idesc = idesc_e4m3(kRows, BN);
     bool ok = true;
-    const int64_t steps = run.steps();
+    const int64_t steps = rank == 0 ? run.steps() : 0;
     int s = 0;
     uint32_t phase = 0;
     for (int64_t g = 0; g < steps; ++g) {
       const int buf = static_cast<int>(g & 1);
-      ok = mbar_wait(&full[s], phase, a.budget) &&
-           mbar_wait(&d_empty[buf], (static_cast<uint32_t>(g >> 1) & 1u) ^ 1u, a.budget) && !aborted();
+      const uint32_t dphase = (static_cast<uint32_t>(g >> 1) & 1u) ^ 1u;
+      ok = mbar_wait(&full[s], phase, a.budget) && mbar_wait(&d_empty[buf], dphase, a.budget) && !aborted();
       if (!__all_sync(0xFFFFFFFFu, ok)) {
         ok = false;
         break;
@@ -315,9 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t wd = umma_desc_sw128(base + ring + s * C::kStageBytes + kTileX);
       if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < kBK / 32; ++i) umma_e4m3(tmem + buf * BN, xd + 2 * i, wd + 2 * i, idesc, i != 0);
-        umma_commit(&empty[s]);
-        umma_commit(&d_full[buf]);
+        for (int i = 0; i < kBK / 32; ++i) mma_step<PAIR>(tmem + buf * BN, xd + 2 * i, wd + 2 * i, idesc, i != 0);
+        mma_commit<PAIR>(&empty[s]);
+        mma_commit<PAIR>(&d_full[buf]);
       }
       __syncwarp();
       if (++s == kStages) {
@@ -325,9 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         phase ^= 1u;
       }
     }
-    if (elect_one()) {
+    if (rank == 0 && elect_one()) {
       if (!ok) fail();
-      umma_commit(done);  // also on the abort path: tensor memory is quiet before exit
+      mma_commit<PAIR>(done);  // also on the abort path: tensor memory is quiet before exit
     }
     __syncwarp();
   } else if (warp == kEpiWarps + 2) {
@@ -338,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < nrun && ok; ++k) {
       int t, k0, k1;
       run.get(k, t, k0, k1);
-      const int row0 = (t / a.sp.tm) * kBM;
+      const int row0 = (t / a.sp.tm) * kRows + rank * kBM;
       const int64_t m0 = static_cast<int64_t>(t % a.sp.tm) * BN, last = (a.M - 1) / 128;
       const float* swl = a.sw + min(m0 / 128, last) * a.kblocks;
       const float* swh = a.sw + min((m0 + BN / 2) / 128, last) * a.kblocks;
@@ -389,12 +463,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++ephase;
       return r;
     };
+    auto release = [&](int buf) {  // the buffer may be filled again
+      if (PAIR) leader_arrive(&d_empty[buf]);
+      else mbar_arrive(&d_empty[buf]);
+    };
     bool ok = true;
     uint32_t g = 0, fq = 0;  // k-steps and slots of factors done
     for (int k = 0; k < nrun && ok; ++k) {
       int t, k0, k1;
       run.get(k, t, k0, k1);
-      const int row0 = (t / a.sp.tm) * kBM;
+      const int row0 = (t / a.sp.tm) * kRows + rank * kBM;
       const int64_t m0 = static_cast<int64_t>(t % a.sp.tm) * BN;
       const int row = row0 + 32 * quarter + lane;
       const bool row_ok = row < a.B;
@@ -428,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {  // the buffer is free
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&d_empty[buf]);
+              if (lane == 0) release(buf);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -436,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            acc2[8 * c + i]);
           }
         } else if (lane == 0) {
-          mbar_arrive(&d_empty[buf]);
+          release(buf);
         }
         if (fj == kFactorSteps - 1 || ks + 1 == k1) {
           __syncwarp();  // every lane has its factor
@@ -491,47 +569,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) fail();
   }
 
-  // teardown: every MMA has finished before tensor memory is freed
+  // teardown: every MMA has finished before tensor memory is freed, and a
+  // pair's CTAs leave together
   tc_fence_before();
   __syncthreads();
   if (warp == kEpiWarps + 1) {
     if (lane == 0 && !mbar_wait(done, 0, a.budget)) report(a.dev_status, GQ_DEV_TIMEOUT);
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * BN);
   }
+  if (PAIR) cluster_sync_all();
+  if (warp == kEpiWarps + 1) acc_dealloc<PAIR>(tmem, 2 * BN);
 }
 
 // ------------------------------------------------------------------- host
-// Tiles of 128 x 256 run the tensor core best (fewer shared-memory reads for
-// each multiply-add) and are taken when there are enough of them; otherwise
+// Tiles of a pair of CTAs run the tensor core best (less shared-memory traffic
+// for each multiply-add) and are taken when there are enough of them; otherwise
 // tiles of 128 x 128, whole ones if they fill most of the SMs, else cut.
 struct Choice {
   int bn;
+  bool pair;
   Split sp;
 };
 Choice choose(int64_t M, int64_t K, int64_t B) {
   const int64_t sms = sm_count();
-  const int64_t tb = (B + kBM - 1) / kBM, S = (K + kBK - 1) / kBK;
-  auto split = [&](int bn, bool whole) {
+  const int64_t S = (K + kBK - 1) / kBK;
+  auto split = [&](int rows, int bn, int64_t ctas, bool whole) {
     Split s;
     s.S = static_cast<int>(S);
     s.tm = static_cast<int>((M + bn - 1) / bn);
-    s.T = static_cast<int>(tb * s.tm);
-    s.U = tb * s.tm * S;
-    s.P = static_cast<int>(i64min(sms, whole ? s.T : s.U));
+    s.T = static_cast<int>((B + rows - 1) / rows * s.tm);
+    s.U = static_cast<int64_t>(s.T) * S;
+    s.P = static_cast<int>(i64min(ctas, whole ? s.T : s.U));
     s.whole = whole && s.P > 1;
     return s;
   };
-  const int64_t t256 = tb * ((M + 255) / 256), t128 = tb * ((M + 127) / 128);
-  if (t256 >= 2 * sms) return Choice{256, split(256, true)};
-  if (t128 > sms) return Choice{128, split(128, true)};
-  if (10 * t128 >= 8 * sms && B > 64) return Choice{128, split(128, true)};
-  return Choice{128, split(128, false)};
+  const int64_t tpair = (B + 255) / 256 * ((M + 255) / 256), t128 = (B + 127) / 128 * ((M + 127) / 128);
+  if (tpair >= sms && B > 128) return Choice{256, true, split(256, 256, sms / 2, true)};
+  if (t128 > sms || (10 * t128 >= 8 * sms && B > 64)) return Choice{128, false, split(128, 128, sms, true)};
+  return Choice{128, false, split(128, 128, sms, false)};
 }
 
 size_t ws_bytes_of(const Choice& c, int64_t B) {
-  if (c.sp.whole || c.sp.T == 1 && c.sp.P == 1) return kCountBytes;  // no parts
+  if (c.sp.whole || c.sp.P == 1) return kCountBytes;  // no parts
   const int64_t rows = B < kBM ? B : kBM;
   return kCountBytes + static_cast<size_t>(c.sp.P) * 2 * static_cast<size_t>(rows) * c.bn * sizeof(float);
 }
@@ -556,17 +636,21 @@ gq_status encode(CUtensorMap* map, const void* p, int64_t rows, int64_t K, int b
              : GQ_ERR_CUDA;
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 gq_status launch_fp8(const CUtensorMap& xmap, const CUtensorMap& wmap, const Args& a, bool pdl, cudaStream_t s) {
-  auto kern = fp8_gemm_kernel<BN>;
+  auto kern = fp8_gemm_kernel<BN, PAIR>;
+  constexpr int smem = Cfg<BN, PAIR>::kSmem;
   thread_local unsigned long long configured_ctx = 0;  // per host thread and context
   const unsigned long long ctx = context_id();
   if (ctx == 0 || ctx != configured_ctx) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return GQ_ERR_CUDA;
     configured_ctx = ctx;
   }
-  return launch(kern, dim3(static_cast<unsigned>(a.sp.P)), dim3(kThreads), Cfg<BN>::kSmem, s, pdl, xmap, wmap, a);
+  if (PAIR)
+    return launch_cluster(kern, dim3(static_cast<unsigned>(2 * a.sp.P)), dim3(kThreads), smem, s, pdl, 2u, xmap,
+                          wmap, a);
+  return launch(kern, dim3(static_cast<unsigned>(a.sp.P)), dim3(kThreads), smem, s, pdl, xmap, wmap, a);
 }
 
 }  // namespace
@@ -621,10 +705,10 @@ GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, in
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCountBytes);
   CUtensorMap xmap, wmap;
   gq_status st = encode(&xmap, X, B, K, a.xrows);
-  if (st == GQ_OK) st = encode(&wmap, W, M, K, c.bn);
+  if (st == GQ_OK) st = encode(&wmap, W, M, K, 128);
   if (st != GQ_OK) return st;
   const bool pdl = (flags & GQ_GEMV_PDL) != 0;
-  return c.bn == 256 ? launch_fp8<256>(xmap, wmap, a, pdl, s) : launch_fp8<128>(xmap, wmap, a, pdl, s);
+  return c.pair ? launch_fp8<256, true>(xmap, wmap, a, pdl, s) : launch_fp8<128, false>(xmap, wmap, a, pdl, s);
 }
 
 }  // extern "C"
