@@ -553,6 +553,8 @@ def _workspace(name: str, workspace, need: int, device: torch.device, stream: in
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a uint8 CUDA tensor")
+        if need == 0:
+            return None, 0
         return _auto_workspace(name, need, device, stream)[1:]
     if workspace is None:
         return None, 0

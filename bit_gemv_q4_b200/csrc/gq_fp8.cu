@@ -54,21 +54,54 @@ __device__ __forceinline__ unsigned absmax8(const float v[8]) {
   return m;
 }
 
-// Eight codes of values with scale s.
-__device__ __forceinline__ uint2 codes8(const float v[8], float s) {
+// Whether x * (1 / s) may round to another code than x / s does, both rounded
+// to fp32 first.  The product is at most 3 steps of 2^-23 (relative) off the
+// quotient, so only products within 4 steps of the middle between two codes
+// need the division: for |q| >= 2^-6 the middles have a mantissa of three bits,
+// a one and zeros.  Below 2^-6 codes are evenly spaced, and all divide.
+__device__ __forceinline__ bool near_middle(float q) {
+  const unsigned u = __float_as_uint(q);
+  return ((u + 4u - 0x80000u) & 0xFFFFFu) <= 8u || (u & 0x7FFFFFFFu) < 0x3C800000u;
+}
+
+// Eight codes of values with scale s (r = 1 / s where that is exact enough,
+// else zero).  IEEE division takes most of the kernels' instructions; the
+// middles are rare (1 in 10^5 values, and zeros).
+__device__ __forceinline__ uint2 codes8(const float v[8], float s, float r) {
+  float q[8];
+  bool slow = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    q[i] = __fmul_rn(v[i], r);
+    slow |= near_middle(q[i]) && q[i] != 0.f;
+  }
+  if (slow || r == 0.f) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      float d = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d = j == i ? v[j] : d;
+      d = s > 0.f ? __fdiv_rn(d, s) : 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = j == i ? d : q[j];
+    }
+  }
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t c[2];
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const float2 f = make_float2(s > 0.f ? __fdiv_rn(v[4 * h + 2 * p], s) : 0.f,
-                                   s > 0.f ? __fdiv_rn(v[4 * h + 2 * p + 1], s) : 0.f);
-      c[p] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-    }
-    w[h] = c[0] | (c[1] << 16);
+    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * h], q[4 * h + 1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * h + 2], q[4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
+    w[h] = a | (b << 16);
   }
   return make_uint2(w[0], w[1]);
+}
+
+// The scale of a block and its reciprocal for codes8() (none for scales whose
+// reciprocal is subnormal or infinite, and for non-finite ones).
+__device__ __forceinline__ float scale_of(unsigned maxbits, float& r) {
+  const float s = __fdiv_rn(__uint_as_float(maxbits), kTop);
+  r = s > 1e-37f && s < 1e37f ? __frcp_rn(s) : 0.f;
+  return s;
 }
 
 // Row blocks: half a warp each, eight values a lane.
@@ -87,44 +120,45 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const void* x, int64
   unsigned m = absmax8(v);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  const float s = __fdiv_rn(__uint_as_float(m), kTop);
+  float inv;
+  const float s = scale_of(m, inv);
   if (!mine) return;
-  *reinterpret_cast<uint2*>(q + r * K + k) = codes8(v, s);
+  *reinterpret_cast<uint2*>(q + r * K + k) = codes8(v, s, inv);
   if (lane == 0) {
     scales[block] = s;
     if (m >= 0x7F800000u) report(dev_status, GQ_DEV_NONFINITE);
   }
 }
 
-// 128 x 128 blocks: one CTA each, 16 lanes to a row, 16 rows at a time.
+// 128 x 128 blocks: one CTA each, 16 lanes to a row, 32 rows at a time.
+constexpr int kTileThreads = 512;
 template <int TYPE>
-__global__ void __launch_bounds__(256) quantize_tiles_kernel(const void* x, int64_t R, int K, int kblocks,
-                                                             uint8_t* q, float* scales, int* dev_status) {
-  __shared__ unsigned top[8];
+__global__ void __launch_bounds__(kTileThreads) quantize_tiles_kernel(const void* x, int64_t R, int K, int kblocks,
+                                                                      uint8_t* q, float* scales, int* dev_status) {
+  constexpr int kRowsAtOnce = kTileThreads / 16, kPasses = kBlk / kRowsAtOnce;
+  __shared__ unsigned top[kTileThreads / 32];
   const int64_t rb = blockIdx.x / kblocks;
   const int kb = static_cast<int>(blockIdx.x - rb * kblocks);
   const int k = kb * kBlk + 8 * (threadIdx.x & 15);
   const int64_t r0 = rb * kBlk + (threadIdx.x >> 4);
-  float v[8][8];
+  float v[kPasses][8];
   unsigned m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (r0 + 16 * i < R && k < K) {
-      load8<TYPE>(x, (r0 + 16 * i) * K + k, v[i]);
-      m = max(m, absmax8(v[i]));
-    }
-  }
+  for (int i = 0; i < kPasses; ++i)
+    if (r0 + kRowsAtOnce * i < R && k < K) load8<TYPE>(x, (r0 + kRowsAtOnce * i) * K + k, v[i]);
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i)
+    if (r0 + kRowsAtOnce * i < R && k < K) m = max(m, absmax8(v[i]));
   m = __reduce_max_sync(0xFFFFFFFFu, m);
   if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
   __syncthreads();
-  m = 0;
+  m = __reduce_max_sync(0xFFFFFFFFu, top[threadIdx.x & (kTileThreads / 32 - 1)]);
+  float inv;
+  const float s = scale_of(m, inv);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, top[i]);
-  const float s = __fdiv_rn(__uint_as_float(m), kTop);
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (r0 + 16 * i < R && k < K)
-      *reinterpret_cast<uint2*>(q + (r0 + 16 * i) * K + k) = codes8(v[i], s);
+  for (int i = 0; i < kPasses; ++i)
+    if (r0 + kRowsAtOnce * i < R && k < K)
+      *reinterpret_cast<uint2*>(q + (r0 + kRowsAtOnce * i) * K + k) = codes8(v[i], s, inv);
   if (threadIdx.x == 0) {
     scales[blockIdx.x] = s;
     if (m >= 0x7F800000u) report(dev_status, GQ_DEV_NONFINITE);
@@ -203,7 +237,7 @@ GQ_API gq_status gq_quantize_fp8(const void* x, int x_dtype, int64_t R, int64_t 
   const int64_t grid = rows == 1 ? (blocks + 15) / 16 : blocks;
   if (grid > 0x7FFFFFFFLL) return GQ_ERR_SHAPE;
   auto run = [&](auto kern) {
-    return launch(kern, dim3(static_cast<unsigned>(grid)), dim3(256), 0, as_stream(stream), false, x, R,
+    return launch(kern, dim3(static_cast<unsigned>(grid)), dim3(rows == 1 ? 256 : kTileThreads), 0, as_stream(stream), false, x, R,
                   static_cast<int>(K), kblocks, static_cast<uint8_t*>(q), scales, dev_status);
   };
   if (rows == 1)

@@ -41,6 +41,7 @@
 
 #include "gq.h"
 #include "gq_device.cuh"
+#include "gq_fp8.h"
 #include "gq_host.h"
 #include "gq_tc.cuh"
 
@@ -611,6 +612,7 @@ Choice choose(int64_t M, int64_t K, int64_t B) {
 }
 
 size_t ws_bytes_of(const Choice& c, int64_t B) {
+  if (B <= kFp8GemvMaxB) return 0;
   if (c.sp.whole || c.sp.P == 1) return kCountBytes;  // no parts
   const int64_t rows = B < kBM ? B : kBM;
   return kCountBytes + static_cast<size_t>(c.sp.P) * 2 * static_cast<size_t>(rows) * c.bn * sizeof(float);
@@ -684,8 +686,11 @@ GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, in
   if (misaligned16(W) || misaligned16(X) || misaligned16(w_scales) || misaligned16(x_scales))
     return GQ_ERR_ALIGNMENT;
   const Choice c = choose(M, K, B);
-  if (!workspace || ws_bytes < ws_bytes_of(c, B)) return GQ_ERR_WORKSPACE;
-  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GQ_ERR_ALIGNMENT;
+  const size_t need = ws_bytes_of(c, B);
+  if (need && (!workspace || ws_bytes < need)) return GQ_ERR_WORKSPACE;
+  if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return GQ_ERR_ALIGNMENT;
+  const bool pdl = (flags & GQ_GEMV_PDL) != 0;
+  if (B <= kFp8GemvMaxB) return fp8_gemv(W, w_scales, M, K, X, x_scales, B, Y, y_dtype, pdl, s);
 
   Args a{};
   a.sx = x_scales;
@@ -707,7 +712,6 @@ GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, in
   gq_status st = encode(&xmap, X, B, K, a.xrows);
   if (st == GQ_OK) st = encode(&wmap, W, M, K, 128);
   if (st != GQ_OK) return st;
-  const bool pdl = (flags & GQ_GEMV_PDL) != 0;
   return c.pair ? launch_fp8<256, true>(xmap, wmap, a, pdl, s) : launch_fp8<128, false>(xmap, wmap, a, pdl, s);
 }
 

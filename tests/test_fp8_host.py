@@ -15,7 +15,8 @@ def test_sizes():
         assert gq.gq_fp8_scales(*bad) == 0
     assert gq.gq_gemm_fp8_workspace_bytes(0, 128, 1) == 0
     assert gq.gq_gemm_fp8_workspace_bytes(128, 24, 1) == 0
-    assert gq.gq_gemm_fp8_workspace_bytes(4096, 4096, 1) > 0
+    assert gq.gq_gemm_fp8_workspace_bytes(4096, 4096, 1) == 0      # few tokens need none
+    assert gq.gq_gemm_fp8_workspace_bytes(4096, 4096, 100) > 0
 
 
 def test_quantize_refusals():
@@ -54,8 +55,9 @@ def test_gemm_refusals():
         assert call(**{n: None}) == INVALID
         assert call(**{n: A + 4}) == ALIGN
     assert call(st=A + 1) == ALIGN
-    need = gq.gq_gemm_fp8_workspace_bytes(256, 128, 4)
-    assert call(work=None) == WORKSPACE and call(wb=need - 1) == WORKSPACE and call(work=A + 16) == ALIGN
+    need = gq.gq_gemm_fp8_workspace_bytes(256, 128, 100)
+    assert call(B=100, work=None) == WORKSPACE and call(B=100, wb=need - 1) == WORKSPACE
+    assert call(B=100, work=A + 16) == ALIGN
     assert call(M=0) == 0 and call(B=0) == 0
 
 

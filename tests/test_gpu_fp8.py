@@ -69,6 +69,26 @@ def test_quantize_extremes():
     assert float(s[0, 0]) == 0.0 and not q[0].float().any()
 
 
+def test_quantize_codes_at_the_middles():
+    # quotients at, and one to five fp32 steps beside, every middle between two codes; zeros and the
+    # evenly spaced small codes too
+    mids = [(1 + (2 * m + 1) / 16) * 2.0 ** e for e in range(-6, 9) for m in range(8)]
+    mids += [(2 * m + 1) * 2.0 ** -10 for m in range(8)]
+    v = np.array([m for m in mids if m < 448], dtype=np.float32)
+    near = np.concatenate([(v.view(np.int32) + d).view(np.float32) for d in range(-5, 6)])
+    for s in (1.0, 3.0, 0.1, 7e-3, 1.7e-36, 3e34):
+        row = (near.astype(np.float64) * s).astype(np.float32)
+        n = -(-(row.size + 1) // 127)
+        x = np.zeros((n, 128), dtype=np.float32)
+        x[:, 0] = np.float32(448 * s)                # sets the scale near s
+        x[:, 1:].reshape(-1)[:] = 0
+        x[:, 1:] = np.resize(row, n * 127).reshape(n, 127)
+        q, sc = gq.gq_quantize_fp8(torch.from_numpy(x).cuda(), 1)
+        want, ws = quantized(x, 1)
+        assert np.array_equal(sc.cpu().numpy(), ws)
+        assert np.array_equal(q.float().cpu().numpy().astype(np.float64), want)
+
+
 @pytest.mark.parametrize("rows", [1, 128])
 def test_quantize_reports_nonfinite_and_keeps_other_blocks(rows):
     x = torch.randn(130, 272, device="cuda")
@@ -108,6 +128,8 @@ def check(Y, W, ws, X, xs):
 
 @pytest.mark.parametrize("M,K,B,yt", [
     (1, 16, 1, "f32"), (128, 128, 128, "f32"), (5, 48, 3, "bf16"), (300, 144, 130, "f32"),
+    (200, 4096, 100, "f32"), (1000, 2064, 67, "f16"), (129, 4096, 128, "bf16"), (2000, 512, 65, "f32"),
+    (70, 11008, 7, "f32"), (33, 1040, 16, "f32"), (64, 2048, 17, "f32"),
     (4096, 4096, 1, "bf16"), (1000, 2064, 9, "f16"), (129, 4096, 33, "f32"), (2000, 512, 64, "f32"),
     (11000, 256, 37, "f16"), (257, 8192, 65, "bf16"), (4096, 1024, 500, "bf16"),
     (520, 400, 4000, "f32"), (6001, 384, 1300, "f16"), (9000, 128, 2500, "f32"), (4095, 640, 2049, "bf16"),
@@ -122,7 +144,7 @@ def test_gemm(M, K, B, yt):
 
 
 def test_gemm_guards_and_one_workspace_for_all_sizes():
-    cases = [(1000, 2064, 9), (129, 4096, 33), (300, 144, 130), (4096, 256, 1)]
+    cases = [(1000, 2064, 9), (129, 4096, 33), (300, 144, 130), (200, 4096, 100), (4096, 256, 1)]
     need = max(gq.gq_gemm_fp8_workspace_bytes(*c) for c in cases)
     buf = torch.zeros(need + 512, dtype=torch.uint8, device="cuda")
     buf[need:] = 0xA5
