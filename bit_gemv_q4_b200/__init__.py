@@ -688,11 +688,12 @@ def gq_quantize_fp8(x: torch.Tensor, rows: int, out: torch.Tensor | None = None,
     if rows not in (1, 128):
         raise ValueError("rows is 1 or 128")
     R, K = x.shape
+    given = out is not None or scales is not None
     if out is None:
         out = x.new_empty((R, K), dtype=torch.float8_e4m3fn)
     if scales is None:
         scales = x.new_empty((-(-R // rows), -(-K // 128)), dtype=torch.float32)
-    if _fp8_pair(out, scales, rows, "out") != (R, K):
+    if given and _fp8_pair(out, scales, rows, "out") != (R, K):
         raise ValueError("out has another shape than x")
     _check(lib.gq_quantize_fp8(_ptr(x), _DTYPE_CODE[x.dtype], R, K, rows, _ptr(out), _ptr(scales),
                                _ptr(dev_status), _raw_stream(stream, x.device)), "gq_quantize_fp8")

@@ -47,37 +47,30 @@ struct RouteArgs {
   float* weights;
   int* dev_status;
   int64_t T;
-  int H, E, k, xtype, wtype, sigmoid, norm;
+  int H, E, k, sigmoid, norm;
   float scale;
 };
 
-// Values h .. h+7 of a row (zeros past H).
-__device__ __forceinline__ void load8(const void* base, int64_t row, int h, int H, int type, bool ok,
-                                      float v[8]) {
-  if (!ok || h >= H) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    return;
-  }
-  const int64_t at = row * H + h;
-  if (type == GQ_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    return;
-  }
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (type == GQ_F16) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[q]));
-      v[2 * q] = f.x, v[2 * q + 1] = f.y;
-    } else {
-      v[2 * q] = __uint_as_float(w[q] << 16);
-      v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
-    }
-  }
+// Eight consecutive values as they are stored.
+template <int TYPE>
+struct Raw {
+  uint4 v[TYPE == GQ_F32 ? 2 : 1];
+};
+template <int TYPE>
+__device__ __forceinline__ void load8(Raw<TYPE>& r, const void* base, int64_t at, bool ok) {
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + at * (TYPE == GQ_F32 ? 4 : 2));
+  r.v[0] = ok ? __ldg(p) : uint4{};
+  if constexpr (TYPE == GQ_F32) r.v[1] = ok ? __ldg(p + 1) : uint4{};
+}
+// Value i of them (i a constant).
+template <int TYPE>
+__device__ __forceinline__ double value(const Raw<TYPE>& r, int i) {
+  const uint4 u = r.v[TYPE == GQ_F32 ? i >> 2 : 0];
+  const int j = TYPE == GQ_F32 ? i & 3 : i >> 1;
+  const uint32_t w = j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w;
+  if constexpr (TYPE == GQ_F32) return static_cast<double>(__uint_as_float(w));
+  if constexpr (TYPE == GQ_BF16) return static_cast<double>(__uint_as_float((i & 1) ? w & 0xFFFF0000u : w << 16));
+  return static_cast<double>(__half2float(__ushort_as_half(static_cast<unsigned short>((i & 1) ? w >> 16 : w))));
 }
 
 __device__ __forceinline__ void mma_f64(double c[2], double a, double b) {
@@ -86,17 +79,31 @@ __device__ __forceinline__ void mma_f64(double c[2], double a, double b) {
       : "d"(a), "d"(b));
 }
 
-// A double's bits in an order that unsigned integers have.
+// A double's bits in an order that unsigned integers have, and back.
 __device__ __forceinline__ uint64_t sortable(double v) {
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
   return (u >> 63) ? ~u : u | 0x8000000000000000ull;
 }
+__device__ __forceinline__ double unsorted(uint64_t k) {
+  return __longlong_as_double(static_cast<long long>((k >> 63) ? k & 0x7FFFFFFFFFFFFFFFull : ~k));
+}
 
-// One warp: the experts of token t from its scores (shared memory).
-__device__ void pick(const RouteArgs& a, int64_t t, const double* s) {
+// One warp: the experts of token t; lane l has the keys of experts l + 32 i, N
+// at most, in registers.
+template <int N>
+__device__ __forceinline__ void pick(const RouteArgs& a, int64_t t) {
   const int lane = threadIdx.x & 31;
+  const double* s = a.scores + t * a.E;
+  uint64_t key[N];  // 0: no expert, or taken
   bool bad = false;
-  for (int e = lane; e < a.E; e += 32) bad |= !isfinite(s[e]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = lane + 32 * i;
+    double v = e < a.E ? __ldcg(s + e) : 0.0;
+    bad |= !isfinite(v);
+    if (a.bias && e < a.E) v += static_cast<double>(__ldg(a.bias + e));
+    key[i] = e < a.E ? sortable(v + 0.0) : 0;  // (-0 and +0 are equal keys)
+  }
   if (__any_sync(0xFFFFFFFFu, bad)) {  // no experts: the token's outputs are zeros
     if (lane < a.k) {
       a.ids[t * a.k + lane] = -1;
@@ -105,48 +112,46 @@ __device__ void pick(const RouteArgs& a, int64_t t, const double* s) {
     if (lane == 0) report(a.dev_status, GQ_DEV_NONFINITE);
     return;
   }
-  unsigned taken = 0;  // this lane's experts lane + 32 i that are taken
-  uint64_t best = 0;   // largest key among the others (0: none left) and its index
-  int at = 0;
-  auto scan = [&]() {
-    best = 0;
-    for (int i = 0, e = lane; e < a.E; ++i, e += 32) {
-      if ((taken >> i) & 1u) continue;
-      // -0 and +0 are equal keys
-      const double v = (a.bias ? s[e] + static_cast<double>(__ldg(a.bias + e)) : s[e]) + 0.0;
-      const uint64_t key = sortable(v);
-      if (key > best) {
-        best = key;
-        at = e;
+  float sum = 0.f;  // of exp(z - max) over this lane's experts (softmax)
+  double top = 0.0;
+  int mine = 0;         // lane j: the j-th expert
+  uint64_t mykey = 0;   // and its key
+  for (int j = 0; j < a.k; ++j) {
+    uint64_t best = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
       }
     }
-  };
-  scan();
-  int mine = 0;  // lane j: the j-th expert
-  for (int j = 0; j < a.k; ++j) {
     const unsigned hi = static_cast<unsigned>(best >> 32);
-    const unsigned top = __reduce_max_sync(0xFFFFFFFFu, hi);
-    const unsigned lo = hi == top ? static_cast<unsigned>(best) : 0u;
-    const unsigned low = __reduce_max_sync(0xFFFFFFFFu, lo);
-    const bool is = best != 0 && hi == top && lo == low;
-    const unsigned e = __reduce_min_sync(0xFFFFFFFFu, is ? static_cast<unsigned>(at) : 0xFFFFFFFFu);
-    if (lane == j) mine = static_cast<int>(e);
-    if (is && static_cast<unsigned>(at) == e) {
-      taken |= 1u << (e >> 5);
-      scan();
-    }
-  }
-  float w = 0.f, sum = 0.f;
-  if (a.sigmoid) {
-    if (lane < a.k) w = static_cast<float>(s[mine]);
-  } else {
-    double m = s[lane < a.E ? lane : 0];
-    for (int e = lane; e < a.E; e += 32) m = fmax(m, s[e]);
+    const unsigned thi = __reduce_max_sync(0xFFFFFFFFu, hi);
+    const unsigned tlo = __reduce_max_sync(0xFFFFFFFFu, hi == thi ? static_cast<unsigned>(best) : 0u);
+    const bool is = hi == thi && static_cast<unsigned>(best) == tlo && best != 0;
+    const unsigned e = __reduce_min_sync(0xFFFFFFFFu, is ? static_cast<unsigned>(lane + 32 * at) : 0xFFFFFFFFu);
+    const uint64_t win = static_cast<uint64_t>(thi) << 32 | tlo;
+    if (j == 0 && !a.sigmoid) {  // the largest z is known: the softmax's sum, before any key goes
+      top = unsorted(win);
+      if (!a.norm) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if (lane < a.k) w = expf(static_cast<float>(s[mine] - m));
-    if (!a.norm)
-      for (int e = lane; e < a.E; e += 32) sum += expf(static_cast<float>(s[e] - m));
+        for (int i = 0; i < N; ++i)
+          if (key[i]) sum += expf(static_cast<float>(unsorted(key[i]) - top));
+      }
+    }
+    if (lane == j) {
+      mine = static_cast<int>(e);
+      mykey = win;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (static_cast<unsigned>(lane + 32 * i) == e) key[i] = 0;
+  }
+  float w = 0.f;
+  if (lane < a.k) {
+    if (!a.sigmoid) w = expf(static_cast<float>(unsorted(mykey) - top));
+    else w = static_cast<float>(a.bias ? __ldcg(s + mine) : unsorted(mykey));
   }
   if (a.norm) sum = w;
   if (a.norm || !a.sigmoid) {
@@ -160,8 +165,9 @@ __device__ void pick(const RouteArgs& a, int64_t t, const double* s) {
   }
 }
 
-__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
-  extern __shared__ __align__(16) double keys[];  // [8][E] of the picking CTA
+template <int XT, int WT>
+__global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteArgs a) {
+  constexpr int kBatch = XT == GQ_F32 || WT == GQ_F32 ? 2 : 4;  // pieces of a row read at once
   __shared__ double part[kWarps][64];
   __shared__ int last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, t4 = lane & 3;
@@ -169,18 +175,28 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * kTile;
   pdl_wait();
   pdl_launch_dependents();
-  double c[2] = {0.0, 0.0};
+  double c[2][2] = {};
   const bool eok = e0 + row < a.E, tok = t0 + row < a.T;
-#pragma unroll 2
-  for (int h = 32 * warp; h < a.H; h += 32 * kWarps) {
-    float w[8], x[8];
-    load8(a.w, e0 + row, h + 8 * t4, a.H, a.wtype, eok, w);
-    load8(a.x, t0 + row, h + 8 * t4, a.H, a.xtype, tok, x);
+  const int64_t we = static_cast<int64_t>(e0 + row) * a.H + 8 * t4, xe = (t0 + row) * a.H + 8 * t4;
+  for (int h0 = 32 * warp; h0 < a.H; h0 += 32 * kWarps * kBatch) {
+    Raw<WT> w[kBatch];
+    Raw<XT> x[kBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mma_f64(c, static_cast<double>(w[i]), static_cast<double>(x[i]));
+    for (int b = 0; b < kBatch; ++b) {
+      const int h = h0 + 32 * kWarps * b;
+      const bool in = h + 8 * t4 < a.H;
+      load8(w[b], a.w, we + h, eok && in);
+      load8(x[b], a.x, xe + h, tok && in);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (h0 + 32 * kWarps * b >= a.H) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mma_f64(c[i & 1], value(w[b], i), value(x[b], i));
+    }
   }
-  part[warp][row * 8 + 2 * t4] = c[0];
-  part[warp][row * 8 + 2 * t4 + 1] = c[1];
+  part[warp][row * 8 + 2 * t4] = c[0][0] + c[1][0];
+  part[warp][row * 8 + 2 * t4 + 1] = c[0][1] + c[1][1];
   __syncthreads();
   if (threadIdx.x < 64) {
     double z = 0.0;
@@ -189,22 +205,33 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
     if (a.sigmoid) z = 1.0 / (1.0 + exp(-z));  // NaN stays NaN
     const int e = e0 + (threadIdx.x >> 3);
     const int64_t t = t0 + (threadIdx.x & 7);
-    if (e < a.E && t < a.T) a.scores[t * a.E + e] = z;
-    __threadfence();
+    if (e < a.E && t < a.T) __stcg(a.scores + t * a.E + e, z);
   }
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
     last = atomicAdd(a.counts + blockIdx.y, 1) == static_cast<int>(gridDim.x) - 1;
+    __threadfence();
   }
   __syncthreads();
   if (!last) return;
-  __threadfence();
-  const int nt = static_cast<int>(i64min(kTile, a.T - t0));
-  for (int i = threadIdx.x; i < nt * a.E; i += kThreads) keys[i] = __ldcg(a.scores + t0 * a.E + i);
   if (threadIdx.x == 0) a.counts[blockIdx.y] = 0;
-  __syncthreads();
-  if (warp < nt) pick(a, t0 + warp, keys + warp * a.E);
+  const int64_t t = t0 + warp;
+  if (warp >= kTile || t >= a.T) return;
+  if (a.E <= 64) pick<2>(a, t);
+  else if (a.E <= 128) pick<4>(a, t);
+  else if (a.E <= 256) pick<8>(a, t);
+  else if (a.E <= 512) pick<16>(a, t);
+  else pick<32>(a, t);
+}
+
+template <int XT>
+gq_status launch_route(const RouteArgs& a, int wtype, dim3 grid, bool pdl, cudaStream_t s) {
+  switch (wtype) {
+    case GQ_F32: return launch(route_kernel<XT, GQ_F32>, grid, dim3(kThreads), 0, s, pdl, a);
+    case GQ_F16: return launch(route_kernel<XT, GQ_F16>, grid, dim3(kThreads), 0, s, pdl, a);
+    default: return launch(route_kernel<XT, GQ_BF16>, grid, dim3(kThreads), 0, s, pdl, a);
+  }
 }
 
 }  // namespace
@@ -249,22 +276,15 @@ GQ_API gq_status gq_moe_route(const void* x, int x_dtype, int64_t T, int64_t H, 
   a.H = static_cast<int>(H);
   a.E = static_cast<int>(E);
   a.k = static_cast<int>(k);
-  a.xtype = x_dtype;
-  a.wtype = w_dtype;
   a.sigmoid = sigmoid;
   a.norm = (flags & GQ_ROUTE_NORM) != 0;
   a.scale = scale;
-  thread_local unsigned long long configured_ctx = 0;  // per host thread and context
-  const unsigned long long ctx = context_id();
-  if (ctx == 0 || ctx != configured_ctx) {
-    if (cudaFuncSetAttribute(route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kTile * kMaxE * static_cast<int>(sizeof(double))) != cudaSuccess)
-      return GQ_ERR_CUDA;
-    configured_ctx = ctx;
-  }
   const dim3 grid(static_cast<unsigned>((E + kTile - 1) / kTile), static_cast<unsigned>((T + kTile - 1) / kTile));
-  return launch(route_kernel, grid, dim3(kThreads), static_cast<size_t>(kTile * E) * sizeof(double),
-                as_stream(stream), (flags & GQ_GEMV_PDL) != 0, a);
+  const bool pdl = (flags & GQ_GEMV_PDL) != 0;
+  cudaStream_t s = as_stream(stream);
+  return x_dtype == GQ_F32   ? launch_route<GQ_F32>(a, w_dtype, grid, pdl, s)
+         : x_dtype == GQ_F16 ? launch_route<GQ_F16>(a, w_dtype, grid, pdl, s)
+                             : launch_route<GQ_BF16>(a, w_dtype, grid, pdl, s);
 }
 
 }  // extern "C"
