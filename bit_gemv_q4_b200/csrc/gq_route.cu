@@ -166,7 +166,7 @@ __device__ __forceinline__ void pick(const RouteArgs& a, int64_t t) {
 }
 
 template <int XT, int WT>
-__global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) route_kernel(const __grid_constant__ RouteArgs a) {
   constexpr int kBatch = XT == GQ_F32 || WT == GQ_F32 ? 2 : 4;  // pieces of a row read at once
   __shared__ double part[kWarps][64];
   __shared__ int last;
