@@ -11,7 +11,9 @@
 // One cooperative launch of one CTA per SM in three phases with a grid barrier
 // between them: gate and up with the activation (h, fp32, in the workspace),
 // down (one fp32 row of outputs for each token and slot), and the weighted sum
-// over a token's slots.  The first copies of down's weights are under way while
+// over a token's slots.  For a single token whose slots' h all fit in shared
+// memory, down's rows run over all slots, with the weights folded into h, and y
+// is stored at once: no third phase.  The first copies of down's weights are under way while
 // a CTA waits for the others.  (As three launches joined by programmatic
 // dependent launch the phases cost 8 us between the weight streams of the first
 // two: a CTA's shared memory keeps the next launch out of its SM.)
@@ -21,7 +23,7 @@
 // with at most `cap` of its pairs.  The work of all segments, one item for 16
 // weight rows (of gate and of up, or of down), is cut into even runs, one for
 // each CTA.  A run is a string of stages (8 blocks of 32 weights x 16 rows, 2.3
-// KB) that its 24 warps share evenly, so that the split is even whatever the
+// KB) that its 20 warps share evenly, so that the split is even whatever the
 // sizes are.  Each warp copies its own stages to its own ring in shared memory
 // (cp.async): tiled storage is ordered by the lanes that multiply it, so the
 // copies are whole lines and a lane reads back its own codes, and warps wait
@@ -52,7 +54,7 @@
 namespace gq {
 namespace {
 
-constexpr int kWarps = 24;
+constexpr int kWarps = 20;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxT = 64, kMaxTopK = 16, kMaxE = 1024;
 constexpr int kMaxPairs = kMaxT * kMaxTopK;
@@ -100,12 +102,14 @@ struct MoeArgs {
   void* y;                  // [T][H]
   float* h;                 // [pairs][I], by slot
   float* out;               // [pairs][H], by pair
-  unsigned* hmax;           // [pairs] largest |h| of a slot as bits, zero between calls
+  unsigned* hmax;           // [2][pairs] largest |h| of a slot as bits; see hmax_set()
   unsigned long long* arrivals;  // at the grid barriers, a multiple of the grid between calls
   int* dev_status;
   long long budget;
   int T, k, E, H;
   Div by_grid;
+  int single;               // one token: down's rows run over its slots
+  Div by_slots[kMaxTopK];   // stages of such a row, by slots
   int xtype, ytype;
   int bbytes;               // room for B fragments
   uint32_t b_off, tab_off, plan_off;  // dynamic shared memory, after the rings
@@ -116,11 +120,21 @@ struct Seg {
   int n;
 };
 
+struct Col {
+  int row;           // of x, or of h
+  float scale, mul;  // the power of two, and a single token's slot weight
+  int dst, pitch;    // of its B fragments: shared offset, columns
+};
+
 struct Plan {
   int nseg[2];
   int go;                              // the grid barrier was passed
+  unsigned* hmax_now;                  // the set of this call
   unsigned xmax[kMaxT];                // largest |x| of a token as bits
+  unsigned common;                     // a single token's largest |weight * h|
   // of a string's segments
+  int ncols;                           // tokens of all segments
+  Col col[kMaxSegs * kMaxCols];
   int boff[kMaxSegs];                  // their B fragments
   float inv[kMaxSegs][kMaxCols];       // 1 / scale of their tokens
   unsigned hmax[kMaxSegs][kMaxCols];   // largest |h|
@@ -257,49 +271,93 @@ __device__ __forceinline__ int col_pitch(int ncol) {
   return ncol <= 2 ? ncol : ncol <= 4 ? 4 : 8;
 }
 
-// B fragments of a segment's tokens at shared offset b_off.  Column c of block b
-// and lane group t: 16 bytes at ((b * pitch + c) * 4 + t) * 16, the values 4t,
-// 4t+2, 4t+1, 4t+3 of the block and the same at +16; zeros up to whole stages.
 __host__ __device__ __forceinline__ int padded(int K) { return (K + 255) & ~255; }
 
+// The tokens of a string's segments (all threads call it).  A single token's h
+// is multiplied by its slot's weight and scaled by the largest product of all
+// slots.
 template <bool GATE_UP>
-__device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& pl, const Seg& sg, int local,
-                                       int b_off) {
-  const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
+__device__ __forceinline__ void load_cols(const MoeArgs& a, const Phase& ph, Plan& pl, int seg0, int segs) {
+  const bool single = !GATE_UP && a.single;
+  const int i = threadIdx.x / kMaxCols, c = threadIdx.x % kMaxCols;
+  float mul = 1.0f;
+  unsigned top = 0;
+  Seg sg{0, 0, 0};
+  if (i < segs) sg = pl.seg[!GATE_UP][seg0 + i];
+  const int row = c < sg.n ? (GATE_UP ? pl.order[sg.slot0 + c] / a.k : sg.slot0 + c) : 0;
+  if (c < sg.n) {
+    top = GATE_UP ? pl.xmax[row] : __ldcg(pl.hmax_now + row);
+    if (single) {
+      mul = __ldcg(a.weights + pl.order[row]);
+      top = __float_as_uint(fabsf(__uint_as_float(top) * mul));
+      atomicMax(&pl.common, top);
+    }
+  }
+  if (single) {
+    __syncthreads();
+    top = pl.common;
+  }
+  if (c < sg.n) {
+    int before = 0, off = a.b_off;  // columns and bytes of the segments before
+    for (int j = 0; j < i; ++j) {
+      const int n = pl.seg[!GATE_UP][seg0 + j].n;
+      before += n;
+      off += col_pitch(ph.two ? 2 * n : n) * padded(ph.K) * 2;
+    }
+    const float s = scale_of(top);
+    pl.col[before + c] = Col{row, s, mul, off + (ph.two ? 2 * c : c) * 64, col_pitch(ph.two ? 2 * sg.n : sg.n)};
+    pl.inv[i][c] = 1.0f / s;  // a power of two: exact
+    pl.hmax[i][c] = 0u;
+    if (c == 0) pl.boff[i] = off;
+    if (i == segs - 1 && c == 0) pl.ncols = before + sg.n;
+  }
+  __syncthreads();
+}
+
+// B fragments of the string's tokens.  Column c of block b and lane group t: 16
+// bytes at ((b * pitch + c) * 4 + t) * 16 of its segment, the values 4t, 4t+2,
+// 4t+1, 4t+3 of the block and the same at +16; zeros up to whole stages.
+template <bool GATE_UP>
+__device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, const Plan& pl) {
+  constexpr int kBatch = 2;  // pieces of 8 values read at once
   const int vecs = padded(ph.K) / 8, real = ph.K / 8;
-  auto row_of = [&](int c) { return GATE_UP ? pl.order[sg.slot0 + c] / a.k : sg.slot0 + c; };
-  auto max_of = [&](int c) { return GATE_UP ? pl.xmax[row_of(c)] : __ldcg(a.hmax + sg.slot0 + c); };
   const int type = GATE_UP ? a.xtype : GQ_F32;
   const void* src = GATE_UP ? a.x : a.h;
-  if (threadIdx.x < sg.n) {  // scale_of() is a power of two: the reciprocal is exact
-    pl.inv[local][threadIdx.x] = 1.0f / scale_of(max_of(threadIdx.x));
-    pl.hmax[local][threadIdx.x] = 0u;
-  }
-  if (threadIdx.x == 0) pl.boff[local] = b_off;
-  const int nvec = sg.n * vecs;
-  for (int i = threadIdx.x; i < nvec; i += kThreads) {
-    const int c = ph.by_vecs(i), r = i - c * vecs;
-    const int b = r >> 2, q = r & 3;
-    float v[8] = {};
-    if (r < real) load8(src, static_cast<int64_t>(row_of(c)) * ph.K + 8 * r, type, v);
-    const float s = scale_of(max_of(c));
-    const int col = ph.two ? 2 * c : c;
-    const int t0 = 2 * (q & 1);
-    for (int part = 0; part <= ph.two; ++part) {
-      __half hv[8];
+  const int nvec = pl.ncols * vecs;
+  for (int i0 = threadIdx.x; i0 < nvec; i0 += kBatch * kThreads) {
+    float v[kBatch][8];
+    int cs[kBatch], rs[kBatch];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float f = part ? v[j] : v[j] * s;  // the second pass holds remainders
-        hv[j] = __float2half_rn(f);
-        v[j] = f - __half2float(hv[j]);
-      }
-      uint8_t* d = msm + b_off + (static_cast<uint32_t>(b * pitch + col + part) * 4 + t0) * 16 + (q >> 1) * 8;
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kThreads;
+      cs[u] = i < nvec ? ph.by_vecs(i) : -1;
+      rs[u] = i - cs[u] * vecs;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const __half2 lo = __halves2half2(hv[4 * u], hv[4 * u + 2]);
-        const __half2 hi = __halves2half2(hv[4 * u + 1], hv[4 * u + 3]);
-        *reinterpret_cast<uint2*>(d + 16 * u) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                                           *reinterpret_cast<const uint32_t*>(&hi));
+      for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
+      if (cs[u] >= 0 && rs[u] < real)
+        load8(src, static_cast<int64_t>(pl.col[cs[u]].row) * ph.K + 8 * rs[u], type, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (cs[u] < 0) break;
+      const Col col = pl.col[cs[u]];
+      const int b = rs[u] >> 2, q = rs[u] & 3;
+      for (int part = 0; part <= ph.two; ++part) {
+        __half hv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float f = part ? v[u][j] : v[u][j] * col.mul * col.scale;  // the second pass holds remainders
+          hv[j] = __float2half_rn(f);
+          v[u][j] = f - __half2float(hv[j]);
+        }
+        uint8_t* d = msm + col.dst + (b * col.pitch + part) * 64 + 2 * (q & 1) * 16 + (q >> 1) * 8;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const __half2 lo = __halves2half2(hv[4 * w], hv[4 * w + 2]);
+          const __half2 hi = __halves2half2(hv[4 * w + 1], hv[4 * w + 3]);
+          *reinterpret_cast<uint2*>(d + 16 * w) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                             *reinterpret_cast<const uint32_t*>(&hi));
+        }
       }
     }
   }
@@ -391,6 +449,7 @@ struct Feed {
   const uint8_t* code;
   const uint8_t* scale;
   int s, g, k, left;
+  int segs;  // a single token's down: segments of a row (0: one)
 
   __device__ __forceinline__ void seek(const Phase& ph, const Plan& pl, int stages, int lane) {
     const bool up = GATE_UP && k >= stages;
@@ -433,7 +492,12 @@ struct Feed {
       if (end || ((kk + 1) & 7) == 0) {  // another tile
         if (k == (GATE_UP ? 2 * stages : stages)) {
           k = 0;
-          if (++g == ph.groups) {
+          if (!GATE_UP && segs) {
+            if (++s == segs) {
+              s = 0;
+              ++g;
+            }
+          } else if (++g == ph.groups) {
             g = 0;
             ++s;
           }
@@ -478,6 +542,9 @@ __device__ __forceinline__ unsigned put(const MoeArgs& a, const Phase& ph, const
     const float h = __fdividef(v, 1.0f + expf(-v)) * up;
     __stcg(a.h + static_cast<int64_t>(sg.slot0 + c) * (ph.groups * 16) + row, h);
     return __float_as_uint(h) & 0x7FFFFFFFu;
+  } else if (a.single) {
+    store_elem(a.y, row, v, a.ytype);
+    return 0u;
   } else {
     __stcg(a.out + static_cast<int64_t>(pl.order[sg.slot0 + c]) * (ph.groups * 16) + row, v);
     return 0u;
@@ -491,6 +558,7 @@ struct Work {
   String st;
   int u0, u1;     // this warp's stages of the string
   int s0, g0, k0; // where they begin
+  Div item;       // stages of an item
   Feed<FMT, GATE_UP> feed;
 
   __device__ __forceinline__ static uint32_t ring() { return (threadIdx.x >> 5) * (kDepth * kStageBytes); }
@@ -499,8 +567,14 @@ struct Work {
     more = r < r1;
     if (!more) return;
     st.ra = r;
-    st.seg0 = ph.by_groups(r);
-    st.segs = 0;
+    if (!GATE_UP && a.single) {  // one string: all slots' h are in shared memory
+      st.seg0 = 0;
+      st.segs = pl.nseg[1];
+      r = r1;
+    } else {
+      st.seg0 = ph.by_groups(r);
+      st.segs = 0;
+    }
     int bytes = 0;
     while (r < r1 && st.segs < kMaxSegs) {
       const int s = st.seg0 + st.segs;
@@ -511,20 +585,33 @@ struct Work {
     }
     st.rb = r;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const unsigned tu = (st.rb - st.ra) * ph.by_item.d;
+    const unsigned tu = (st.rb - st.ra) * item.d;
     u0 = static_cast<int>(tu * warp / kWarps);
     u1 = static_cast<int>(tu * (warp + 1) / kWarps);
-    const int i = ph.by_item(u0);
-    feed.k = k0 = u0 - i * ph.by_item.d;
-    feed.s = s0 = ph.by_groups(st.ra + i);
-    feed.g = g0 = st.ra + i - s0 * ph.groups;
+    const int i = item(u0);
+    feed.k = k0 = u0 - i * item.d;
+    feed.segs = 0;
+    if (!GATE_UP && a.single) {
+      s0 = 0;
+      g0 = st.ra + i;
+      feed.segs = st.segs;
+      feed.s = ph.by_item(k0);
+      feed.k = k0 - feed.s * ph.stages;
+    } else {
+      feed.s = s0 = ph.by_groups(st.ra + i);
+      g0 = st.ra + i - s0 * ph.groups;
+    }
+    feed.g = g0;
     feed.left = u1 - u0;
     if (feed.left > 0) feed.seek(ph, pl, ph.stages, lane);
     feed.step(ph, pl, ph.stages, ring(), lane);
   }
   __device__ __forceinline__ void start(const MoeArgs& a, const Plan& pl) {
     const Phase& ph = a.ph[!GATE_UP];
-    const int total = pl.nseg[!GATE_UP] * ph.groups;  // at most 2^20
+    const bool single = !GATE_UP && a.single;
+    const int nseg = pl.nseg[!GATE_UP];
+    const int total = single ? (nseg ? ph.groups : 0) : nseg * ph.groups;  // at most 2^20
+    item = single && nseg ? a.by_slots[nseg - 1] : ph.by_item;
     const int each = a.by_grid(total), rest = total - each * static_cast<int>(gridDim.x);
     const int b = static_cast<int>(blockIdx.x);
     r = each * b + a.by_grid(rest * b);
@@ -542,7 +629,7 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
   // columns past the last repeat existing ones (or hold what was there); their sums are not used
   const uint8_t* xb = msm + pl.boff[local] + (g8 & (CP - 1)) * 64 + t * 16;
-  const int stages = ph.stages, all = ph.by_item.d;
+  const int all = wk.item.d, stages = GATE_UP ? ph.stages : all;  // of an item, and of a row of it
   float acc[4] = {}, gate[4] = {};
   unsigned top[2] = {0u, 0u};  // largest |h| of this lane's tokens
   int kk = GATE_UP && k >= stages ? k - stages : k;
@@ -592,7 +679,7 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
     stage_math<FMT, CP>(msm + slot, lane, acc, x);
     x += 8 * 64 * CP;
     __syncwarp();  // every lane has read the stage
-    wk.feed.step(ph, pl, stages, slot, lane);
+    wk.feed.step(ph, pl, ph.stages, slot, lane);
     slot = slot == wk.ring() + (kDepth - 1) * kStageBytes ? wk.ring() : slot + kStageBytes;
     ++k;
     if (++kk == stages) row_end();
@@ -624,10 +711,9 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
 // item that this warp began and did not end (`cut`: row group g of segment sg,
 // `end` its last stage + 1) takes the later warps' parts in order.
 template <int FMT, bool GATE_UP>
-__device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Plan& pl, const String& st, bool cut,
+__device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Plan& pl, const String& st, unsigned tu, bool cut,
                                            const Seg& sg, int local, int g, unsigned u1, unsigned end) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned tu = (st.rb - st.ra) * ph.by_item.d;
   __syncthreads();  // the parts are there; nobody reads B any more
   if (cut) {
     const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
@@ -660,7 +746,7 @@ __device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Pl
     if (threadIdx.x < st.segs * kMaxCols) {
       const int i = threadIdx.x / kMaxCols, c = threadIdx.x % kMaxCols;
       const Seg sh = pl.seg[0][st.seg0 + i];
-      if (c < sh.n) atomicMax(a.hmax + sh.slot0 + c, pl.hmax[i][c]);
+      if (c < sh.n) atomicMax(pl.hmax_now + sh.slot0 + c, pl.hmax[i][c]);
     }
   }
 }
@@ -669,15 +755,11 @@ __device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Pl
 template <int FMT, bool GATE_UP>
 __device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, GATE_UP>& wk) {
   const Phase& ph = a.ph[!GATE_UP];
-  const int all = ph.by_item.d;
+  const int all = wk.item.d;
   while (wk.more) {
     const String st = wk.st;
-    int b_off = a.b_off;
-    for (int i = 0; i < st.segs; ++i) {
-      const Seg sg = pl.seg[!GATE_UP][st.seg0 + i];
-      load_b<GATE_UP>(a, ph, pl, sg, i, b_off);
-      b_off += col_pitch(ph.two ? 2 * sg.n : sg.n) * padded(ph.K) * 2;
-    }
+    load_cols<GATE_UP>(a, ph, pl, st.seg0, st.segs);
+    load_b<GATE_UP>(a, ph, pl);
     // the rest of the ring (the first copies went ahead of B: a full ring of them would hold it up)
     for (int d = 1; d < kDepth; ++d)
       wk.feed.step(ph, pl, ph.stages, wk.ring() + d * kStageBytes, threadIdx.x & 31);
@@ -706,10 +788,11 @@ __device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, 
       g = k = 0;
     }
     // the item that the warp's last stage is of
-    const int li = ph.by_item(max(u1 - 1 - last_base, 0)), begin = last_base + li * all;
+    const int li = wk.item(max(u1 - 1 - last_base, 0)), begin = last_base + li * all;
     const bool cut = u1 > wk.u0 && begin >= wk.u0 && u1 < begin + all;
+    const unsigned tu = (st.rb - st.ra) * all;
     wk.next(a, ph, pl);
-    join_parts<FMT, GATE_UP>(a, ph, pl, st, cut, sg, last_s - st.seg0, li, u1, begin + all);
+    join_parts<FMT, GATE_UP>(a, ph, pl, st, tu, cut, sg, last_s - st.seg0, li, u1, begin + all);
     if (wk.more) __syncthreads();  // before the next string's values
   }
 }
@@ -744,6 +827,22 @@ __device__ __forceinline__ bool grid_wait(const MoeArgs& a, Plan& pl, unsigned l
   return pl.go != 0;
 }
 
+// The set of hmax that this call uses: by the parity of the barriers that the
+// grid has passed, which no CTA of this call can have changed before this CTA
+// arrives.  It is all zeros; the other set is cleared here for a call after one
+// barrier, and this call's own set at the end of a call with two.
+__device__ __forceinline__ void hmax_set(const MoeArgs& a, Plan& pl) {
+  if (threadIdx.x == 0) {
+    const unsigned long long n = __ldcg(a.arrivals);
+    pl.hmax_now = a.hmax + ((n / gridDim.x) & 1) * kMaxPairs;
+  }
+  if (blockIdx.x == 0) {
+    __syncthreads();
+    unsigned* other = pl.hmax_now == a.hmax ? a.hmax + kMaxPairs : a.hmax;
+    for (int i = threadIdx.x; i < kMaxPairs; i += kThreads) other[i] = 0u;
+  }
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ MoeArgs a) {
   __shared__ Plan pl;
@@ -754,9 +853,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     pl.order = reinterpret_cast<short*>(pl.seg[1] + pairs);
   }
   if (threadIdx.x < kMaxT) pl.xmax[threadIdx.x] = 0u;
+  if (threadIdx.x == 0) pl.common = 0u;
   __syncthreads();
   pdl_wait();  // ids and x are final
   pdl_launch_dependents();
+  hmax_set(a, pl);
   make_plan(pl, a);
   {
     Work<FMT, true> gate_up;
@@ -769,6 +870,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   bool ok = grid_wait(a, pl, target);
   if (ok) {
     run_phase<FMT, false>(a, pl, down);
+    if (a.single) {
+      if (pl.nseg[1] == 0)  // no slot names an expert
+        for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.H; i += static_cast<int>(gridDim.x) * kThreads)
+          store_elem(a.y, i, 0.f, a.ytype);
+      return;
+    }
     target = grid_arrive(a);
     ok = grid_wait(a, pl, target);
   }
@@ -781,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   // slots' largest values are cleared for the next call
   const int n = a.T * a.H;
   const int i0 = static_cast<int>(blockIdx.x * kThreads + threadIdx.x);
-  if (i0 < a.T * a.k) a.hmax[i0] = 0u;
+  if (i0 < a.T * a.k) pl.hmax_now[i0] = 0u;
   for (int i = i0; i < n; i += static_cast<int>(gridDim.x) * kThreads) {
     const int t = i / a.H, c = i - t * a.H;
     float v = 0.f;
@@ -804,7 +911,7 @@ Ws ws_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
   Ws w;
   w.arrivals = 0;
   w.hmax = 256;
-  w.h = w.hmax + kMaxPairs * 4;  // one size for every call, so that calls of any sizes may follow
+  w.h = w.hmax + 2 * kMaxPairs * 4;  // one size for every call, so that calls of any sizes may follow
   w.out = w.h + round256(static_cast<size_t>(T * k * I) * 4);
   w.total = w.out + round256(static_cast<size_t>(T * k * H) * 4);
   return w;
@@ -819,23 +926,30 @@ bool moe_width(int fmt, int64_t K) { return K % (fmt == GQ_FMT_Q4_0 ? 64 : 256) 
 // fragments (2 bytes for each value of a column), the table of parts, and the
 // plan.  Segments are as wide as both phases' columns and parts fit; what is
 // left takes more segments of a string.
-static_assert(sizeof(Plan) <= 2048, "the static part");
-constexpr size_t kDynSmem = kSmemBudget - 2048;
+static_assert(sizeof(Plan) <= 5120, "the static part");
+constexpr size_t kDynSmem = kSmemBudget - 5120;
 size_t shape_smem(MoeArgs& a) {
   const int pairs = a.T * a.k;
   const size_t plan = (static_cast<size_t>(pairs) * (2 * sizeof(Seg) + 2) + 15) & ~size_t(15);
   const size_t left = kDynSmem - kRingBytes - plan;
   size_t tab = 0, b = 0;
+  // one token: a column (or two) for each slot, if all of them fit beside the parts
+  const size_t slots = static_cast<size_t>(a.k) * padded(a.ph[1].K) * 2 * (a.ph[1].two ? 2 : 1);
+  // and if they are few enough for every CTA to read them all: 16384 values
+  // took 2 us less than a third phase, 22016 took 2 us more
+  a.single = a.T == 1 && a.k * padded(a.ph[1].K) <= 16384 &&
+             slots + 2 * kWarps * 2 * 16 * 2 * sizeof(float) <= left;
   for (int f = 0; f < 2; ++f) {
     Phase& ph = a.ph[f];
     const size_t part = 2 * kWarps * (f == 0 ? 2 : 1) * 16 * sizeof(float);  // for each column
-    const size_t need = static_cast<size_t>(pairs) * (ph.two ? 2 : 1);
+    const size_t need = (f == 1 && a.single ? 1 : static_cast<size_t>(pairs)) * (ph.two ? 2 : 1);
     size_t c = ph.two ? 2 : 1;  // powers of two
     while (c < kMaxCols && c < need && 2 * c * (static_cast<size_t>(padded(ph.K)) * 2 + part) <= left) c *= 2;
     ph.cap = static_cast<int>(ph.two ? c / 2 : c);
     tab = c * part > tab ? c * part : tab;
     b = c * padded(ph.K) * 2 > b ? c * padded(ph.K) * 2 : b;
   }
+  if (a.single) b = slots > b ? slots : b;
   // the phases use the same room one after the other: narrower segments if both do not fit
   while (b + tab > left) {
     const size_t c0 = static_cast<size_t>(a.ph[0].cap) * (a.ph[0].two ? 2 : 1);
@@ -844,6 +958,7 @@ size_t shape_smem(MoeArgs& a) {
     const size_t b0 = c0 * padded(a.ph[0].K) * 2, b1 = c1 * padded(a.ph[1].K) * 2;
     tab = t0 > t1 ? t0 : t1;
     b = b0 > b1 ? b0 : b1;
+    if (a.single && slots > b) b = slots;
     if (b + tab <= left) break;
     Phase& ph = t0 >= t1 && a.ph[0].cap > 1 ? a.ph[0] : a.ph[1].cap > 1 ? a.ph[1] : a.ph[0];
     ph.cap /= 2;
@@ -854,6 +969,7 @@ size_t shape_smem(MoeArgs& a) {
     ph.by_vecs = make_div(padded(ph.K) / 8);
   }
   for (int f = 0; f < 2; ++f) a.ph[f].part = (f == 0 ? 2 : 1) * 16 * a.ph[f].cap * (a.ph[f].two ? 2 : 1);
+  for (int n = 0; n < kMaxTopK; ++n) a.by_slots[n] = make_div((n + 1) * a.ph[1].stages);
   a.b_off = kRingBytes;
   a.bbytes = static_cast<int>((left - tab) & ~size_t(15));
   a.tab_off = a.b_off + a.bbytes;

@@ -76,6 +76,39 @@ def test_layer_shapes(fmt, E, H, I, T, k, xt, yt):
     assert torch.equal(m(x, ids, w, y_dtype=DT[yt]), y)  # the same bits again
 
 
+@pytest.mark.parametrize("fmt,E,H,I,k,xt,yt", [
+    (Q40, 16, 512, 704, 6, "bf16", "bf16"), (Q40, 20, 256, 192, 16, "f16", "f32"),
+    (KSB, 16, 256, 512, 8, "f32", "f32"), (Q40, 4, 64, 64, 3, "f16", "f16"),
+    (Q40, 2, 64, 16384, 2, "f16", "f32"),       # a slot's h is too wide for the others to stay beside it
+    (Q40, 3, 2112, 320, 2, "bf16", "f32"),
+])
+def test_layer_single_token(fmt, E, H, I, k, xt, yt):
+    m = Layer(fmt, E, H, I)
+    x, ids, w = inputs(1, H, E, k, xt, seed=I + k)
+    w[0, 0] = -3.0                               # weights of any sign and size
+    if k > 2:
+        w[0, 1] = 1e-4
+    for change in (None, "skip", "twice", "none"):
+        if change == "skip":
+            ids[0, k // 2] = -1
+        if change == "twice":
+            ids[0, -1] = ids[0, 0]
+        if change == "none":
+            ids[:] = -1
+        y = m(x, ids, w, y_dtype=DT[yt])
+        m.check(y, x, ids, w)
+        assert torch.equal(m(x, ids, w, y_dtype=DT[yt]), y)
+    assert not y.any()
+
+
+def test_layer_single_tokens_and_batches_in_turn_on_one_workspace():
+    m = Layer(Q40, 8, 512, 192)
+    ws = torch.zeros(gq.gq_moe_workspace_bytes(gq.GQ_FMT_Q4_0, 512, 192, 9, 3), dtype=torch.uint8, device="cuda")
+    for n, T in enumerate((1, 1, 4, 1, 9, 9, 1, 1, 1, 2)):
+        x, ids, w = inputs(T, 512, 8, 3, "f16", seed=n, spread=10.0 ** (n % 5 - 2))
+        m.check(m(x, ids, w, y_dtype=torch.float32, workspace=ws), x, ids, w)
+
+
 @pytest.mark.parametrize("spread", [1e-6, 1e4])
 def test_layer_scales_of_activations(spread):
     m = Layer(Q40, 8, 512, 192)
