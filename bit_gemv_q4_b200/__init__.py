@@ -725,9 +725,8 @@ def gq_gemm_fp8(W: torch.Tensor, w_scales: torch.Tensor, X: torch.Tensor, x_scal
                 y_dtype=torch.bfloat16, out: torch.Tensor | None = None, workspace="auto",
                 flags: int = 0, dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [B, M] of W [M, K] in 128 x 128 blocks and X [B, K] in 1 x 128 blocks (codes and scales
-    as gq_quantize_fp8 returns them).  workspace: "auto" (a zeroed buffer cached per device and
-    stream) or a uint8 CUDA tensor of gq_gemm_fp8_workspace_bytes(M, K, B) bytes, zero before its
-    first use."""
+    as gq_quantize_fp8 returns them).  workspace: "auto" (a buffer cached per device and stream)
+    or a uint8 CUDA tensor of gq_gemm_fp8_workspace_bytes(M, K, B) bytes."""
     M, K = _fp8_pair(W, w_scales, 128, "W")
     B, K2 = _fp8_pair(X, x_scales, 1, "X")
     if K != K2:

@@ -11,15 +11,17 @@
 //
 // One CTA per SM, over tiles of 128 tokens x BN weight rows and k-steps of one
 // group:
-//  * warp 8 (producer): both operands' 128-byte rows by TMA, 128-byte swizzle;
-//  * warp 9 (MMA): four tcgen05.mma (K = 32) to a k-step, into one of two
-//    accumulator buffers in tensor memory;
-//  * warp 10 (scales): the factors of four k-steps at a time, ahead of their
+//  * warp 16 (producer): both operands' 128-byte rows by TMA, 128-byte swizzle;
+//  * warp 17 (MMA): four tcgen05.mma (K = 32) to a k-step, into one of the
+//    accumulator buffers in tensor memory (512 columns in all);
+//  * warp 18 (scales): the factors of four k-steps at a time, ahead of their
 //    use, into shared memory;
-//  * warps 0..7: read the buffer back and add it, times the factor, to sums in
-//    registers (a thread holds one token and BN / 2 columns); at the end of a
-//    tile they round once and store.
-// While the warps add one group the MMAs fill the other buffer.
+//  * warps 0..15: read the buffer back and add it, times the factor, to sums in
+//    registers (a thread holds one token and a quarter of the columns); at the
+//    end of a tile they round once and store, through shared memory and TMA
+//    where Y's rows allow it (from registers the stores of a 180 MB output cost
+//    48 us: the tile's sums have to leave before the next one's begin).
+// While the warps add one group the MMAs fill other buffers.
 //
 // With many tiles two CTAs of a cluster share one of 256 tokens x 256 weight
 // rows (cta_group::2): each holds its 128 tokens and half of the weight rows, so
@@ -28,11 +30,12 @@
 // The leader's MMA warp issues for both; loads of both count on its barriers,
 // commits arrive at both CTAs', and both epilogues release its buffers.
 //
-// When tiles are few, the k-steps of all tiles are divided evenly over the SMs
-// and a tile cut between CTAs is joined through fp32 partial sums in the
-// workspace: the CTA that completes it adds the parts in CTA order, so results
-// do not depend on scheduling.  For fewer than 128 tokens only the rows that
-// exist are loaded; the other lanes hold garbage that nothing reads.
+// When tiles are few, each is cut along K into the same number of pieces, which
+// leave fp32 sums in the workspace; a second launch adds them in order.  (Cutting
+// the k-steps of all tiles evenly and joining in the CTA that came last cost 10
+// us more at 37 tokens.)
+// For fewer than 128 tokens only the rows that exist are loaded; the other
+// lanes hold garbage that nothing reads.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -50,22 +53,19 @@ namespace {
 
 constexpr int kBM = 128;                 // tokens of a tile
 constexpr int kBK = 128;                 // bytes of K in a step: one group of scales
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kThreads = 32 * (kEpiWarps + 3);
+constexpr int kStoreBytes = 2048;        // 32 rows x 64 bytes of outputs, for each epilogue warp
 constexpr int kFactorSteps = 4;          // k-steps of a slot of factors
 constexpr int kFactorSlots = 3;
 constexpr int kFactorBytes = kFactorSlots * kFactorSteps * 2 * kBM * 4;  // for each half of the columns
 constexpr int kTileX = kBM * kBK;
-constexpr int kMaxCut = 4096;            // tiles of a split call at most
-constexpr size_t kCountBytes = kMaxCut * sizeof(int);
 
-// Unit u of T * S: k-step u % S of tile u / S.  CTA i of P takes units [U i / P, U (i + 1) / P),
-// or with `whole` the tiles i, i + P, ...
+// Tile t covers tokens rows * (t / tm) .. and weight rows BN * (t % tm) ..; it is
+// cut into `cuts` pieces along its S k-steps.  CTA (or pair) i of P takes pieces
+// i, i + P, ...
 struct Split {
-  int64_t U;
-  int S, T, P;
-  int whole;
-  int tm;  // tiles along M; tile t covers tokens 128 (t / tm) and weight rows BN (t % tm)
+  int S, T, P, tm, cuts;
 };
 
 struct Args {
@@ -78,8 +78,7 @@ struct Args {
   int B, kblocks, ytype, xrows;  // xrows: rows of an X box
   int ybytes;                    // alignment of Y's rows, 16 or 32 bytes, or 0
   Split sp;
-  int* counts;
-  float* parts;  // [P][2][rows][BN]
+  float* parts;  // [pieces][rows][BN] of cut tiles
 };
 
 extern __shared__ __align__(1024) uint8_t fsm[];
@@ -109,12 +108,6 @@ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void store32(void* p, const uint32_t v[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 __device__ __forceinline__ uint32_t pack2(float a, float b, int type) {
   if (type == GQ_F16) {
     const __half2 h = __floats2half2_rn(a, b);
@@ -124,92 +117,92 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, int type) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// N (a multiple of 16) consecutive outputs of one token from weight row m on.
+// N consecutive outputs of one token from weight row m on.
 template <int N>
 __device__ __forceinline__ void store_row(const Args& a, int64_t row, int64_t m, const float* v) {
   const int64_t at = row * a.M + m;
-  if (a.ybytes && m + N <= a.M) {
-    if (a.ytype == GQ_F32) {
-      float* d = static_cast<float*>(a.Y) + at;
-#pragma unroll
-      for (int i = 0; i < N; i += 8) {
-        if (a.ybytes == 32) {
-          store32(d + i, reinterpret_cast<const uint32_t*>(v + i));
-        } else {
-          *reinterpret_cast<float4*>(d + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-          *reinterpret_cast<float4*>(d + i + 4) = make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
-        }
-      }
-    } else {
-      uint16_t* d = static_cast<uint16_t*>(a.Y) + at;
-#pragma unroll
-      for (int i = 0; i < N; i += 16) {
-        uint32_t p[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = pack2(v[i + 2 * j], v[i + 2 * j + 1], a.ytype);
-        if (a.ybytes == 32) {
-          store32(d + i, p);
-        } else {
-          *reinterpret_cast<uint4*>(d + i) = make_uint4(p[0], p[1], p[2], p[3]);
-          *reinterpret_cast<uint4*>(d + i + 8) = make_uint4(p[4], p[5], p[6], p[7]);
-        }
-      }
-    }
-    return;
-  }
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (m + i < a.M) store_elem(a.Y, at + i, v[i], a.ytype);
 }
 
-__device__ __forceinline__ int64_t unit_begin(const Split& sp, int i) { return sp.U * i / sp.P; }
-__device__ __forceinline__ int unit_owner(const Split& sp, int64_t u) {
-  return static_cast<int>(((u + 1) * sp.P - 1) / sp.U);
+// This thread's bulk stores have read their shared memory (READ), or are done.
+template <bool READ>
+__device__ __forceinline__ void bulk_stores_wait() {
+  if constexpr (READ) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  else asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// The tiles of a CTA's run and the k-steps of each: a cut first or last tile
-// before the whole ones between them, so that cut tiles complete early.
-struct Run {
-  int ta, tb, S, stride;
-  int64_t u0, u1;
-  __device__ __forceinline__ int count() const { return (tb - ta) / stride + 1; }
-  __device__ __forceinline__ int64_t steps() const { return stride > 1 ? static_cast<int64_t>(count()) * S : u1 - u0; }
-  __device__ __forceinline__ void get(int k, int& t, int& k0, int& k1) const {
-    if (stride > 1) {
-      t = ta + k * stride;
-      k0 = 0;
-      k1 = S;
-      return;
+// A warp's 32 tokens x N columns (lane: token) from column m, token row on: 64
+// bytes of each row at a time through `buf` (64-byte swizzle, so that lanes
+// write without bank conflicts).  Rows and columns past Y's end are not stored.
+template <int N>
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, uint8_t* buf, const float* v, int m, int row,
+                                           int64_t M, int type) {
+  const int lane = threadIdx.x & 31, turn = (lane >> 1) & 3;
+  auto send = [&](int col) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && col < M) {
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(col),
+                   "r"(row), "r"(smem_addr(buf))
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      bulk_stores_wait<true>();
     }
-    t = (k == 0) ? ta : (k == 1) ? tb : ta + k - 1;
-    k0 = (t == ta) ? static_cast<int>(u0 - static_cast<int64_t>(ta) * S) : 0;
-    k1 = (t == tb) ? static_cast<int>(u1 - static_cast<int64_t>(tb) * S) : S;
+    __syncwarp();
+  };
+  if (type == GQ_F32) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4*>(buf + lane * 64 + ((q ^ turn) << 4)) =
+            make_float4(v[c + 4 * q], v[c + 4 * q + 1], v[c + 4 * q + 2], v[c + 4 * q + 3]);
+      send(m + c);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(buf + lane * 64 + ((q ^ turn) << 4)) =
+            make_uint4(pack2(v[c + 8 * q], v[c + 8 * q + 1], type), pack2(v[c + 8 * q + 2], v[c + 8 * q + 3], type),
+                       pack2(v[c + 8 * q + 4], v[c + 8 * q + 5], type), pack2(v[c + 8 * q + 6], v[c + 8 * q + 7], type));
+      send(m + c);
+    }
+  }
+}
+
+// The pieces of a CTA (or pair).
+struct Run {
+  int first;
+  const Split& sp;
+  __device__ __forceinline__ int count() const { return (sp.T * sp.cuts - first + sp.P - 1) / sp.P; }
+  __device__ __forceinline__ void get(int k, int& t, int& k0, int& k1) const {
+    const int p = first + k * sp.P, c = p % sp.cuts;
+    t = p / sp.cuts;
+    k0 = static_cast<int>(static_cast<int64_t>(sp.S) * c / sp.cuts);
+    k1 = static_cast<int>(static_cast<int64_t>(sp.S) * (c + 1) / sp.cuts);
+  }
+  __device__ __forceinline__ int64_t steps() const {
+    int64_t n = 0;
+    for (int k = 0; k < count(); ++k) {
+      int t, k0, k1;
+      get(k, t, k0, k1);
+      n += k1 - k0;
+    }
+    return n;
   }
 };
-__device__ __forceinline__ Run run_of(const Split& sp, int i) {
-  Run r;
-  r.S = sp.S;
-  r.stride = 1;
-  if (sp.whole) {  // at least two CTAs
-    r.ta = i;
-    r.tb = sp.T - 1;
-    r.stride = sp.P;
-    r.u0 = r.u1 = 0;
-    return r;
-  }
-  r.u0 = unit_begin(sp, i);
-  r.u1 = unit_begin(sp, i + 1);
-  r.ta = static_cast<int>(r.u0 / sp.S);
-  r.tb = static_cast<int>((r.u1 - 1) / sp.S);
-  return r;
-}
 
 template <int BN, bool PAIR>
 struct Cfg {
   static constexpr int kRowsW = PAIR ? BN / 2 : BN;  // weight rows in this CTA's shared memory
   static constexpr int kStageBytes = kTileX + kRowsW * kBK;
-  static constexpr int kStages = kRowsW == 256 ? 4 : 6;
-  static constexpr int kSmem = kStages * kStageBytes + kFactorBytes + 1024 + 256;
+  static constexpr int kStages = 5;
+  static constexpr int kBufs = 512 / BN;  // accumulator buffers
+  static constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kStoreBytes + kFactorBytes + 1024 + 256;
 };
 
 // ------------------------------------------------------------ pairs of CTAs
@@ -279,27 +272,26 @@ __device__ __forceinline__ void leader_arrive(uint64_t* bar) {
 template <int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-                    const Args a) {
+                    const __grid_constant__ CUtensorMap ymap, const __grid_constant__ Args a) {
   using C = Cfg<BN, PAIR>;
-  constexpr int kStages = C::kStages, kHalf = BN / 2;
+  constexpr int kStages = C::kStages, kBufs = C::kBufs, kCols = BN / (kEpiWarps / 4);  // columns of an epilogue warp
   const uint32_t base = smem_addr(fsm);
   const uint32_t ring = ((base + 1023u) & ~1023u) - base;
-  float* factors = reinterpret_cast<float*>(fsm + ring + kStages * C::kStageBytes);  // [slot][step][half][token]
-  uint64_t* full = reinterpret_cast<uint64_t*>(fsm + ring + kStages * C::kStageBytes + kFactorBytes);
+  uint8_t* staging = fsm + ring + kStages * C::kStageBytes;
+  float* factors = reinterpret_cast<float*>(staging + kEpiWarps * kStoreBytes);  // [slot][step][half][token]
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStoreBytes + kFactorBytes);
   uint64_t* empty = full + kStages;
-  uint64_t* d_full = empty + kStages;  // [2] a group's sums are in the buffer
-  uint64_t* d_empty = d_full + 2;      // [2] they have been read
-  uint64_t* done = d_empty + 2;        // every MMA of the CTA has finished
+  uint64_t* d_full = empty + kStages;  // [buffers] a group's sums are in the buffer
+  uint64_t* d_empty = d_full + kBufs;  // [buffers] they have been read
+  uint64_t* done = d_empty + kBufs;        // every MMA of the CTA has finished
   uint64_t* f_full = done + 1;         // [slots] factors
   uint64_t* f_empty = f_full + kFactorSlots;
-  uint64_t* e_bar = f_empty + kFactorSlots;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(e_bar + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(f_empty + kFactorSlots);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  int* last_flag = abort_flag + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
-  const Run run = run_of(a.sp, PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x));
+  const Run run{PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x), a.sp};
   constexpr int kRows = PAIR ? 2 * kBM : kBM;  // tokens of a tile
   const int nrun = run.count();
   if (threadIdx.x == 0) {
@@ -307,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBufs; ++i) {
       mbar_init(&d_full[i], 1);
       mbar_init(&d_empty[i], PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
@@ -316,12 +308,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&f_empty[i], kEpiWarps);
     }
     mbar_init(done, 1);
-    mbar_init(e_bar, kEpiWarps);
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == kEpiWarps + 1) {
-    acc_alloc<PAIR>(tmem_slot, 2 * BN);
+    acc_alloc<PAIR>(tmem_slot, kBufs * BN);
   }
   tc_fence_before();
   if (PAIR) cluster_sync_all();  // both CTAs' barriers are there
@@ -378,9 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0;
     uint32_t phase = 0;
     for (int64_t g = 0; g < steps; ++g) {
-      const int buf = static_cast<int>(g & 1);
-      const uint32_t dphase = (static_cast<uint32_t>(g >> 1) & 1u) ^ 1u;
-      ok = mbar_wait(&full[s], phase, a.budget) && mbar_wait(&d_empty[buf], dphase, a.budget) && !aborted();
+      const int buf = static_cast<int>(g % kBufs);
+      const uint32_t dphase = (static_cast<uint32_t>(g / kBufs) & 1u) ^ 1u;
+      ok = mbar_wait(&full[s], phase, a.budget) && mbar_wait(&d_empty[buf], dphase, a.budget);
       if (!__all_sync(0xFFFFFFFFu, ok)) {
         ok = false;
         break;
@@ -452,18 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) fail();
   } else {
     // ---------------------------------------------------------- epilogue
-    const int quarter = warp & 3, half = warp >> 2;
+    const int quarter = warp & 3, half = (warp >> 2) * kCols / (BN / 2);  // rows; which factors
     const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
-    const int cols0 = half * kHalf;
+    const int cols0 = (warp >> 2) * kCols;
     const int prows = min(kBM, a.B);  // rows of a part
-    uint32_t ephase = 0;
-    auto epi_sync = [&]() -> bool {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(e_bar);
-      const bool r = mbar_wait(e_bar, ephase & 1u, a.budget);
-      ++ephase;
-      return r;
-    };
     auto release = [&](int buf) {  // the buffer may be filled again
       if (PAIR) leader_arrive(&d_empty[buf]);
       else mbar_arrive(&d_empty[buf]);
@@ -478,40 +461,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = row0 + 32 * quarter + lane;
       const bool row_ok = row < a.B;
       const bool any = row0 + 32 * quarter < a.B;  // some lane of the warp has a token
-      float2 acc2[kHalf / 2];
+      float2 acc2[kCols / 2];
 #pragma unroll
-      for (int i = 0; i < kHalf / 2; ++i) acc2[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < kCols / 2; ++i) acc2[i] = make_float2(0.f, 0.f);
       float* acc = reinterpret_cast<float*>(acc2);
       for (int ks = k0; ks < k1; ++ks, ++g) {
-        const int buf = g & 1;
+        const int buf = g % kBufs;
         const int fs = fq % kFactorSlots, fj = (ks - k0) % kFactorSteps;
         bool got = fj != 0 || mbar_wait(&f_full[fs], (fq / kFactorSlots) & 1u, a.budget);
         const float fac = factors[((fs * kFactorSteps + fj) * 2 + half) * kBM + 32 * quarter + lane];
-        got = got && mbar_wait(&d_full[buf], (g >> 1) & 1u, a.budget);
-        if (!__all_sync(0xFFFFFFFFu, got) || aborted()) {
+        got = got && mbar_wait(&d_full[buf], (g / kBufs) & 1u, a.budget);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (any) {
-          // 16 columns at a time: the next ones are on their way while these are added
+          // 16 columns at a time; four warps on each scheduler take turns
           const float2 f = make_float2(fac, fac);
           const uint32_t src = tmem + lane_base + static_cast<uint32_t>(buf * BN + cols0);
-          uint32_t v[2][16];
-          tmem_ld16(src, v[0]);
 #pragma unroll
-          for (int c = 0; c < kHalf / 16; ++c) {
+          for (int c = 0; c < kCols / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld16(src + 16 * c, v);
             tmem_wait_ld();
-            if (c + 1 < kHalf / 16) {
-              tmem_ld16(src + 16 * (c + 1), v[(c + 1) & 1]);
-            } else {  // the buffer is free
+            if (c + 1 == kCols / 16) {  // the buffer is free
               tc_fence_before();
               __syncwarp();
               if (lane == 0) release(buf);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              acc2[8 * c + i] = __ffma2_rn(f, make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])),
+              acc2[8 * c + i] = __ffma2_rn(f, make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
                                            acc2[8 * c + i]);
           }
         } else if (lane == 0) {
@@ -524,49 +505,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      if (k1 - k0 == a.sp.S) {
-        if (row_ok) store_row<kHalf>(a, row, m0 + cols0, acc);
-        continue;
-      }
-      // a cut tile: publish this part; the CTA that completes the tile adds
-      // the parts in CTA order and resets the count
-      const int slot = (t == run.ta) ? 0 : 1;
-      const int prow = 32 * quarter + lane;
-      if (row_ok) {
-        float4* d = reinterpret_cast<float4*>(
-            a.parts + ((static_cast<int64_t>(blockIdx.x) * 2 + slot) * prows + prow) * BN + cols0);
+      if (a.sp.cuts > 1) {  // a piece: its sums go to the workspace
+        const int prow = 32 * quarter + lane;
+        if (row_ok) {
+          float4* d = reinterpret_cast<float4*>(
+              a.parts + (static_cast<int64_t>(run.first + k * a.sp.P) * prows + prow) * BN + cols0);
 #pragma unroll
-        for (int i = 0; i < kHalf / 4; ++i)
-          __stcg(d + i, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
-      }
-      __threadfence();
-      if (!(ok = __all_sync(0xFFFFFFFFu, epi_sync()))) break;
-      if (threadIdx.x == 0)
-        *reinterpret_cast<volatile int*>(last_flag) =
-            atomicAdd(&a.counts[t], k1 - k0) + (k1 - k0) == a.sp.S;
-      if (!(ok = __all_sync(0xFFFFFFFFu, epi_sync()))) break;
-      if (!*reinterpret_cast<volatile int*>(last_flag)) continue;
-      __threadfence();
-      const int64_t first = static_cast<int64_t>(t) * a.sp.S;
-      const int i0 = unit_owner(a.sp, first), i1 = unit_owner(a.sp, first + a.sp.S - 1);
-      if (row_ok) {
-        for (int i = i0; i <= i1; ++i) {
-          const int sl = (unit_begin(a.sp, i) / a.sp.S == t) ? 0 : 1;
-          const float4* p = reinterpret_cast<const float4*>(
-              a.parts + ((static_cast<int64_t>(i) * 2 + sl) * prows + prow) * BN + cols0);
-#pragma unroll
-          for (int q = 0; q < kHalf / 4; ++q) {
-            const float4 v = __ldcg(p + q);
-            acc[4 * q] = (i == i0 ? 0.f : acc[4 * q]) + v.x;
-            acc[4 * q + 1] = (i == i0 ? 0.f : acc[4 * q + 1]) + v.y;
-            acc[4 * q + 2] = (i == i0 ? 0.f : acc[4 * q + 2]) + v.z;
-            acc[4 * q + 3] = (i == i0 ? 0.f : acc[4 * q + 3]) + v.w;
-          }
+          for (int i = 0; i < kCols / 4; ++i)
+            __stcg(d + i, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
         }
-        store_row<kHalf>(a, row, m0 + cols0, acc);
+      } else if (a.ybytes) {
+        if (any) store_tile<kCols>(&ymap, staging + warp * kStoreBytes, acc, static_cast<int>(m0) + cols0,
+                                   row0 + 32 * quarter, a.M, a.ytype);
+      } else if (row_ok) {
+        store_row<kCols>(a, row, m0 + cols0, acc);
       }
-      if (threadIdx.x == 0) a.counts[t] = 0;
     }
+    bulk_stores_wait<false>();
     if (!ok && lane == 0) fail();
   }
 
@@ -580,13 +535,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
   }
   if (PAIR) cluster_sync_all();
-  if (warp == kEpiWarps + 1) acc_dealloc<PAIR>(tmem, 2 * BN);
+  if (warp == kEpiWarps + 1) acc_dealloc<PAIR>(tmem, kBufs * BN);
+}
+
+// Y of a call whose tiles (of BN weight rows) were cut: the pieces' sums in
+// order, four weight rows of a token to a thread.
+template <int BN>
+__global__ void __launch_bounds__(256) fp8_sum_kernel(const float* parts, void* Y, int64_t M, int B, int rows, int tm,
+                                                      int cuts, int ytype) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t quads = static_cast<int64_t>(tm) * (BN / 4);
+  const int64_t b = i / quads, q = i - b * quads;
+  if (b >= B) return;
+  const int64_t m = q * 4;
+  const int tile = static_cast<int>(b / kBM) * tm + static_cast<int>(m / BN);
+  const float4* p = reinterpret_cast<const float4*>(
+      parts + (static_cast<int64_t>(tile) * cuts * rows + b % kBM) * BN + m % BN);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < cuts; ++c) {
+    const float4 u = __ldcg(p + static_cast<int64_t>(c) * rows * (BN / 4));
+    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+  }
+  const float o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (m + j < M) store_elem(Y, b * M + m + j, o[j], ytype);
 }
 
 // ------------------------------------------------------------------- host
-// Tiles of a pair of CTAs run the tensor core best (less shared-memory traffic
-// for each multiply-add) and are taken when there are enough of them; otherwise
-// tiles of 128 x 128, whole ones if they fill most of the SMs, else cut.
+// Tiles of 128 x 128 take one unit of time for a k-step (0.42 us) and about
+// three more for a tile or piece; a second launch to add pieces up and its
+// traffic take about eight.  A pair's 256 x 256 tile takes 1.55 units a k-step, on
+// half as many SM pairs.  The plan with the shortest longest CTA is taken.
+// Measured, 128 x 128 (uncut) against pairs: 500 tokens x 4096 x 4096, 17.6 and
+// 23.6 us; 1000 tokens, 30.9 and 24.9; 200 tokens x 11008 x 4096, 39.3 and 24.1;
+// 2048 tokens, 131 and 99.5.  One piece against four: 128 tokens x 4096 x 4096,
+// 16.0 and 13.2; x 4096 x 11008, 35.2 and 19.6.
 struct Choice {
   int bn;
   bool pair;
@@ -595,27 +581,34 @@ struct Choice {
 Choice choose(int64_t M, int64_t K, int64_t B) {
   const int64_t sms = sm_count();
   const int64_t S = (K + kBK - 1) / kBK;
-  auto split = [&](int rows, int bn, int64_t ctas, bool whole) {
+  auto split = [&](int rows, int bn, int64_t ctas, int64_t cuts) {
     Split s;
     s.S = static_cast<int>(S);
     s.tm = static_cast<int>((M + bn - 1) / bn);
     s.T = static_cast<int>((B + rows - 1) / rows * s.tm);
-    s.U = static_cast<int64_t>(s.T) * S;
-    s.P = static_cast<int>(i64min(ctas, whole ? s.T : s.U));
-    s.whole = whole && s.P > 1;
+    s.cuts = static_cast<int>(cuts);
+    s.P = static_cast<int>(i64min(ctas, s.T * cuts));
     return s;
   };
   const int64_t tpair = (B + 255) / 256 * ((M + 255) / 256), t128 = (B + 127) / 128 * ((M + 127) / 128);
-  if (tpair >= sms && B > 128) return Choice{256, true, split(256, 256, sms / 2, true)};
-  if (t128 > sms || (10 * t128 >= 8 * sms && B > 64)) return Choice{128, false, split(128, 128, sms, true)};
-  return Choice{128, false, split(128, 128, sms, false)};
+  const int64_t whole = (t128 + sms - 1) / sms * (S + 3);
+  const int64_t pairs = (tpair + sms / 2 - 1) / (sms / 2) * (S + 3) * 14 / 9;
+  int64_t best = 1, least = whole;
+  for (int64_t c = 2; c <= 16 && c <= S && t128 < 2 * sms; ++c) {
+    const int64_t steps = (t128 * c + sms - 1) / sms * ((S + c - 1) / c + 3) + 8;
+    if (steps < least) {
+      least = steps;
+      best = c;
+    }
+  }
+  if (B > 128 && pairs < least) return Choice{256, true, split(256, 256, sms / 2, 1)};
+  return Choice{128, false, split(128, 128, sms, best)};
 }
 
-size_t ws_bytes_of(const Choice& c, int64_t B) {
-  if (B <= kFp8GemvMaxB) return 0;
-  if (c.sp.whole || c.sp.P == 1) return kCountBytes;  // no parts
+size_t ws_bytes_of(const Choice& c, int64_t M, int64_t K, int64_t B) {
+  if (fp8_gemv_takes(M, K, B) || c.sp.cuts == 1) return 0;
   const int64_t rows = B < kBM ? B : kBM;
-  return kCountBytes + static_cast<size_t>(c.sp.P) * 2 * static_cast<size_t>(rows) * c.bn * sizeof(float);
+  return static_cast<size_t>(c.sp.T) * c.sp.cuts * static_cast<size_t>(rows) * c.bn * sizeof(float);
 }
 
 bool gemm_dims(int64_t M, int64_t K, int64_t B) {
@@ -624,22 +617,23 @@ bool gemm_dims(int64_t M, int64_t K, int64_t B) {
   return t <= 0x7FFFFFFFLL;
 }
 
-gq_status encode(CUtensorMap* map, const void* p, int64_t rows, int64_t K, int box_rows) {
+gq_status encode(CUtensorMap* map, CUtensorMapDataType type, int esize, const void* p, int64_t rows, int64_t cols,
+                 int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
   EncodeTiled enc = tensor_map_encoder();
   if (!enc) return GQ_ERR_CUDA;
-  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(K)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK), static_cast<cuuint32_t>(box_rows)};
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(cols) * esize};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t es[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dim, stride, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+  return enc(map, type, 2, const_cast<void*>(p), dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? GQ_OK
              : GQ_ERR_CUDA;
 }
 
 template <int BN, bool PAIR>
-gq_status launch_fp8(const CUtensorMap& xmap, const CUtensorMap& wmap, const Args& a, bool pdl, cudaStream_t s) {
+gq_status launch_fp8(const CUtensorMap& xmap, const CUtensorMap& wmap, const CUtensorMap& ymap, const Args& a,
+                     bool pdl, cudaStream_t s) {
   auto kern = fp8_gemm_kernel<BN, PAIR>;
   constexpr int smem = Cfg<BN, PAIR>::kSmem;
   thread_local unsigned long long configured_ctx = 0;  // per host thread and context
@@ -651,8 +645,9 @@ gq_status launch_fp8(const CUtensorMap& xmap, const CUtensorMap& wmap, const Arg
   }
   if (PAIR)
     return launch_cluster(kern, dim3(static_cast<unsigned>(2 * a.sp.P)), dim3(kThreads), smem, s, pdl, 2u, xmap,
-                          wmap, a);
-  return launch(kern, dim3(static_cast<unsigned>(a.sp.P)), dim3(kThreads), smem, s, pdl, xmap, wmap, a);
+                          wmap, ymap, a);
+  return launch(kern, dim3(static_cast<unsigned>(a.sp.P)), dim3(kThreads), smem, s, pdl, xmap, wmap, ymap,
+                a);
 }
 
 }  // namespace
@@ -662,7 +657,7 @@ extern "C" {
 
 GQ_API size_t gq_gemm_fp8_workspace_bytes(int64_t M, int64_t K, int64_t B) {
   if (M <= 0 || K <= 0 || B <= 0 || !gq::gemm_dims(M, K, B)) return 0;
-  return gq::ws_bytes_of(gq::choose(M, K, B), B);
+  return gq::ws_bytes_of(gq::choose(M, K, B), M, K, B);
 }
 
 GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, int64_t K, const void* X,
@@ -686,11 +681,11 @@ GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, in
   if (misaligned16(W) || misaligned16(X) || misaligned16(w_scales) || misaligned16(x_scales))
     return GQ_ERR_ALIGNMENT;
   const Choice c = choose(M, K, B);
-  const size_t need = ws_bytes_of(c, B);
+  const size_t need = ws_bytes_of(c, M, K, B);
   if (need && (!workspace || ws_bytes < need)) return GQ_ERR_WORKSPACE;
   if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return GQ_ERR_ALIGNMENT;
   const bool pdl = (flags & GQ_GEMV_PDL) != 0;
-  if (B <= kFp8GemvMaxB) return fp8_gemv(W, w_scales, M, K, X, x_scales, B, Y, y_dtype, pdl, s);
+  if (fp8_gemv_takes(M, K, B)) return fp8_gemv(W, w_scales, M, K, X, x_scales, B, Y, y_dtype, pdl, s);
 
   Args a{};
   a.sx = x_scales;
@@ -703,16 +698,27 @@ GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, in
   a.kblocks = static_cast<int>((K + kBK - 1) / kBK);
   a.ytype = y_dtype;
   a.xrows = static_cast<int>(B < kBM ? (B + 7) / 8 * 8 : kBM);
-  const int64_t align = static_cast<int64_t>((reinterpret_cast<uintptr_t>(Y) | static_cast<uintptr_t>(M * dtype_size(y_dtype))) & 31u);
-  a.ybytes = align == 0 ? 32 : align == 16 ? 16 : 0;
+  const int esize = dtype_size(y_dtype);
+  a.ybytes = M * esize % 16 == 0 ? 16 : 0;  // rows that TMA can store
   a.sp = c.sp;
-  a.counts = static_cast<int*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCountBytes);
-  CUtensorMap xmap, wmap;
-  gq_status st = encode(&xmap, X, B, K, a.xrows);
-  if (st == GQ_OK) st = encode(&wmap, W, M, K, 128);
+  a.parts = static_cast<float*>(workspace);
+  CUtensorMap xmap, wmap, ymap = {};
+  gq_status st = encode(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, X, B, K, kBK, a.xrows, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == GQ_OK) st = encode(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, M, K, kBK, c.pair ? c.bn / 2 : c.bn,
+                                 CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == GQ_OK && a.ybytes)
+    st = encode(&ymap,
+                y_dtype == GQ_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                : y_dtype == GQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                esize, Y, B, M, 64 / esize, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (st != GQ_OK) return st;
-  return c.pair ? launch_fp8<256, true>(xmap, wmap, a, pdl, s) : launch_fp8<128, false>(xmap, wmap, a, pdl, s);
+  if (c.pair) return launch_fp8<256, true>(xmap, wmap, ymap, a, pdl, s);
+  st = launch_fp8<128, false>(xmap, wmap, ymap, a, pdl, s);
+  if (st != GQ_OK || c.sp.cuts == 1) return st;
+  const int64_t threads = B * c.sp.tm * (128 / 4);
+  return launch(fp8_sum_kernel<128>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, s, true,
+                a.parts, Y, M, a.B, static_cast<int>(B < kBM ? B : kBM), c.sp.tm, c.sp.cuts, y_dtype);
 }
 
 }  // extern "C"

@@ -12,7 +12,7 @@
 // four lanes a whole 64-byte piece.  A group's sums come out of four MMAs and
 // are added, times its two scales, in fp32.
 //
-// A CTA takes 16 or 32 weight rows and all of K, which its eight warps share
+// A CTA takes 16 weight rows and all of K, which its eight warps share
 // group by group; their sums are added in warp order through shared memory.  A
 // warp reads several groups of weights at once: what is in flight, not
 // arithmetic, sets the rate.
@@ -57,42 +57,40 @@ __device__ __forceinline__ uint4 read_once(const uint8_t* p) {
   return v;
 }
 
-// NT tiles of 8 tokens, RG groups of 16 weight rows, `AHEAD` groups of K read at
-// once.  blockIdx.y: tokens 8 NT at a time.
-template <int NT, int RG, int AHEAD>
+// NT tiles of 8 tokens; AHEAD groups of K read at once (four, at two CTAs to an
+// SM: fewer at three or four CTAs were slower, and so were CTAs that go through
+// several row groups, reading the next one's weights before joining).
+template <int NT, int AHEAD>
 __global__ void __launch_bounds__(kThreads) fp8_gemv_kernel(const Args a) {
-  __shared__ float part[kWarps][16 * RG][8 * NT + 1];
+  __shared__ float part[kWarps][16][8 * NT + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * (16 * RG);
-  const int b0 = blockIdx.y * (8 * NT);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16;
   pdl_launch_dependents();
   pdl_wait();
-  const uint8_t* w[2 * RG];  // rows g8 and g8 + 8 of each row group (the last row stands in for those past it)
+  const uint8_t* w[2];  // rows g8 and g8 + 8 (the last row stands in for those past it)
 #pragma unroll
-  for (int i = 0; i < 2 * RG; ++i) w[i] = a.W + i64min(m0 + 8 * i + g8, a.M - 1) * a.K + 16 * t;
+  for (int i = 0; i < 2; ++i) w[i] = a.W + i64min(m0 + 8 * i + g8, a.M - 1) * a.K + 16 * t;
   const uint8_t* x[NT];
   const float* sx[NT][2];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    x[j] = a.X + static_cast<int64_t>(min(b0 + 8 * j + g8, a.B - 1)) * a.K + 16 * t;
+    x[j] = a.X + static_cast<int64_t>(min(8 * j + g8, a.B - 1)) * a.K + 16 * t;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      sx[j][i] = a.sx + static_cast<int64_t>(min(b0 + 8 * j + 2 * t + i, a.B - 1)) * a.groups;
+      sx[j][i] = a.sx + static_cast<int64_t>(min(8 * j + 2 * t + i, a.B - 1)) * a.groups;
   }
   const float* sw = a.sw + m0 / 128 * a.groups;
-  float acc[RG][NT][4];
+  float acc[NT][4];
 #pragma unroll
-  for (int r = 0; r < RG; ++r)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[r][j][0] = acc[r][j][1] = acc[r][j][2] = acc[r][j][3] = 0.f;
+  for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 
   for (int g0 = warp; g0 < a.groups; g0 += kWarps * AHEAD) {
-    uint4 wv[AHEAD][2 * RG][2];
+    uint4 wv[AHEAD][2][2];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       const int g = g0 + kWarps * u;
 #pragma unroll
-      for (int i = 0; i < 2 * RG; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int64_t k = static_cast<int64_t>(g) * 128 + 64 * h;
@@ -113,44 +111,37 @@ __global__ void __launch_bounds__(kThreads) fp8_gemv_kernel(const Args a) {
           xv[h] = k + 16 * t < a.K ? __ldg(reinterpret_cast<const uint4*>(x[j] + k)) : make_uint4(0, 0, 0, 0);
         }
         const float f0 = s * __ldg(sx[j][0] + g), f1 = s * __ldg(sx[j][1] + g);
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < RG; ++r) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 lo = wv[u][2 * r][h], hi = wv[u][2 * r + 1][h];
-            mma_e4m3(c, lo.x, hi.x, lo.y, hi.y, xv[h].x, xv[h].y);
-            mma_e4m3(c, lo.z, hi.z, lo.w, hi.w, xv[h].z, xv[h].w);
-          }
-          acc[r][j][0] = fmaf(f0, c[0], acc[r][j][0]);
-          acc[r][j][1] = fmaf(f1, c[1], acc[r][j][1]);
-          acc[r][j][2] = fmaf(f0, c[2], acc[r][j][2]);
-          acc[r][j][3] = fmaf(f1, c[3], acc[r][j][3]);
+        for (int h = 0; h < 2; ++h) {
+          const uint4 lo = wv[u][0][h], hi = wv[u][1][h];
+          mma_e4m3(c, lo.x, hi.x, lo.y, hi.y, xv[h].x, xv[h].y);
+          mma_e4m3(c, lo.z, hi.z, lo.w, hi.w, xv[h].z, xv[h].w);
         }
+        acc[j][0] = fmaf(f0, c[0], acc[j][0]);
+        acc[j][1] = fmaf(f1, c[1], acc[j][1]);
+        acc[j][2] = fmaf(f0, c[2], acc[j][2]);
+        acc[j][3] = fmaf(f1, c[3], acc[j][3]);
       }
     }
   }
 #pragma unroll
-  for (int r = 0; r < RG; ++r)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[warp][16 * r + g8 + 8 * (i >> 1)][8 * j + 2 * t + (i & 1)] = acc[r][j][i];
+    for (int i = 0; i < 4; ++i) part[warp][g8 + 8 * (i >> 1)][8 * j + 2 * t + (i & 1)] = acc[j][i];
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * RG * 8 * NT; i += kThreads) {
-    const int row = i % (16 * RG), c = i / (16 * RG);
+  for (int i = threadIdx.x; i < 16 * 8 * NT; i += kThreads) {
+    const int row = i % 16, c = i / 16;
     float v = 0.f;
 #pragma unroll
     for (int q = 0; q < kWarps; ++q) v += part[q][row][c];
-    if (m0 + row < a.M && b0 + c < a.B) store_elem(a.Y, static_cast<int64_t>(b0 + c) * a.M + m0 + row, v, a.ytype);
+    if (m0 + row < a.M && c < a.B) store_elem(a.Y, static_cast<int64_t>(c) * a.M + m0 + row, v, a.ytype);
   }
 }
 
-template <int NT, int RG, int AHEAD>
+template <int NT, int AHEAD>
 gq_status run(const Args& a, bool pdl, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((a.M + 16 * RG - 1) / (16 * RG)),
-                  static_cast<unsigned>((a.B + 8 * NT - 1) / (8 * NT)));
-  return launch(fp8_gemv_kernel<NT, RG, AHEAD>, grid, dim3(kThreads), 0, s, pdl, a);
+  return launch(fp8_gemv_kernel<NT, AHEAD>, dim3(static_cast<unsigned>((a.M + 15) / 16)), dim3(kThreads), 0, s, pdl, a);
 }
 
 }  // namespace
@@ -159,8 +150,8 @@ gq_status fp8_gemv(const void* W, const float* sw, int64_t M, int64_t K, const v
                    int64_t B, void* Y, int yt, bool pdl, cudaStream_t s) {
   Args a{static_cast<const uint8_t*>(W), sw, static_cast<const uint8_t*>(X), sx, Y, M, K, static_cast<int>(B),
          static_cast<int>((K + 127) / 128), yt};
-  if (B <= 8) return run<1, 1, 4>(a, pdl, s);
-  return run<2, 1, 4>(a, pdl, s);
+  if (B <= 8) return run<1, 4>(a, pdl, s);
+  return run<2, 4>(a, pdl, s);
 }
 
 }  // namespace gq

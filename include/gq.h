@@ -475,10 +475,8 @@ GQ_API gq_status gq_dequantize_fp8(const void* q, const float* scales, int64_t R
  * core, the groups' sums times the two scales' fp32 product added in fp32,
  * rounded once to y_dtype.  Results do not depend on scheduling.
  * workspace / ws_bytes: at least gq_gemm_fp8_workspace_bytes(M, K, B) bytes
- *   (GQ_ERR_WORKSPACE otherwise), 256-byte aligned, all zero before its first
- *   use; a successful call leaves it ready for the next call of any sizes;
- *   after a call that fails or reports GQ_DEV_TIMEOUT, zero it again.  Calls
- *   that may run at the same time need separate workspaces.
+ *   (GQ_ERR_WORKSPACE otherwise; 0 for many shapes), 256-byte aligned, of any
+ *   contents.  Calls that may run at the same time need separate workspaces.
  * flags: 0 or GQ_GEMV_PDL (the call may be scheduled early; it waits for the
  *   preceding kernel before it reads anything).
  * dev_status: optional, receives GQ_DEV_TIMEOUT if a pipeline wait gives up. */

@@ -55,7 +55,8 @@ def test_gemm_refusals():
         assert call(**{n: None}) == INVALID
         assert call(**{n: A + 4}) == ALIGN
     assert call(st=A + 1) == ALIGN
-    need = gq.gq_gemm_fp8_workspace_bytes(256, 128, 100)
+    need = gq.gq_gemm_fp8_workspace_bytes(256, 4096, 100)
+    ok["K"] = 4096
     assert call(B=100, work=None) == WORKSPACE and call(B=100, wb=need - 1) == WORKSPACE
     assert call(B=100, work=A + 16) == ALIGN
     assert call(M=0) == 0 and call(B=0) == 0

@@ -129,7 +129,8 @@ def check(Y, W, ws, X, xs):
 @pytest.mark.parametrize("M,K,B,yt", [
     (1, 16, 1, "f32"), (128, 128, 128, "f32"), (5, 48, 3, "bf16"), (300, 144, 130, "f32"),
     (200, 4096, 100, "f32"), (1000, 2064, 67, "f16"), (129, 4096, 128, "bf16"), (2000, 512, 65, "f32"),
-    (70, 11008, 7, "f32"), (33, 1040, 16, "f32"), (64, 2048, 17, "f32"),
+    (70, 11008, 7, "f32"), (33, 1040, 16, "f32"), (64, 2048, 17, "f32"), (6200, 4096, 16, "bf16"),
+    (700, 2048, 600, "f32"), (12000, 256, 300, "bf16"), (2571, 272, 1025, "f32"), (2572, 272, 1025, "f32"),
     (4096, 4096, 1, "bf16"), (1000, 2064, 9, "f16"), (129, 4096, 33, "f32"), (2000, 512, 64, "f32"),
     (11000, 256, 37, "f16"), (257, 8192, 65, "bf16"), (4096, 1024, 500, "bf16"),
     (520, 400, 4000, "f32"), (6001, 384, 1300, "f16"), (9000, 128, 2500, "f32"), (4095, 640, 2049, "bf16"),
