@@ -141,6 +141,8 @@ struct Plan {
   // in dynamic shared memory
   Seg* seg[2];                         // [pairs] of each phase
   short* order;                        // [pairs] slot -> pair
+  float* weight;                       // [pairs] 0 where the id names nothing
+  int* id;                             // [pairs, rounded up to 4] the expert, or kNobody
 };
 
 extern __shared__ __align__(1024) uint8_t msm[];
@@ -178,79 +180,85 @@ __device__ __forceinline__ void load8(const void* base, int64_t i, int type, flo
   }
 }
 
+constexpr int kNobody = kMaxE;  // sorts behind every expert
+
 // Pairs sorted by expert (stable), the segments of both phases, and the tokens'
 // largest |x|.  ids outside [0, E) are left out.  A pair's slot is the number of
-// pairs that go before it, counted by one or more lanes of its own.
+// smaller keys (expert, pair), counted by one or more lanes of its own.
 __device__ void make_plan(Plan& pl, const MoeArgs& a) {
   const int P = a.T * a.k, P4 = (P + 3) & ~3;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int* ids = reinterpret_cast<int*>(msm);  // in the rings' place
-  short* rank = reinterpret_cast<short*>(ids + P4);  // by slot: place among its expert's,
-  short* count = rank + P4;                          // how many these are,
-  short* expert = count + P4;                        // and the expert
+  int* key = reinterpret_cast<int*>(msm);  // in the rings' place, until the first copies
+  short* expert = reinterpret_cast<short*>(key + P4);  // by slot
   for (int p = threadIdx.x; p < P4; p += kThreads) {
     const int id = p < P ? __ldcg(a.ids + p) : -1;
+    const float w = p < P ? __ldcg(a.weights + p) : 0.f;
+    const bool ok = id >= 0 && id < a.E;
     if (blockIdx.x == 0 && (id < -1 || id >= a.E)) report(a.dev_status, GQ_DEV_RANGE);
-    ids[p] = id >= 0 && id < a.E ? id : 0x7FFFFFFF;
+    pl.id[p] = ok ? id : kNobody;
+    if (p < P) pl.weight[p] = w;
+    key[p] = (ok ? id : kNobody) * kMaxPairs + p;
   }
-  const int share = max(1, kWarps / a.T), vecs = a.H / 8;  // warps for each token
-  for (int i = warp; i < a.T * share; i += kWarps) {
-    const int t = i / share;
-    unsigned m = 0;
-#pragma unroll 4
-    for (int r = (i - t * share) * 32 + lane; r < vecs; r += 32 * share) {
-      float v[8];
-      load8(a.x, static_cast<int64_t>(t) * a.H + 8 * r, a.xtype, v);
+  // x, 32 pieces of 8 values of a token to a warp at a time, four of these on their way
+  const int vecs = a.H / 8, rows = (vecs + 31) / 32, chunks = a.T * rows;
+  for (int c0 = warp; c0 < chunks; c0 += 4 * kWarps) {
+    unsigned m[4];
+    int t[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(v[q]) & 0x7FFFFFFFu);
+    for (int u = 0; u < 4; ++u) {
+      const int c = c0 + u * kWarps;
+      t[u] = c / rows;
+      const int r = (c - t[u] * rows) * 32 + lane;
+      float v[8] = {};
+      if (c < chunks && r < vecs) load8(a.x, static_cast<int64_t>(t[u]) * a.H + 8 * r, a.xtype, v);
+      m[u] = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m[u] = max(m[u], __float_as_uint(v[q]) & 0x7FFFFFFFu);
     }
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if (lane == 0) atomicMax(&pl.xmax[t], m);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const unsigned top = __reduce_max_sync(0xFFFFFFFFu, m[u]);
+      if (lane == 0 && top) atomicMax(&pl.xmax[t[u]], top);
+    }
   }
   __syncthreads();
   int share_log = 0;  // 2^share_log lanes for each pair
   while (share_log < 5 && (P << (share_log + 1)) <= kThreads) ++share_log;
   const int lanes = 1 << share_log, sub = lane & (lanes - 1);
-  int slots = 0;
+  int slots = 0;  // pairs that name an expert
   for (int p0 = 0; p0 < P; p0 += kThreads >> share_log) {
     const int p = p0 + (threadIdx.x >> share_log);
-    const int id = p < P ? ids[p] : 0x7FFFFFFF;
-    int less = 0, same = 0, before = 0;
+    const int mine = p < P ? key[p] : 0x7FFFFFFF;
+    int less = 0;
     for (int q = 4 * sub; q < P4; q += 4 * lanes) {
-      const int4 v = *reinterpret_cast<const int4*>(ids + q);
-      less += (v.x < id) + (v.y < id) + (v.z < id) + (v.w < id);
-      const int eq = (v.x == id) | (v.y == id) << 1 | (v.z == id) << 2 | (v.w == id) << 3;
-      same += __popc(eq);
-      before += __popc(eq & ((1 << min(max(p - q, 0), 4)) - 1));
+      const int4 v = *reinterpret_cast<const int4*>(key + q);
+      less += (v.x < mine) + (v.y < mine) + (v.z < mine) + (v.w < mine);
     }
-    for (int o = lanes >> 1; o > 0; o >>= 1) {
-      less += __shfl_xor_sync(0xFFFFFFFFu, less, o);
-      same += __shfl_xor_sync(0xFFFFFFFFu, same, o);
-      before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
-    }
-    const bool ok = sub == 0 && id != 0x7FFFFFFF;
+    for (int o = lanes >> 1; o > 0; o >>= 1) less += __shfl_xor_sync(0xFFFFFFFFu, less, o);
+    const bool ok = sub == 0 && mine < kNobody * kMaxPairs;
     if (ok) {
-      const int slot = less + before;
-      pl.order[slot] = static_cast<short>(p);
-      rank[slot] = static_cast<short>(before);
-      count[slot] = static_cast<short>(same);
-      expert[slot] = static_cast<short>(id);
+      pl.order[less] = static_cast<short>(p);
+      expert[less] = static_cast<short>(pl.id[p]);
     }
     slots += __syncthreads_count(ok);
   }
-  if (warp < 2) {  // a segment begins at every cap-th pair of an expert
-    const int cap = a.ph[warp].cap;  // a power of two
+  if (warp < 2) {  // a segment begins with an expert and after every cap of its pairs
+    const int cap = a.ph[warp].cap;
     Seg* seg = pl.seg[warp];
-    int n = 0;
+    int n = 0, first = 0;  // segments; the current expert's first slot
     for (int s0 = 0; s0 < slots; s0 += 32) {
       const int s = s0 + lane;
-      const bool begins = s < slots && (rank[s] & (cap - 1)) == 0;
+      const bool head = s < slots && (s == 0 || expert[s] != expert[s - 1]);
+      const unsigned heads = __ballot_sync(0xFFFFFFFFu, head), upto = heads & (0xFFFFFFFFu >> (31 - lane));
+      const int run = upto ? s0 + 31 - __clz(upto) : first;
+      const bool begins = s < slots && ((s - run) & (cap - 1)) == 0;
       const unsigned b = __ballot_sync(0xFFFFFFFFu, begins);
-      if (begins)
-        seg[n + __popc(b & ((1u << lane) - 1u))] =
-            Seg{expert[s], static_cast<short>(s), min(cap, count[s] - rank[s])};
+      if (begins) seg[n + __popc(b & ((1u << lane) - 1u))] = Seg{expert[s], static_cast<short>(s), 0};
       n += __popc(b);
+      if (heads) first = s0 + 31 - __clz(heads);
     }
+    __syncwarp();
+    for (int i = lane; i < n; i += 32) seg[i].n = (i + 1 < n ? seg[i + 1].slot0 : slots) - seg[i].slot0;
     if (lane == 0) pl.nseg[warp] = n;
   }
   __syncthreads();
@@ -288,7 +296,7 @@ __device__ __forceinline__ void load_cols(const MoeArgs& a, const Phase& ph, Pla
   if (c < sg.n) {
     top = GATE_UP ? pl.xmax[row] : __ldcg(pl.hmax_now + row);
     if (single) {
-      mul = __ldcg(a.weights + pl.order[row]);
+      mul = pl.weight[pl.order[row]];
       top = __float_as_uint(fabsf(__uint_as_float(top) * mul));
       atomicMax(&pl.common, top);
     }
@@ -850,7 +858,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     const int pairs = a.T * a.k;
     pl.seg[0] = reinterpret_cast<Seg*>(msm + a.plan_off);
     pl.seg[1] = pl.seg[0] + pairs;
-    pl.order = reinterpret_cast<short*>(pl.seg[1] + pairs);
+    pl.id = reinterpret_cast<int*>(pl.seg[1] + pairs);
+    pl.weight = reinterpret_cast<float*>(pl.id + ((pairs + 3) & ~3));
+    pl.order = reinterpret_cast<short*>(pl.weight + pairs);
   }
   if (threadIdx.x < kMaxT) pl.xmax[threadIdx.x] = 0u;
   if (threadIdx.x == 0) pl.common = 0u;
@@ -892,10 +902,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   for (int i = i0; i < n; i += static_cast<int>(gridDim.x) * kThreads) {
     const int t = i / a.H, c = i - t * a.H;
     float v = 0.f;
+#pragma unroll 4
     for (int j = 0; j < a.k; ++j) {
-      const int id = __ldcg(a.ids + t * a.k + j);
-      if (id >= 0 && id < a.E)
-        v = fmaf(__ldcg(a.weights + t * a.k + j), __ldcg(a.out + static_cast<int64_t>(t * a.k + j) * a.H + c), v);
+      const int p = t * a.k + j;
+      if (pl.id[p] != kNobody) v = fmaf(pl.weight[p], __ldcg(a.out + static_cast<int64_t>(p) * a.H + c), v);
     }
     store_elem(a.y, i, v, a.ytype);
   }
@@ -930,7 +940,7 @@ static_assert(sizeof(Plan) <= 5120, "the static part");
 constexpr size_t kDynSmem = kSmemBudget - 5120;
 size_t shape_smem(MoeArgs& a) {
   const int pairs = a.T * a.k;
-  const size_t plan = (static_cast<size_t>(pairs) * (2 * sizeof(Seg) + 2) + 15) & ~size_t(15);
+  const size_t plan = (static_cast<size_t>(pairs) * (2 * sizeof(Seg) + 2 + 8) + 12 + 15) & ~size_t(15);
   const size_t left = kDynSmem - kRingBytes - plan;
   size_t tab = 0, b = 0;
   // one token: a column (or two) for each slot, if all of them fit beside the parts
