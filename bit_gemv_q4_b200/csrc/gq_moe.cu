@@ -122,7 +122,7 @@ struct Seg {
 
 struct Col {
   int row;           // of x, or of h
-  float scale, mul;  // the power of two, and a single token's slot weight
+  float mul;         // a single token's slot weight
   int dst, pitch;    // of its B fragments: shared offset, columns
 };
 
@@ -130,11 +130,11 @@ struct Plan {
   int nseg[2];
   int go;                              // the grid barrier was passed
   unsigned* hmax_now;                  // the set of this call
-  unsigned xmax[kMaxT];                // largest |x| of a token as bits
   unsigned common;                     // a single token's largest |weight * h|
   // of a string's segments
   int ncols;                           // tokens of all segments
   Col col[kMaxSegs * kMaxCols];
+  unsigned top[kMaxSegs * kMaxCols];   // their largest magnitude as bits
   int boff[kMaxSegs];                  // their B fragments
   float inv[kMaxSegs][kMaxCols];       // 1 / scale of their tokens
   unsigned hmax[kMaxSegs][kMaxCols];   // largest |h|
@@ -158,32 +158,39 @@ __device__ __forceinline__ void copies_wait() {  // all but the newest N groups 
 }
 
 // ------------------------------------------------------------------- plan
-// Eight consecutive values of an element type as floats.
-__device__ __forceinline__ void load8(const void* base, int64_t i, int type, float v[8]) {
+// Eight consecutive values of an element type, as they are stored and as floats.
+struct Raw {
+  uint4 a, b;
+};
+__device__ __forceinline__ Raw read8(const void* base, int64_t i, int type) {
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * (type == GQ_F32 ? 4 : 2));
+  Raw r;
+  r.a = __ldcg(p);
+  r.b = type == GQ_F32 ? __ldcg(p + 1) : uint4{};
+  return r;
+}
+__device__ __forceinline__ void values(const Raw& r, int type, float v[8]) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
   if (type == GQ_F32) {
-    const float4 a = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
-    const float4 b = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i + 4));
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (type == GQ_F16) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[q]));
-        v[2 * q] = f.x, v[2 * q + 1] = f.y;
-      } else {
-        v[2 * q] = __uint_as_float(w[q] << 16);
-        v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
-      }
+    for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(w[q]);
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (type == GQ_F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[q]));
+      v[2 * q] = f.x, v[2 * q + 1] = f.y;
+    } else {
+      v[2 * q] = __uint_as_float(w[q] << 16);
+      v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
     }
   }
 }
 
 constexpr int kNobody = kMaxE;  // sorts behind every expert
 
-// Pairs sorted by expert (stable), the segments of both phases, and the tokens'
-// largest |x|.  ids outside [0, E) are left out.  A pair's slot is the number of
+// Pairs sorted by expert (stable), and the segments of both phases.  ids outside [0, E) are left out.  A pair's slot is the number of
 // smaller keys (expert, pair), counted by one or more lanes of its own.
 __device__ void make_plan(Plan& pl, const MoeArgs& a) {
   const int P = a.T * a.k, P4 = (P + 3) & ~3;
@@ -198,28 +205,6 @@ __device__ void make_plan(Plan& pl, const MoeArgs& a) {
     pl.id[p] = ok ? id : kNobody;
     if (p < P) pl.weight[p] = w;
     key[p] = (ok ? id : kNobody) * kMaxPairs + p;
-  }
-  // x, 32 pieces of 8 values of a token to a warp at a time, four of these on their way
-  const int vecs = a.H / 8, rows = (vecs + 31) / 32, chunks = a.T * rows;
-  for (int c0 = warp; c0 < chunks; c0 += 4 * kWarps) {
-    unsigned m[4];
-    int t[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int c = c0 + u * kWarps;
-      t[u] = c / rows;
-      const int r = (c - t[u] * rows) * 32 + lane;
-      float v[8] = {};
-      if (c < chunks && r < vecs) load8(a.x, static_cast<int64_t>(t[u]) * a.H + 8 * r, a.xtype, v);
-      m[u] = 0;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) m[u] = max(m[u], __float_as_uint(v[q]) & 0x7FFFFFFFu);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const unsigned top = __reduce_max_sync(0xFFFFFFFFu, m[u]);
-      if (lane == 0 && top) atomicMax(&pl.xmax[t[u]], top);
-    }
   }
   __syncthreads();
   int share_log = 0;  // 2^share_log lanes for each pair
@@ -281,94 +266,106 @@ __device__ __forceinline__ int col_pitch(int ncol) {
 
 __host__ __device__ __forceinline__ int padded(int K) { return (K + 255) & ~255; }
 
-// The tokens of a string's segments (all threads call it).  A single token's h
-// is multiplied by its slot's weight and scaled by the largest product of all
-// slots.
+// B fragments of the tokens of a string's segments (all threads call it).
+// Column c of block b and lane group t: 16 bytes at ((b * pitch + c) * 4 + t) * 16
+// of its segment, the values 4t, 4t+2, 4t+1, 4t+3 of the block and the same at
+// +16; zeros up to whole stages.  fp16 x goes in as it is; otherwise a token's
+// largest magnitude sets its scale: of h it is known, of x it is taken here, from
+// the values of this CTA's tokens as they pass (all SMs read the same lines, at
+// 16 bytes a nanosecond each, so reading all tokens for it cost 5 us at 32).  A
+// single token's h is multiplied by its slot's weight and scaled by the largest
+// product of all slots.
 template <bool GATE_UP>
-__device__ __forceinline__ void load_cols(const MoeArgs& a, const Phase& ph, Plan& pl, int seg0, int segs) {
+__device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& pl, int seg0, int segs) {
+  constexpr int kKeep = 4;  // pieces of 8 values that a thread keeps between the two passes
   const bool single = !GATE_UP && a.single;
+  const int type = GATE_UP ? a.xtype : GQ_F32;
+  const bool find = GATE_UP && type != GQ_F16;
   const int i = threadIdx.x / kMaxCols, c = threadIdx.x % kMaxCols;
-  float mul = 1.0f;
-  unsigned top = 0;
+  int before = 0;  // columns of the segments before this thread's
   Seg sg{0, 0, 0};
   if (i < segs) sg = pl.seg[!GATE_UP][seg0 + i];
-  const int row = c < sg.n ? (GATE_UP ? pl.order[sg.slot0 + c] / a.k : sg.slot0 + c) : 0;
   if (c < sg.n) {
-    top = GATE_UP ? pl.xmax[row] : __ldcg(pl.hmax_now + row);
+    const int row = GATE_UP ? pl.order[sg.slot0 + c] / a.k : sg.slot0 + c;
+    unsigned top = find ? 0u : GATE_UP ? 0x46800000u : __ldcg(pl.hmax_now + row);  // (2^14: a scale of 1)
+    float mul = 1.0f;
     if (single) {
       mul = pl.weight[pl.order[row]];
       top = __float_as_uint(fabsf(__uint_as_float(top) * mul));
       atomicMax(&pl.common, top);
     }
-  }
-  if (single) {
-    __syncthreads();
-    top = pl.common;
-  }
-  if (c < sg.n) {
-    int before = 0, off = a.b_off;  // columns and bytes of the segments before
+    int off = a.b_off;
     for (int j = 0; j < i; ++j) {
       const int n = pl.seg[!GATE_UP][seg0 + j].n;
       before += n;
       off += col_pitch(ph.two ? 2 * n : n) * padded(ph.K) * 2;
     }
-    const float s = scale_of(top);
-    pl.col[before + c] = Col{row, s, mul, off + (ph.two ? 2 * c : c) * 64, col_pitch(ph.two ? 2 * sg.n : sg.n)};
-    pl.inv[i][c] = 1.0f / s;  // a power of two: exact
+    pl.col[before + c] = Col{row, mul, off + (ph.two ? 2 * c : c) * 64, col_pitch(ph.two ? 2 * sg.n : sg.n)};
+    pl.top[before + c] = top;
     pl.hmax[i][c] = 0u;
     if (c == 0) pl.boff[i] = off;
     if (i == segs - 1 && c == 0) pl.ncols = before + sg.n;
   }
   __syncthreads();
-}
-
-// B fragments of the string's tokens.  Column c of block b and lane group t: 16
-// bytes at ((b * pitch + c) * 4 + t) * 16 of its segment, the values 4t, 4t+2,
-// 4t+1, 4t+3 of the block and the same at +16; zeros up to whole stages.
-template <bool GATE_UP>
-__device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, const Plan& pl) {
-  constexpr int kBatch = 2;  // pieces of 8 values read at once
-  const int vecs = padded(ph.K) / 8, real = ph.K / 8;
-  const int type = GATE_UP ? a.xtype : GQ_F32;
+  const int vecs = padded(ph.K) / 8, real = ph.K / 8, nvec = pl.ncols * vecs;
   const void* src = GATE_UP ? a.x : a.h;
-  const int nvec = pl.ncols * vecs;
-  for (int i0 = threadIdx.x; i0 < nvec; i0 += kBatch * kThreads) {
-    float v[kBatch][8];
-    int cs[kBatch], rs[kBatch];
+  auto fetch = [&](int i) -> Raw {  // piece i of the columns
+    const int cc = ph.by_vecs(i), r = i - cc * vecs;
+    if (i >= nvec || r >= real) return Raw{};
+    return read8(src, static_cast<int64_t>(pl.col[cc].row) * ph.K + 8 * r, type);
+  };
+  Raw kept[kKeep];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + u * kThreads;
-      cs[u] = i < nvec ? ph.by_vecs(i) : -1;
-      rs[u] = i - cs[u] * vecs;
+  for (int u = 0; u < kKeep; ++u) kept[u] = fetch(threadIdx.x + u * kThreads);
+  if (find) {
+    auto note = [&](const Raw& r, int i) {
+      float v[8];
+      values(r, type, v);
+      unsigned m = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
-      if (cs[u] >= 0 && rs[u] < real)
-        load8(src, static_cast<int64_t>(pl.col[cs[u]].row) * ph.K + 8 * rs[u], type, v[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (cs[u] < 0) break;
-      const Col col = pl.col[cs[u]];
-      const int b = rs[u] >> 2, q = rs[u] & 3;
-      for (int part = 0; part <= ph.two; ++part) {
-        __half hv[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float f = part ? v[u][j] : v[u][j] * col.mul * col.scale;  // the second pass holds remainders
-          hv[j] = __float2half_rn(f);
-          v[u][j] = f - __half2float(hv[j]);
-        }
-        uint8_t* d = msm + col.dst + (b * col.pitch + part) * 64 + 2 * (q & 1) * 16 + (q >> 1) * 8;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const __half2 lo = __halves2half2(hv[4 * w], hv[4 * w + 2]);
-          const __half2 hi = __halves2half2(hv[4 * w + 1], hv[4 * w + 3]);
-          *reinterpret_cast<uint2*>(d + 16 * w) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                                             *reinterpret_cast<const uint32_t*>(&hi));
-        }
+      for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(v[q]) & 0x7FFFFFFFu);
+      // (whole warps are of one column but where a column ends inside a warp)
+      const int cc = i < nvec ? ph.by_vecs(i) : -1;
+      if (__match_any_sync(0xFFFFFFFFu, cc) == 0xFFFFFFFFu) {
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if ((threadIdx.x & 31) == 0 && cc >= 0) atomicMax(&pl.top[cc], m);
+      } else if (cc >= 0) {
+        atomicMax(&pl.top[cc], m);
       }
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u) note(kept[u], threadIdx.x + u * kThreads);
+    for (int i0 = kKeep * kThreads; i0 < nvec; i0 += kThreads) note(fetch(i0 + threadIdx.x), i0 + threadIdx.x);
+    __syncthreads();
   }
+  if (c < sg.n)  // scale_of() is a power of two: the reciprocal is exact
+    pl.inv[i][c] = 1.0f / scale_of(single ? pl.common : pl.top[before + c]);
+  auto put8 = [&](const Raw& raw, int i) {
+    if (i >= nvec) return;
+    const int cc = ph.by_vecs(i), r = i - cc * vecs;
+    const Col col = pl.col[cc];
+    const float f = scale_of(single ? pl.common : pl.top[cc]) * col.mul;
+    float v[8];
+    values(raw, type, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= f;
+    uint8_t* d = msm + col.dst + (r >> 2) * col.pitch * 64 + (r & 1) * 32 + (r & 2) * 4;
+    auto store = [&](uint8_t* d) {  // and leaves what fp16 leaves out
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const __half2 lo = __floats2half2_rn(v[4 * w], v[4 * w + 2]), hi = __floats2half2_rn(v[4 * w + 1], v[4 * w + 3]);
+        *reinterpret_cast<uint2*>(d + 16 * w) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                           *reinterpret_cast<const uint32_t*>(&hi));
+        const float2 l = __half22float2(lo), h = __half22float2(hi);
+        v[4 * w] -= l.x, v[4 * w + 2] -= l.y, v[4 * w + 1] -= h.x, v[4 * w + 3] -= h.y;
+      }
+    };
+    store(d);
+    if (ph.two) store(d + 64);
+  };
+#pragma unroll
+  for (int u = 0; u < kKeep; ++u) put8(kept[u], threadIdx.x + u * kThreads);
+  for (int i0 = kKeep * kThreads; i0 < nvec; i0 += kThreads) put8(fetch(i0 + threadIdx.x), i0 + threadIdx.x);
 }
 
 // ------------------------------------------------------------------ stages
@@ -766,8 +763,7 @@ __device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, 
   const int all = wk.item.d;
   while (wk.more) {
     const String st = wk.st;
-    load_cols<GATE_UP>(a, ph, pl, st.seg0, st.segs);
-    load_b<GATE_UP>(a, ph, pl);
+    load_b<GATE_UP>(a, ph, pl, st.seg0, st.segs);
     // the rest of the ring (the first copies went ahead of B: a full ring of them would hold it up)
     for (int d = 1; d < kDepth; ++d)
       wk.feed.step(ph, pl, ph.stages, wk.ring() + d * kStageBytes, threadIdx.x & 31);
@@ -862,7 +858,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     pl.weight = reinterpret_cast<float*>(pl.id + ((pairs + 3) & ~3));
     pl.order = reinterpret_cast<short*>(pl.weight + pairs);
   }
-  if (threadIdx.x < kMaxT) pl.xmax[threadIdx.x] = 0u;
   if (threadIdx.x == 0) pl.common = 0u;
   __syncthreads();
   pdl_wait();  // ids and x are final
