@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 
 import torch
@@ -513,26 +514,32 @@ def _auto_workspace(name: str, need: int, device: torch.device, stream: int):
     """(tensor, address, bytes) of the call's workspace on `stream`."""
     key = (name, device.index, stream)
     ws = _call_ws.get(key)
-    if ws is not None and ws[2] >= need and not torch.cuda.is_current_stream_capturing():
+    if (ws is not None and ws[2] >= need and stream == torch._C._cuda_getCurrentRawStream(device.index)
+            and not torch.cuda.is_current_stream_capturing()):
         return ws
     # cleared on the call's own stream; a captured call keeps a workspace of its own, which its
     # graph clears
     with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-        t = torch.zeros(need, dtype=torch.uint8, device=device)
-        ws = (t, t.data_ptr() or None, need)
-        if not torch.cuda.is_current_stream_capturing():
-            _call_ws[key] = ws
+        capturing = torch.cuda.is_current_stream_capturing()
+        if ws is None or ws[2] < need or capturing:
+            t = torch.zeros(need, dtype=torch.uint8, device=device)
+            ws = (t, t.data_ptr() or None, need)
+            if not capturing:
+                _call_ws[key] = ws
     return ws
 
 
 def _on_device(call):
     """Run the call with its first tensor's device as the current one."""
+    name = next(iter(inspect.signature(call).parameters))
+
     @functools.wraps(call)
-    def wrapped(first, *args, **kw):
-        if first.is_cuda and first.get_device() != torch.cuda.current_device():
+    def wrapped(*args, **kw):
+        first = args[0] if args else kw.get(name)
+        if isinstance(first, torch.Tensor) and first.is_cuda and first.get_device() != torch.cuda.current_device():
             with torch.cuda.device(first.device):
-                return call(first, *args, **kw)
-        return call(first, *args, **kw)
+                return call(*args, **kw)
+        return call(*args, **kw)
     return wrapped
 
 
@@ -550,15 +557,17 @@ def _raw_stream(stream, device: torch.device) -> int:
 
 
 def _workspace(name: str, workspace, need: int, device: torch.device, stream: int):
+    """(address, bytes, what keeps the memory until the launch)."""
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a uint8 CUDA tensor")
         if need == 0:
-            return None, 0
-        return _auto_workspace(name, need, device, stream)[1:]
+            return None, 0, None
+        keep, ptr, size = _auto_workspace(name, need, device, stream)
+        return ptr, size, keep
     if workspace is None:
-        return None, 0
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+        return None, 0, None
+    return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
 
 
 def gq_moe_route_workspace_bytes(T: int, E: int) -> int:
@@ -595,7 +604,7 @@ def gq_moe_route(x: torch.Tensor, Wr: torch.Tensor, k: int, bias: torch.Tensor |
         weights = x.new_empty((T, k), dtype=torch.float32)
     elif weights.dtype != torch.float32 or weights.numel() != T * k:
         raise ValueError("weights holds T * k fp32 values")
-    ws, ws_bytes = _workspace("route", workspace, _size("gq_moe_route_workspace_bytes", T, E), x.device, s)
+    ws, ws_bytes, keep = _workspace("route", workspace, _size("gq_moe_route_workspace_bytes", T, E), x.device, s)
     _check(lib.gq_moe_route(_ptr(x), _DTYPE_CODE[x.dtype], T, H, _ptr(Wr), _DTYPE_CODE[Wr.dtype], E,
                             _ptr(bias), k, scale, _ptr(ids), _ptr(weights), ws, ws_bytes, flags,
                             _ptr(dev_status), s), "gq_moe_route")
@@ -624,7 +633,7 @@ def _moe(name: str, fmt: int, gate, up, down, E: int, I: int, x: torch.Tensor, i
         out = x.new_empty((T, H), dtype=y_dtype)
     elif out.dtype not in _DTYPE_CODE or out.numel() != T * H:
         raise ValueError("out holds T * H values")
-    ws, ws_bytes = _workspace(name, workspace, _size("gq_moe_workspace_bytes", fmt, H, I, T, k), x.device, s)
+    ws, ws_bytes, keep = _workspace(name, workspace, _size("gq_moe_workspace_bytes", fmt, H, I, T, k), x.device, s)
     _check(getattr(lib, name)(_ptr(gate), _ptr(up), _ptr(down), E, H, I, _ptr(x), _DTYPE_CODE[x.dtype],
                               T, _ptr(ids), _ptr(weights), k, _ptr(out), _DTYPE_CODE[out.dtype], ws,
                               ws_bytes, flags, _ptr(dev_status), s), name)
@@ -704,6 +713,8 @@ def gq_quantize_fp8(x: torch.Tensor, rows: int, out: torch.Tensor | None = None,
 def gq_dequantize_fp8(q: torch.Tensor, scales: torch.Tensor, rows: int, dtype=torch.float32,
                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """scale * code of a matrix in blocks of rows x 128, in `dtype`."""
+    if rows not in (1, 128):
+        raise ValueError("rows is 1 or 128")
     R, K = _fp8_pair(q, scales, rows, "q")
     if dtype not in _DTYPE_CODE:
         raise TypeError("outputs must be float32, float16 or bfloat16")
@@ -738,7 +749,8 @@ def gq_gemm_fp8(W: torch.Tensor, w_scales: torch.Tensor, X: torch.Tensor, x_scal
         out = X.new_empty((B, M), dtype=y_dtype)
     elif out.dtype not in _DTYPE_CODE or out.numel() != B * M:
         raise ValueError("out holds B * M values")
-    ws, ws_bytes = _workspace("gq_gemm_fp8", workspace, _size("gq_gemm_fp8_workspace_bytes", M, K, B), X.device, s)
+    ws, ws_bytes, keep = _workspace("gq_gemm_fp8", workspace, _size("gq_gemm_fp8_workspace_bytes", M, K, B),
+                                    X.device, s)
     _check(lib.gq_gemm_fp8(_ptr(W), _ptr(w_scales), M, K, _ptr(X), _ptr(x_scales), B, _ptr(out),
                            _DTYPE_CODE[out.dtype], ws, ws_bytes, flags, _ptr(dev_status), s), "gq_gemm_fp8")
     return out

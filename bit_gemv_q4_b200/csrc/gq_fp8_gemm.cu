@@ -76,7 +76,7 @@ struct Args {
   long long budget;
   int64_t M;
   int B, kblocks, ytype, xrows;  // xrows: rows of an X box
-  int ybytes;                    // alignment of Y's rows, 16 or 32 bytes, or 0
+  int tma_y;                     // Y's rows are whole 16-byte pieces, so that TMA can store them
   Split sp;
   float* parts;  // [pieces][rows][BN] of cut tiles
 };
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kCols / 4; ++i)
             __stcg(d + i, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
         }
-      } else if (a.ybytes) {
+      } else if (a.tma_y) {
         if (any) store_tile<kCols>(&ymap, staging + warp * kStoreBytes, acc, static_cast<int>(m0) + cols0,
                                    row0 + 32 * quarter, a.M, a.ytype);
       } else if (row_ok) {
@@ -699,14 +699,14 @@ GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, in
   a.ytype = y_dtype;
   a.xrows = static_cast<int>(B < kBM ? (B + 7) / 8 * 8 : kBM);
   const int esize = dtype_size(y_dtype);
-  a.ybytes = M * esize % 16 == 0 ? 16 : 0;  // rows that TMA can store
+  a.tma_y = M * esize % 16 == 0;
   a.sp = c.sp;
   a.parts = static_cast<float*>(workspace);
   CUtensorMap xmap, wmap, ymap = {};
   gq_status st = encode(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, X, B, K, kBK, a.xrows, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st == GQ_OK) st = encode(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W, M, K, kBK, c.pair ? c.bn / 2 : c.bn,
                                  CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st == GQ_OK && a.ybytes)
+  if (st == GQ_OK && a.tma_y)
     st = encode(&ymap,
                 y_dtype == GQ_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                 : y_dtype == GQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16

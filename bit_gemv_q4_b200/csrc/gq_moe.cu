@@ -13,10 +13,10 @@
 // down (one fp32 row of outputs for each token and slot), and the weighted sum
 // over a token's slots.  For a single token whose slots' h all fit in shared
 // memory, down's rows run over all slots, with the weights folded into h, and y
-// is stored at once: no third phase.  The first copies of down's weights are under way while
-// a CTA waits for the others.  (As three launches joined by programmatic
-// dependent launch the phases cost 8 us between the weight streams of the first
-// two: a CTA's shared memory keeps the next launch out of its SM.)
+// is stored at once: no third phase.  The first copies of down's weights are
+// under way while a CTA waits for the others.  (As three launches joined by
+// programmatic dependent launch the phases cost 8 us between the weight streams
+// of the first two: a CTA's shared memory keeps the next launch out of its SM.)
 //
 // Plan.  Every CTA reads the ids and builds the same plan in shared memory:
 // the (token, slot) pairs sorted by expert (stable), and segments of an expert
@@ -190,8 +190,9 @@ __device__ __forceinline__ void values(const Raw& r, int type, float v[8]) {
 
 constexpr int kNobody = kMaxE;  // sorts behind every expert
 
-// Pairs sorted by expert (stable), and the segments of both phases.  ids outside [0, E) are left out.  A pair's slot is the number of
-// smaller keys (expert, pair), counted by one or more lanes of its own.
+// Pairs sorted by expert (stable), and the segments of both phases; ids outside
+// [0, E) are left out.  A pair's slot is the number of smaller keys (expert,
+// pair), counted by one or more lanes of its own.
 __device__ void make_plan(Plan& pl, const MoeArgs& a) {
   const int P = a.T * a.k, P4 = (P + 3) & ~3;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -271,8 +272,8 @@ __host__ __device__ __forceinline__ int padded(int K) { return (K + 255) & ~255;
 // of its segment, the values 4t, 4t+2, 4t+1, 4t+3 of the block and the same at
 // +16; zeros up to whole stages.  fp16 x goes in as it is; otherwise a token's
 // largest magnitude sets its scale: of h it is known, of x it is taken here, from
-// the values of this CTA's tokens as they pass (all SMs read the same lines, at
-// 16 bytes a nanosecond each, so reading all tokens for it cost 5 us at 32).  A
+// the values of this CTA's tokens as they pass (reading all tokens for it in every
+// CTA cost 5 us at 32 tokens).  A
 // single token's h is multiplied by its slot's weight and scaled by the largest
 // product of all slots.
 template <bool GATE_UP>
@@ -716,8 +717,9 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
 // item that this warp began and did not end (`cut`: row group g of segment sg,
 // `end` its last stage + 1) takes the later warps' parts in order.
 template <int FMT, bool GATE_UP>
-__device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Plan& pl, const String& st, unsigned tu, bool cut,
-                                           const Seg& sg, int local, int g, unsigned u1, unsigned end) {
+__device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Plan& pl, const String& st,
+                                           unsigned tu, bool cut, const Seg& sg, int local, int g, unsigned u1,
+                                           unsigned end) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();  // the parts are there; nobody reads B any more
   if (cut) {
@@ -881,8 +883,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
           store_elem(a.y, i, 0.f, a.ytype);
       return;
     }
+  }
+  if (!a.single) {  // (arrived at even after a wait that gave up: the count stays a multiple of the grid)
     target = grid_arrive(a);
-    ok = grid_wait(a, pl, target);
+    ok = ok && grid_wait(a, pl, target);
   }
   if (!ok) {
     copies_wait<0>();

@@ -102,6 +102,7 @@ __device__ __forceinline__ void pick(const RouteArgs& a, int64_t t) {
     double v = e < a.E ? __ldcg(s + e) : 0.0;
     bad |= !isfinite(v);
     if (a.bias && e < a.E) v += static_cast<double>(__ldg(a.bias + e));
+    bad |= isnan(v);
     key[i] = e < a.E ? sortable(v + 0.0) : 0;  // (-0 and +0 are equal keys)
   }
   if (__any_sync(0xFFFFFFFFu, bad)) {  // no experts: the token's outputs are zeros

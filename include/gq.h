@@ -385,8 +385,9 @@ GQ_API gq_status gq_gemm_ksb(const void* W, int64_t M, int64_t K,
  *   ids: [T][k] int32; weights: [T][k] fp32.
  * Products and sums of z are fp64, so which experts are taken does not depend
  * on the order of a sum; exponentials and weights are fp32 (sigmoids fp64).
- * A token with a NaN or infinite score gets ids of -1 and weights of 0, and
- * sets GQ_DEV_NONFINITE.
+ * A token with a NaN or infinite score, or with a NaN in the bias, gets ids of
+ * -1 and weights of 0, and sets GQ_DEV_NONFINITE.  (Infinities in the bias keep
+ * an expert in or out.)
  * workspace / ws_bytes: at least gq_moe_route_workspace_bytes(T, E) bytes
  *   (GQ_ERR_WORKSPACE otherwise), 256-byte aligned, all zero before its first
  *   use; a successful call leaves it ready for the next call of any sizes;
@@ -410,13 +411,14 @@ GQ_API gq_status gq_moe_route(const void* x, int x_dtype, int64_t T, int64_t H, 
  *   gate, up: tiled storage of the E experts' I x H matrices one after another,
  *      i.e. of one (E * I) x H matrix (gq_repack_*); down: of E matrices H x I.
  *      H and I are multiples of 64 (Q4_0) or 256 (KSB), at most 16384; E <= 1024.
- *   x: [T][H] of x_dtype; T <= 64, k <= 16; y: [T][H] of y_dtype.
+ *   x: [T][H] of x_dtype; T <= 64, k <= 16; y: [T][H] of y_dtype (of the same
+ *      type, y may be x itself).
  *   ids: [T][k] int32 (as gq_moe_route writes them).  -1 names no expert; any
  *      other value outside [0, E) counts as -1 and sets GQ_DEV_RANGE.  A token
  *      may name an expert more than once.  A token that names none gets zeros.
  *   weights: [T][k] fp32.
- * Only the experts that some token names are read, each once for up to 16
- * tokens (fewer for wide matrices).
+ * Only the experts that some token names are read, each once for up to 8
+ * tokens (4 where a token takes two fp16 terms, fewer for wide matrices).
  * Arithmetic: products of exact codes with activations in fp16 scaled by a
  * power of two for each token (16-bit x exactly, down to 2^-39 of the token's
  * largest; fp32 x, and the activation between the products when y is fp32, as
@@ -428,9 +430,13 @@ GQ_API gq_status gq_moe_route(const void* x, int x_dtype, int64_t T, int64_t H, 
  *   aligned, all zero before its first use; a successful call leaves it ready
  *   for the next call of any sizes; after a call that fails, zero it again.
  *   Calls that may run at the same time need separate workspaces.
- * flags: 0 or GQ_GEMV_PDL (the first launch may be scheduled early; it waits
- *   for the preceding kernel, which may be the router, before it reads ids or
- *   x). */
+ * flags: 0 or GQ_GEMV_PDL (the call may be scheduled early; it waits for the
+ *   preceding kernel, which may be the router, before it reads ids or x).
+ * One cooperative launch with a CTA on every SM of the device: it starts when
+ *   all of them are free of other kernels' shared memory (GQ_ERR_CUDA if the
+ *   process may not use them all).
+ * dev_status: optional, receives GQ_DEV_RANGE, and GQ_DEV_TIMEOUT if a wait at
+ *   the grid's barrier gives up. */
 GQ_API size_t gq_moe_workspace_bytes(int fmt, int64_t H, int64_t I, int64_t T, int64_t k);
 GQ_API gq_status gq_moe_q4_0_tiled(const void* gate, const void* up, const void* down, int64_t E,
                                    int64_t H, int64_t I, const void* x, int x_dtype, int64_t T,

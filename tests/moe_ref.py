@@ -26,10 +26,10 @@ def experts(fmt, E, R, K, seed, std=0.05):
 
 
 def product(W, d, x, dx, K, two_terms):
-    """(W x, its possible error) for x known to dx.  The kernel adds code * x and -8 * sum(x): terms
-    of at most d * (code + 8) * |x| <= (|W| + 16 d) |x|.  A block of 32 is two MMAs of 16 products
-    on an accumulator input, the blocks' sums are added in fp32: at most K / 32 + 40 additions, each
-    cut to 24 bits (a whole step, 2^-23, where the tensor core truncates).  Two fp16 terms hold 22
+    """(W x, its possible error) for x known to dx.  The kernel adds (code - 8) * x: terms of |W| |x|
+    in sum (16 d |x| more are let through, for a form that adds code * x and -8 * x).  A block of 32
+    is two MMAs of 16 products on an accumulator input, the blocks' sums are added in fp32: at most
+    K / 32 + 40 additions, each cut to 24 bits (a whole step, 2^-23, where the tensor core truncates).  Two fp16 terms hold 22
     bits of x: 2^-22 of it, and 2^-38 of the largest |x| where the remainder is subnormal."""
     ax = np.abs(x)
     mag = (np.abs(W) + 16 * d) @ ax
