@@ -278,7 +278,6 @@ __host__ __device__ __forceinline__ int padded(int K) { return (K + 255) & ~255;
 // product of all slots.
 template <bool GATE_UP>
 __device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& pl, int seg0, int segs) {
-  constexpr int kKeep = 4;  // pieces of 8 values that a thread keeps between the two passes
   const bool single = !GATE_UP && a.single;
   const int type = GATE_UP ? a.xtype : GQ_F32;
   const bool find = GATE_UP && type != GQ_F16;
@@ -315,9 +314,7 @@ __device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& 
     if (i >= nvec || r >= real) return Raw{};
     return read8(src, static_cast<int64_t>(pl.col[cc].row) * ph.K + 8 * r, type);
   };
-  Raw kept[kKeep];
-#pragma unroll
-  for (int u = 0; u < kKeep; ++u) kept[u] = fetch(threadIdx.x + u * kThreads);
+  const Raw first = fetch(threadIdx.x);  // (keeping more than one between the passes made longer code, and slower)
   if (find) {
     auto note = [&](const Raw& r, int i) {
       float v[8];
@@ -334,9 +331,8 @@ __device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& 
         atomicMax(&pl.top[cc], m);
       }
     };
-#pragma unroll
-    for (int u = 0; u < kKeep; ++u) note(kept[u], threadIdx.x + u * kThreads);
-    for (int i0 = kKeep * kThreads; i0 < nvec; i0 += kThreads) note(fetch(i0 + threadIdx.x), i0 + threadIdx.x);
+    note(first, threadIdx.x);
+    for (int i0 = kThreads; i0 < nvec; i0 += kThreads) note(fetch(i0 + threadIdx.x), i0 + threadIdx.x);
     __syncthreads();
   }
   if (c < sg.n)  // scale_of() is a power of two: the reciprocal is exact
@@ -364,9 +360,8 @@ __device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& 
     store(d);
     if (ph.two) store(d + 64);
   };
-#pragma unroll
-  for (int u = 0; u < kKeep; ++u) put8(kept[u], threadIdx.x + u * kThreads);
-  for (int i0 = kKeep * kThreads; i0 < nvec; i0 += kThreads) put8(fetch(i0 + threadIdx.x), i0 + threadIdx.x);
+  put8(first, threadIdx.x);
+  for (int i0 = kThreads; i0 < nvec; i0 += kThreads) put8(fetch(i0 + threadIdx.x), i0 + threadIdx.x);
 }
 
 // ------------------------------------------------------------------ stages
@@ -518,12 +513,18 @@ struct Feed {
   }
 };
 
-// The parts of items that warps share: two for each warp, of both matrices for
-// gate and up.  Part 0 belongs to an item that an earlier warp began, part 1 to
-// one that this warp began and a later one ends.
-__device__ __forceinline__ float* part_at(const MoeArgs& a, const Phase& ph, int warp, int which) {
-  return reinterpret_cast<float*>(msm + a.tab_off) + (2 * warp + which) * ph.part;
+// The parts of items that warps share, of both matrices for gate and up.  The
+// later warps' parts of an item are in a table, one for each warp; the part of
+// the warp that began it, which adds the others to it, is in the last slot of
+// its own ring, which is empty from the end of its stages until the next
+// string's activations are there.
+__device__ __forceinline__ float* later_part(const MoeArgs& a, const Phase& ph, int warp) {
+  return reinterpret_cast<float*>(msm + a.tab_off) + warp * ph.part;
 }
+__device__ __forceinline__ float* first_part() {
+  return reinterpret_cast<float*>(msm + ((threadIdx.x >> 5) * kDepth + kDepth - 1) * kStageBytes);
+}
+static_assert(kDepth > 1 && 2 * 16 * kMaxCols * sizeof(float) <= kStageBytes, "a part of both matrices");
 template <int CP>
 __device__ __forceinline__ void store_part(float* d, const float acc[4], int lane) {
   const int g8 = lane >> 2, t = lane & 3;
@@ -554,6 +555,41 @@ __device__ __forceinline__ unsigned put(const MoeArgs& a, const Phase& ph, const
   } else {
     __stcg(a.out + static_cast<int64_t>(pl.order[sg.slot0 + c]) * (ph.groups * 16) + row, v);
     return 0u;
+  }
+}
+
+// Row group g of an item, whose sums a warp has: rows g8 and g8 + 8, columns 2t
+// and 2t+1 in each lane (two tokens, or one in two columns); top: the largest
+// |h| of the lane's tokens.
+template <bool GATE_UP>
+__device__ __forceinline__ void finish(const MoeArgs& a, const Phase& ph, const Plan& pl, const Seg& sg, int local,
+                                       int g, const float acc[4], const float gate[4], unsigned top[2]) {
+  const int lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = ph.two ? t : 2 * t + i;
+    if (c < sg.n && !(ph.two && i)) {
+      const float f = pl.inv[local][c];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float v = ph.two ? acc[2 * half] + acc[2 * half + 1] : acc[2 * half + i];
+        const float w = ph.two ? gate[2 * half] + gate[2 * half + 1] : gate[2 * half + i];
+        const unsigned m = put<GATE_UP>(a, ph, pl, sg, c, 16 * g + g8 + 8 * half, (GATE_UP ? w : v) * f, v * f);
+        top[i] = max(top[i], m);
+      }
+    }
+  }
+}
+// The segment's largest |h|, from those of the lanes.
+__device__ __forceinline__ void note_tops(const Phase& ph, Plan& pl, const Seg& sg, int local, const unsigned top[2]) {
+  const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    unsigned m = top[i];
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const int c = ph.two ? t : 2 * t + i;
+    if (lane < 4 && c < sg.n && !(ph.two && i) && m) atomicMax(&pl.hmax[local][c], m);
   }
 }
 
@@ -653,23 +689,9 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
       return;
     }
     if (whole) {
-      // columns 2t and 2t+1, rows g8 and g8 + 8: two tokens, or one in two columns
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = ph.two ? t : 2 * t + i;
-        if (c < sg.n && !(ph.two && i)) {
-          const float f = pl.inv[local][c];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float v = ph.two ? acc[2 * half] + acc[2 * half + 1] : acc[2 * half + i];
-            const float w = ph.two ? gate[2 * half] + gate[2 * half + 1] : gate[2 * half + i];
-            const unsigned m = put<GATE_UP>(a, ph, pl, sg, c, 16 * g + g8 + 8 * half, (GATE_UP ? w : v) * f, v * f);
-            top[i] = max(top[i], m);
-          }
-        }
-      }
+      finish<GATE_UP>(a, ph, pl, sg, local, g, acc, gate, top);
     } else {
-      float* d = part_at(a, ph, warp, 0);
+      float* d = later_part(a, ph, warp);
       if (GATE_UP) store_part<CP>(d, gate, lane);
       store_part<CP>(d + (GATE_UP ? 16 * CP : 0), acc, lane);
     }
@@ -691,7 +713,7 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
     if (++kk == stages) row_end();
   }
   if (k > 0 && k < all && u == wk.u1 && wk.u1 > wk.u0) {  // the run ends inside an item
-    float* d = part_at(a, ph, warp, whole);
+    float* d = whole ? first_part() : later_part(a, ph, warp);
     if (GATE_UP) {
       store_part<CP>(d, k < stages ? acc : gate, lane);
       if (k < stages) {
@@ -701,16 +723,7 @@ __device__ __forceinline__ void stream(const MoeArgs& a, const Phase& ph, Plan& 
     }
     store_part<CP>(d + (GATE_UP ? 16 * CP : 0), acc, lane);
   }
-  if (GATE_UP) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {  // over the lanes of a token
-      unsigned m = top[i];
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const int c = ph.two ? t : 2 * t + i;
-      if (g8 == 0 && c < sg.n && !(ph.two && i) && m) atomicMax(&pl.hmax[local][c], m);
-    }
-  }
+  if (GATE_UP) note_tops(ph, pl, sg, local, top);
 }
 
 // After the last stage of a string (stage `u1` of the string would follow): the
@@ -725,28 +738,35 @@ __device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Pl
   if (cut) {
     const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
     const int row = lane & 15, half = lane >> 4;
-    // gate and up: each half of the warp one matrix; down: every other token
-    for (int c0 = 0; c0 < sg.n; c0 += GATE_UP ? 1 : 2) {
-      const int c = GATE_UP ? c0 : min(c0 + half, sg.n - 1);
-      const float* d = part_at(a, ph, warp, 1) + ((GATE_UP ? half * 16 : 0) + row) * pitch + (ph.two ? 2 * c : c);
-      float v = ph.two ? d[0] + d[1] : d[0];
-      d += ph.part;  // the next warp's part 0
+    unsigned tops = 0;  // lane c: token c's largest
+    // two tokens at a time, a lane for each row
+#pragma unroll 1  // (run through once, so that each instruction has to be fetched: short code is faster)
+    for (int c0 = 0; c0 < sg.n; c0 += 2) {
+      const int c = min(c0 + half, sg.n - 1), at = row * pitch + (ph.two ? 2 * c : c), up = 16 * pitch;
+      const float* d = first_part() + at;
+      float v = ph.two ? d[0] + d[1] : d[0], u = 0.f;
+      if (GATE_UP) u = ph.two ? d[up] + d[up + 1] : d[up];
+      d = later_part(a, ph, warp + 1) + at;
       unsigned begin = u1;
       for (unsigned w = warp + 1; begin < end; ++w) {
         const unsigned next = tu * (w + 1) / kWarps;
-        if (next > begin) v += ph.two ? d[0] + d[1] : d[0];  // (a warp without stages has no part)
+        if (next > begin) {  // (a warp without stages has no part)
+          v += ph.two ? d[0] + d[1] : d[0];
+          if (GATE_UP) u += ph.two ? d[up] + d[up + 1] : d[up];
+        }
         begin = next;
-        d += 2 * ph.part;
+        d += ph.part;
       }
-      v *= pl.inv[local][c];
-      const float up = __shfl_down_sync(0xFFFFFFFFu, v, 16);
+      const float f = pl.inv[local][c];
       unsigned m = 0;
-      if (GATE_UP ? half == 0 : c0 + half < sg.n) m = put<GATE_UP>(a, ph, pl, sg, c, 16 * g + row, v, up);
+      if (c0 + half < sg.n) m = put<GATE_UP>(a, ph, pl, sg, c, 16 * g + row, v * f, u * f);
       if (GATE_UP) {
-        m = __reduce_max_sync(0xFFFFFFFFu, m);
-        if (lane == 0) atomicMax(&pl.hmax[local][c], m);
+        const unsigned m0 = __reduce_max_sync(0xFFFFFFFFu, half ? 0u : m), m1 = __reduce_max_sync(0xFFFFFFFFu, half ? m : 0u);
+        if (lane == c0) tops = m0;
+        if (lane == c0 + 1) tops = m1;
       }
     }
+    if (GATE_UP && lane < sg.n) atomicMax(&pl.hmax[local][lane], tops);
   }
   if (GATE_UP) {
     __syncthreads();
@@ -808,10 +828,11 @@ __device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, 
 // The arrivals only ever count up (in 64 bits), so nothing has to be cleared.
 // arrive() returns the count to wait for, in thread 0.
 __device__ __forceinline__ unsigned long long grid_arrive(const MoeArgs& a) {
-  __threadfence();
   __syncthreads();
   if (threadIdx.x) return 0;
-  return (atomicAdd(a.arrivals, 1ull) / gridDim.x + 1) * gridDim.x;
+  unsigned long long before;
+  asm volatile("atom.add.release.gpu.global.u64 %0, [%1], 1;" : "=l"(before) : "l"(a.arrivals) : "memory");
+  return (before / gridDim.x + 1) * gridDim.x;
 }
 __device__ __forceinline__ bool grid_wait(const MoeArgs& a, Plan& pl, unsigned long long target) {
   if (threadIdx.x == 0) {
@@ -826,7 +847,6 @@ __device__ __forceinline__ bool grid_wait(const MoeArgs& a, Plan& pl, unsigned l
         break;
       }
     }
-    __threadfence();
     pl.go = go;
   }
   __syncthreads();
@@ -947,10 +967,10 @@ size_t shape_smem(MoeArgs& a) {
   // and if they are few enough for every CTA to read them all: 16384 values
   // took 2 us less than a third phase, 22016 took 2 us more
   a.single = a.T == 1 && a.k * padded(a.ph[1].K) <= 16384 &&
-             slots + 2 * kWarps * 2 * 16 * 2 * sizeof(float) <= left;
+             slots + kWarps * 2 * 16 * 2 * sizeof(float) <= left;
   for (int f = 0; f < 2; ++f) {
     Phase& ph = a.ph[f];
-    const size_t part = 2 * kWarps * (f == 0 ? 2 : 1) * 16 * sizeof(float);  // for each column
+    const size_t part = kWarps * (f == 0 ? 2 : 1) * 16 * sizeof(float);  // for each column
     const size_t need = (f == 1 && a.single ? 1 : static_cast<size_t>(pairs)) * (ph.two ? 2 : 1);
     size_t c = ph.two ? 2 : 1;  // powers of two
     while (c < kMaxCols && c < need && 2 * c * (static_cast<size_t>(padded(ph.K)) * 2 + part) <= left) c *= 2;
@@ -963,7 +983,7 @@ size_t shape_smem(MoeArgs& a) {
   while (b + tab > left) {
     const size_t c0 = static_cast<size_t>(a.ph[0].cap) * (a.ph[0].two ? 2 : 1);
     const size_t c1 = static_cast<size_t>(a.ph[1].cap) * (a.ph[1].two ? 2 : 1);
-    const size_t t0 = c0 * 4 * kWarps * 16 * sizeof(float), t1 = c1 * 2 * kWarps * 16 * sizeof(float);
+    const size_t t0 = c0 * 2 * kWarps * 16 * sizeof(float), t1 = c1 * kWarps * 16 * sizeof(float);
     const size_t b0 = c0 * padded(a.ph[0].K) * 2, b1 = c1 * padded(a.ph[1].K) * 2;
     tab = t0 > t1 ? t0 : t1;
     b = b0 > b1 ? b0 : b1;
