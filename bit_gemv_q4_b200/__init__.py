@@ -515,12 +515,12 @@ def _auto_workspace(name: str, need: int, device: torch.device, stream: int):
     key = (name, device.index, stream)
     ws = _call_ws.get(key)
     if (ws is not None and ws[2] >= need and stream == torch._C._cuda_getCurrentRawStream(device.index)
-            and not torch.cuda.is_current_stream_capturing()):
+            and not torch._C._cuda_isCurrentStreamCapturing()):
         return ws
     # cleared on the call's own stream; a captured call keeps a workspace of its own, which its
     # graph clears
     with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-        capturing = torch.cuda.is_current_stream_capturing()
+        capturing = torch._C._cuda_isCurrentStreamCapturing()
         if ws is None or ws[2] < need or capturing:
             t = torch.zeros(need, dtype=torch.uint8, device=device)
             ws = (t, t.data_ptr() or None, need)
@@ -536,8 +536,9 @@ def _on_device(call):
     @functools.wraps(call)
     def wrapped(*args, **kw):
         first = args[0] if args else kw.get(name)
-        if isinstance(first, torch.Tensor) and first.is_cuda and first.get_device() != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
+        device = -1 if first is None else first.get_device()  # -1: no CUDA tensor, which the call refuses
+        if device >= 0 and device != torch._C._cuda_getDevice():
+            with torch.cuda.device(device):
                 return call(*args, **kw)
         return call(*args, **kw)
     return wrapped
