@@ -566,13 +566,15 @@ __global__ void __launch_bounds__(256) fp8_sum_kernel(const float* parts, void* 
 
 // ------------------------------------------------------------------- host
 // Tiles of 128 x 128 take one unit of time for a k-step (0.42 us) and about
-// three more for a tile or piece; a second launch to add pieces up and its
-// traffic take about eight.  A pair's 256 x 256 tile takes 1.55 units a k-step, on
-// half as many SM pairs.  The plan with the shortest longest CTA is taken.
+// three more for a tile or piece; a second launch to add pieces up takes five,
+// and writing and reading them an eighth for each of 128 rows.  A pair's 256 x
+// 256 tile takes 1.55 units a k-step, on half as many SM pairs.  The plan with
+// the shortest longest CTA is taken.
 // Measured, 128 x 128 (uncut) against pairs: 500 tokens x 4096 x 4096, 17.6 and
 // 23.6 us; 1000 tokens, 30.9 and 24.9; 200 tokens x 11008 x 4096, 39.3 and 24.1;
-// 2048 tokens, 131 and 99.5.  One piece against four: 128 tokens x 4096 x 4096,
-// 16.0 and 13.2; x 4096 x 11008, 35.2 and 19.6.
+// 2048 tokens, 131 and 99.5.  Whole tiles against pieces: 128 tokens x 4096 x
+// 11008, 35.2 and 22.7 (four); 300 tokens, 35.9 and 42.3 (three); 256 tokens x
+// 2048 x 2048, 10.3 and 14.3 (two).
 struct Choice {
   int bn;
   bool pair;
@@ -595,7 +597,8 @@ Choice choose(int64_t M, int64_t K, int64_t B) {
   const int64_t pairs = (tpair + sms / 2 - 1) / (sms / 2) * (S + 3) * 14 / 9;
   int64_t best = 1, least = whole;
   for (int64_t c = 2; c <= 16 && c <= S && t128 < 2 * sms; ++c) {
-    const int64_t steps = (t128 * c + sms - 1) / sms * ((S + c - 1) / c + 3) + 8;
+    const int64_t steps =
+        (t128 * c + sms - 1) / sms * ((S + c - 1) / c + 3) + 5 + t128 * c * i64min(B, 128) / 1024;
     if (steps < least) {
       least = steps;
       best = c;
