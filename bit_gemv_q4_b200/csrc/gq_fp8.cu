@@ -120,6 +120,8 @@ __device__ __forceinline__ uint2 codes8(const float v[8], const Scale& c) {
 template <int TYPE>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const void* x, int64_t R, int K, int kblocks,
                                                             uint8_t* q, float* scales, int* dev_status) {
+  pdl_wait();
+  pdl_launch_dependents();
   const int64_t block = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 4;
   const int lane = threadIdx.x & 15;
   const bool in = block < R * kblocks;
@@ -146,6 +148,8 @@ constexpr int kTileThreads = 512;
 template <int TYPE>
 __global__ void __launch_bounds__(kTileThreads, 2) quantize_tiles_kernel(const void* x, int64_t R, int K, int kblocks,
                                                                       uint8_t* q, float* scales, int* dev_status) {
+  pdl_wait();
+  pdl_launch_dependents();
   constexpr int kRowsAtOnce = kTileThreads / 16, kPasses = kBlk / kRowsAtOnce;
   __shared__ unsigned top[kTileThreads / 32];  // bits: magnitudes and NaN are ordered as integers
   const int64_t rb = blockIdx.x / kblocks;
@@ -178,6 +182,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) quantize_tiles_kernel(const v
 // Sixteen codes a thread.
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* q, const float* scales, int64_t R,
                                                          int K, int kblocks, int shift, void* out, int type) {
+  pdl_wait();
+  pdl_launch_dependents();
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 16;
   if (i >= R * K) return;
   const int64_t r = i / K;
@@ -247,7 +253,7 @@ GQ_API gq_status gq_quantize_fp8(const void* x, int x_dtype, int64_t R, int64_t 
   const int64_t grid = rows == 1 ? (blocks + 15) / 16 : blocks;
   if (grid > 0x7FFFFFFFLL) return GQ_ERR_SHAPE;
   auto run = [&](auto kern) {
-    return launch(kern, dim3(static_cast<unsigned>(grid)), dim3(rows == 1 ? 256 : kTileThreads), 0, as_stream(stream), false, x, R,
+    return launch(kern, dim3(static_cast<unsigned>(grid)), dim3(rows == 1 ? 256 : kTileThreads), 0, as_stream(stream), true, x, R,
                   static_cast<int>(K), kblocks, static_cast<uint8_t*>(q), scales, dev_status);
   };
   if (rows == 1)
@@ -270,7 +276,7 @@ GQ_API gq_status gq_dequantize_fp8(const void* q, const float* scales, int64_t R
   if (misaligned16(q) || misaligned16(scales) || misaligned16(out)) return GQ_ERR_ALIGNMENT;
   const int64_t grid = (R * K / 16 + 255) / 256;
   if (grid > 0x7FFFFFFFLL) return GQ_ERR_SHAPE;
-  return launch(dequantize_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, as_stream(stream), false,
+  return launch(dequantize_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, as_stream(stream), true,
                 static_cast<const uint8_t*>(q), scales, R, static_cast<int>(K),
                 static_cast<int>((K + kBlk - 1) / kBlk), rows == 1 ? 0 : 7, out, out_dtype);
 }

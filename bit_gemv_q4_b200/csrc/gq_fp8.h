@@ -18,6 +18,6 @@ inline bool fp8_gemv_takes(int64_t M, int64_t K, int64_t B) {
 
 // Arguments as for gq_gemm_fp8, checked there; no workspace.
 gq_status fp8_gemv(const void* W, const float* sw, int64_t M, int64_t K, const void* X, const float* sx,
-                   int64_t B, void* Y, int yt, bool pdl, cudaStream_t s);
+                   int64_t B, void* Y, int yt, cudaStream_t s);
 
 }  // namespace gq

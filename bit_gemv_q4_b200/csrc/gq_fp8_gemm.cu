@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     report(a.dev_status, GQ_DEV_TIMEOUT);
     *reinterpret_cast<volatile int*>(abort_flag) = 1;
   };
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // only now: a dependent may rely on what ran before this call
 
   if (warp == kEpiWarps) {
     // ---------------------------------------------------------- producer
@@ -543,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int BN>
 __global__ void __launch_bounds__(256) fp8_sum_kernel(const float* parts, void* Y, int64_t M, int B, int rows, int tm,
                                                       int cuts, int ytype) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t quads = static_cast<int64_t>(tm) * (BN / 4);
   const int64_t b = i / quads, q = i - b * quads;
@@ -636,7 +636,7 @@ gq_status encode(CUtensorMap* map, CUtensorMapDataType type, int esize, const vo
 
 template <int BN, bool PAIR>
 gq_status launch_fp8(const CUtensorMap& xmap, const CUtensorMap& wmap, const CUtensorMap& ymap, const Args& a,
-                     bool pdl, cudaStream_t s) {
+                     cudaStream_t s) {
   auto kern = fp8_gemm_kernel<BN, PAIR>;
   constexpr int smem = Cfg<BN, PAIR>::kSmem;
   thread_local unsigned long long configured_ctx = 0;  // per host thread and context
@@ -647,9 +647,9 @@ gq_status launch_fp8(const CUtensorMap& xmap, const CUtensorMap& wmap, const CUt
     configured_ctx = ctx;
   }
   if (PAIR)
-    return launch_cluster(kern, dim3(static_cast<unsigned>(2 * a.sp.P)), dim3(kThreads), smem, s, pdl, 2u, xmap,
+    return launch_cluster(kern, dim3(static_cast<unsigned>(2 * a.sp.P)), dim3(kThreads), smem, s, true, 2u, xmap,
                           wmap, ymap, a);
-  return launch(kern, dim3(static_cast<unsigned>(a.sp.P)), dim3(kThreads), smem, s, pdl, xmap, wmap, ymap,
+  return launch(kern, dim3(static_cast<unsigned>(a.sp.P)), dim3(kThreads), smem, s, true, xmap, wmap, ymap,
                 a);
 }
 
@@ -687,8 +687,7 @@ GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, in
   const size_t need = ws_bytes_of(c, M, K, B);
   if (need && (!workspace || ws_bytes < need)) return GQ_ERR_WORKSPACE;
   if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return GQ_ERR_ALIGNMENT;
-  const bool pdl = (flags & GQ_GEMV_PDL) != 0;
-  if (fp8_gemv_takes(M, K, B)) return fp8_gemv(W, w_scales, M, K, X, x_scales, B, Y, y_dtype, pdl, s);
+  if (fp8_gemv_takes(M, K, B)) return fp8_gemv(W, w_scales, M, K, X, x_scales, B, Y, y_dtype, s);
 
   Args a{};
   a.sx = x_scales;
@@ -716,8 +715,8 @@ GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, in
                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                 esize, Y, B, M, 64 / esize, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (st != GQ_OK) return st;
-  if (c.pair) return launch_fp8<256, true>(xmap, wmap, ymap, a, pdl, s);
-  st = launch_fp8<128, false>(xmap, wmap, ymap, a, pdl, s);
+  if (c.pair) return launch_fp8<256, true>(xmap, wmap, ymap, a, s);
+  st = launch_fp8<128, false>(xmap, wmap, ymap, a, s);
   if (st != GQ_OK || c.sp.cuts == 1) return st;
   const int64_t threads = B * c.sp.tm * (128 / 4);
   return launch(fp8_sum_kernel<128>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, s, true,

@@ -65,8 +65,8 @@ __global__ void __launch_bounds__(kThreads) fp8_gemv_kernel(const Args a) {
   __shared__ float part[kWarps][16][8 * NT + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 16;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   const uint8_t* w[2];  // rows g8 and g8 + 8 (the last row stands in for those past it)
 #pragma unroll
   for (int i = 0; i < 2; ++i) w[i] = a.W + i64min(m0 + 8 * i + g8, a.M - 1) * a.K + 16 * t;
@@ -140,18 +140,18 @@ __global__ void __launch_bounds__(kThreads) fp8_gemv_kernel(const Args a) {
 }
 
 template <int NT, int AHEAD>
-gq_status run(const Args& a, bool pdl, cudaStream_t s) {
-  return launch(fp8_gemv_kernel<NT, AHEAD>, dim3(static_cast<unsigned>((a.M + 15) / 16)), dim3(kThreads), 0, s, pdl, a);
+gq_status run(const Args& a, cudaStream_t s) {
+  return launch(fp8_gemv_kernel<NT, AHEAD>, dim3(static_cast<unsigned>((a.M + 15) / 16)), dim3(kThreads), 0, s, true, a);
 }
 
 }  // namespace
 
 gq_status fp8_gemv(const void* W, const float* sw, int64_t M, int64_t K, const void* X, const float* sx,
-                   int64_t B, void* Y, int yt, bool pdl, cudaStream_t s) {
+                   int64_t B, void* Y, int yt, cudaStream_t s) {
   Args a{static_cast<const uint8_t*>(W), sw, static_cast<const uint8_t*>(X), sx, Y, M, K, static_cast<int>(B),
          static_cast<int>((K + 127) / 128), yt};
-  if (B <= 8) return run<1, 4>(a, pdl, s);
-  return run<2, 4>(a, pdl, s);
+  if (B <= 8) return run<1, 4>(a, s);
+  return run<2, 4>(a, s);
 }
 
 }  // namespace gq

@@ -80,11 +80,11 @@ gq_status launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t
   return e == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
 }
 
-// As launch(), with every CTA of the grid resident at the same time (the launch
-// is refused if they do not fit), for kernels with a grid barrier.
+// As launch() with pdl, and with every CTA of the grid resident at the same time
+// (the launch is refused if they do not fit), for kernels with a grid barrier.
 template <typename... KArgs, typename... Args>
 gq_status launch_cooperative(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                             cudaStream_t stream, bool pdl, Args&&... args) {
+                             cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -93,13 +93,10 @@ gq_status launch_cooperative(void (*kernel)(KArgs...), dim3 grid, dim3 block, si
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
-  cfg.numAttrs = 1;
-  if (pdl) {
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 2;
-  }
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
   return e == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
 }

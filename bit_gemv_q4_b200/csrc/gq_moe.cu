@@ -1007,7 +1007,7 @@ size_t shape_smem(MoeArgs& a) {
 }
 
 template <int FMT>
-gq_status launch_moe(MoeArgs& a, bool pdl, cudaStream_t s) {
+gq_status launch_moe(MoeArgs& a, cudaStream_t s) {
   auto kern = moe_kernel<FMT>;
   thread_local unsigned long long configured_ctx = 0;  // per host thread and context
   const unsigned long long ctx = context_id();
@@ -1018,7 +1018,7 @@ gq_status launch_moe(MoeArgs& a, bool pdl, cudaStream_t s) {
     configured_ctx = ctx;
   }
   const size_t smem = shape_smem(a);
-  return launch_cooperative(kern, dim3(sm_count()), dim3(kThreads), smem, s, pdl, a);
+  return launch_cooperative(kern, dim3(sm_count()), dim3(kThreads), smem, s, a);
 }
 
 template <int FMT>
@@ -1079,7 +1079,7 @@ gq_status moe_entry(const void* gate, const void* up, const void* down, int64_t 
   a.H = static_cast<int>(H);
   a.xtype = x_dtype;
   a.ytype = y_dtype;
-  return launch_moe<FMT>(a, (flags & GQ_GEMV_PDL) != 0, s);
+  return launch_moe<FMT>(a, s);
 }
 
 }  // namespace

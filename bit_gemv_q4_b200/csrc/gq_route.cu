@@ -227,11 +227,11 @@ __global__ void __launch_bounds__(kThreads, 2) route_kernel(const __grid_constan
 }
 
 template <int XT>
-gq_status launch_route(const RouteArgs& a, int wtype, dim3 grid, bool pdl, cudaStream_t s) {
+gq_status launch_route(const RouteArgs& a, int wtype, dim3 grid, cudaStream_t s) {
   switch (wtype) {
-    case GQ_F32: return launch(route_kernel<XT, GQ_F32>, grid, dim3(kThreads), 0, s, pdl, a);
-    case GQ_F16: return launch(route_kernel<XT, GQ_F16>, grid, dim3(kThreads), 0, s, pdl, a);
-    default: return launch(route_kernel<XT, GQ_BF16>, grid, dim3(kThreads), 0, s, pdl, a);
+    case GQ_F32: return launch(route_kernel<XT, GQ_F32>, grid, dim3(kThreads), 0, s, true, a);
+    case GQ_F16: return launch(route_kernel<XT, GQ_F16>, grid, dim3(kThreads), 0, s, true, a);
+    default: return launch(route_kernel<XT, GQ_BF16>, grid, dim3(kThreads), 0, s, true, a);
   }
 }
 
@@ -281,11 +281,10 @@ GQ_API gq_status gq_moe_route(const void* x, int x_dtype, int64_t T, int64_t H, 
   a.norm = (flags & GQ_ROUTE_NORM) != 0;
   a.scale = scale;
   const dim3 grid(static_cast<unsigned>((E + kTile - 1) / kTile), static_cast<unsigned>((T + kTile - 1) / kTile));
-  const bool pdl = (flags & GQ_GEMV_PDL) != 0;
   cudaStream_t s = as_stream(stream);
-  return x_dtype == GQ_F32   ? launch_route<GQ_F32>(a, w_dtype, grid, pdl, s)
-         : x_dtype == GQ_F16 ? launch_route<GQ_F16>(a, w_dtype, grid, pdl, s)
-                             : launch_route<GQ_BF16>(a, w_dtype, grid, pdl, s);
+  return x_dtype == GQ_F32   ? launch_route<GQ_F32>(a, w_dtype, grid, s)
+         : x_dtype == GQ_F16 ? launch_route<GQ_F16>(a, w_dtype, grid, s)
+                             : launch_route<GQ_BF16>(a, w_dtype, grid, s);
 }
 
 }  // extern "C"

@@ -393,8 +393,10 @@ GQ_API gq_status gq_gemm_ksb(const void* W, int64_t M, int64_t K,
  *   use; a successful call leaves it ready for the next call of any sizes;
  *   after a call that fails, zero it again.  Calls that may run at the same
  *   time need separate workspaces.
- * flags: GQ_ROUTE_* and GQ_GEMV_PDL (the call may be scheduled early; it waits
- *   for the preceding kernel before it reads anything). */
+ * flags: GQ_ROUTE_* and GQ_GEMV_PDL.  This call and those below may always be
+ *   scheduled while the previous kernel on the stream is still running: they
+ *   wait for it before they read or write anything, so GQ_GEMV_PDL changes
+ *   nothing (it is accepted so that a chain of calls can share its flags). */
 #define GQ_ROUTE_NORM    2u
 #define GQ_ROUTE_SIGMOID 4u
 GQ_API size_t gq_moe_route_workspace_bytes(int64_t T, int64_t E);
@@ -430,8 +432,7 @@ GQ_API gq_status gq_moe_route(const void* x, int x_dtype, int64_t T, int64_t H, 
  *   aligned, all zero before its first use; a successful call leaves it ready
  *   for the next call of any sizes; after a call that fails, zero it again.
  *   Calls that may run at the same time need separate workspaces.
- * flags: 0 or GQ_GEMV_PDL (the call may be scheduled early; it waits for the
- *   preceding kernel, which may be the router, before it reads ids or x).
+ * flags: 0 or GQ_GEMV_PDL (which changes nothing, as for the router).
  * One cooperative launch with a CTA on every SM of the device: it starts when
  *   all of them are free of other kernels' shared memory (GQ_ERR_CUDA if the
  *   process may not use them all).
@@ -483,8 +484,7 @@ GQ_API gq_status gq_dequantize_fp8(const void* q, const float* scales, int64_t R
  * workspace / ws_bytes: at least gq_gemm_fp8_workspace_bytes(M, K, B) bytes
  *   (GQ_ERR_WORKSPACE otherwise; 0 for many shapes), 256-byte aligned, of any
  *   contents.  Calls that may run at the same time need separate workspaces.
- * flags: 0 or GQ_GEMV_PDL (the call may be scheduled early; it waits for the
- *   preceding kernel before it reads anything).
+ * flags: 0 or GQ_GEMV_PDL (which changes nothing, as for the router).
  * dev_status: optional, receives GQ_DEV_TIMEOUT if a pipeline wait gives up. */
 GQ_API size_t gq_gemm_fp8_workspace_bytes(int64_t M, int64_t K, int64_t B);
 GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, int64_t K, const void* X,

@@ -296,3 +296,33 @@ def test_layer_writes_over_its_input():
         m(x, ids, w, out=x)
         assert torch.equal(x, want)
         assert np.isfinite(x.float().cpu().numpy()).all()
+
+
+def test_buffers_that_the_next_call_writes_again():
+    # calls may start early: each has to wait for the one before it before it writes what that one reads
+    m = Layer(Q40, 8, 512, 192)
+    Wr = torch.randn(8, 512, device="cuda")
+    W, ws = gq.gq_quantize_fp8(torch.randn(1030, 512, device="cuda"), 128)
+    xs = [torch.randn(T, 512, device="cuda", dtype=torch.bfloat16) for T in (40, 3, 40, 17, 1, 40) for _ in range(4)]
+    ids, w = torch.empty(40 * 3, dtype=torch.int32, device="cuda"), torch.empty(40 * 3, device="cuda")
+    q = torch.empty(40, 512, dtype=torch.float8_e4m3fn, device="cuda")
+    s, y = torch.empty(40, 4, device="cuda"), torch.empty(40, 512, dtype=torch.bfloat16, device="cuda")
+
+    def chain(x, sync):
+        T = x.shape[0]
+        step = torch.cuda.synchronize if sync else lambda: None
+        i, v = gq.gq_moe_route(x, Wr, 3, ids=ids[:T * 3].view(T, 3), weights=w[:T * 3].view(T, 3))
+        step()
+        m(x, i, v, out=y[:T])
+        step()
+        gq.gq_quantize_fp8(y[:T], 1, out=q[:T], scales=s[:T])
+        step()
+        out = gq.gq_gemm_fp8(W, ws, q[:T], s[:T])
+        step()
+        return out
+
+    want = [chain(x, True) for x in xs]
+    for _ in range(5):
+        got = [chain(x, False) for x in xs]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
