@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* q, const
   if (i >= R * K) return;
   const int64_t r = i / K;
   const int k = static_cast<int>(i - r * K);
-  const float s = __ldg(scales + (r >> shift) * kblocks + k / kBlk);
+  const float s = scales[(r >> shift) * kblocks + k / kBlk];
   const uint4 u = __ldcs(reinterpret_cast<const uint4*>(q + i));
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   float v[16];

@@ -413,12 +413,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < kFactorSteps; ++j) {
           const int kj = min(ks + j, k1 - 1);
-          lo[j] = __ldg(swl + kj);
-          hi[j] = __ldg(swh + kj);
+          lo[j] = swl[kj];
+          hi[j] = swh[kj];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = min(row0 + lane + 32 * i, a.B - 1);
-            x[i][j] = __ldg(a.sx + static_cast<int64_t>(row) * a.kblocks + kj);
+            x[i][j] = a.sx[static_cast<int64_t>(row) * a.kblocks + kj];
           }
         }
         const int slot = q % kFactorSlots;

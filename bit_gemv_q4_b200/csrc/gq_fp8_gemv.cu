@@ -49,9 +49,10 @@ __device__ __forceinline__ void mma_e4m3(float c[4], uint32_t a0, uint32_t a1, u
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// (Volatile, and not through the read-only path: the weights may be the preceding kernel's.)
 __device__ __forceinline__ uint4 read_once(const uint8_t* p) {
   uint4 v;
-  asm("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
       : "l"(p));
   return v;
@@ -101,16 +102,16 @@ __global__ void __launch_bounds__(kThreads) fp8_gemv_kernel(const Args a) {
     for (int u = 0; u < AHEAD; ++u) {
       const int g = g0 + kWarps * u;
       if (g >= a.groups) break;
-      const float s = __ldg(sw + g);
+      const float s = sw[g];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         uint4 xv[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int64_t k = static_cast<int64_t>(g) * 128 + 64 * h;
-          xv[h] = k + 16 * t < a.K ? __ldg(reinterpret_cast<const uint4*>(x[j] + k)) : make_uint4(0, 0, 0, 0);
+          xv[h] = k + 16 * t < a.K ? *reinterpret_cast<const uint4*>(x[j] + k) : make_uint4(0, 0, 0, 0);
         }
-        const float f0 = s * __ldg(sx[j][0] + g), f1 = s * __ldg(sx[j][1] + g);
+        const float f0 = s * sx[j][0][g], f1 = s * sx[j][1][g];
         float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

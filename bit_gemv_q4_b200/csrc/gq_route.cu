@@ -59,8 +59,8 @@ struct Raw {
 template <int TYPE>
 __device__ __forceinline__ void load8(Raw<TYPE>& r, const void* base, int64_t at, bool ok) {
   const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + at * (TYPE == GQ_F32 ? 4 : 2));
-  r.v[0] = ok ? __ldg(p) : uint4{};
-  if constexpr (TYPE == GQ_F32) r.v[1] = ok ? __ldg(p + 1) : uint4{};
+  r.v[0] = ok ? p[0] : uint4{};
+  if constexpr (TYPE == GQ_F32) r.v[1] = ok ? p[1] : uint4{};
 }
 // Value i of them (i a constant).
 template <int TYPE>
@@ -101,7 +101,7 @@ __device__ __forceinline__ void pick(const RouteArgs& a, int64_t t) {
     const int e = lane + 32 * i;
     double v = e < a.E ? __ldcg(s + e) : 0.0;
     bad |= !isfinite(v);
-    if (a.bias && e < a.E) v += static_cast<double>(__ldg(a.bias + e));
+    if (a.bias && e < a.E) v += static_cast<double>(a.bias[e]);
     bad |= isnan(v);
     key[i] = e < a.E ? sortable(v + 0.0) : 0;  // (-0 and +0 are equal keys)
   }
