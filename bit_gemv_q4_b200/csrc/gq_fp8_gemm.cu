@@ -36,6 +36,13 @@
 // us more at 37 tokens.)
 // For fewer than 128 tokens only the rows that exist are loaded; the other
 // lanes hold garbage that nothing reads.
+//
+// Measured: 4096 tokens x 11008 x 4096 (fp32 out), 210 us, 1.76 PFLOP/s (250 us
+// in a long loop, at 1600 MHz under the power limit).  Loads and MMAs alone take
+// 113 us of it, the handshakes 22 more; reading the sums of each group back from
+// tensor memory adds 60 (it shares that memory with the MMAs).  500 tokens x 4096
+// x 11008, 35 us, bound by the tiles' traffic from L2 (10 TB/s); 37 tokens x
+// 11000 x 4096, 16.3 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
