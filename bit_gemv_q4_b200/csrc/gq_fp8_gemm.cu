@@ -11,13 +11,13 @@
 //
 // One CTA per SM, over tiles of 128 tokens x BN weight rows and k-steps of one
 // group:
-//  * warp 16 (producer): both operands' 128-byte rows by TMA, 128-byte swizzle;
-//  * warp 17 (MMA): four tcgen05.mma (K = 32) to a k-step, into one of the
+//  * warp 8 (producer): both operands' 128-byte rows by TMA, 128-byte swizzle;
+//  * warp 9 (MMA): four tcgen05.mma (K = 32) to a k-step, into one of the
 //    accumulator buffers in tensor memory (512 columns in all);
-//  * warp 18 (scales): the factors of four k-steps at a time, ahead of their
+//  * warp 10 (scales): the factors of four k-steps at a time, ahead of their
 //    use, into shared memory;
-//  * warps 0..15: read the buffer back and add it, times the factor, to sums in
-//    registers (a thread holds one token and a quarter of the columns); at the
+//  * warps 0..7: read the buffer back and add it, times the factor, to sums in
+//    registers (a thread holds one token and half of the columns); at the
 //    end of a tile they round once and store, through shared memory and TMA
 //    where Y's rows allow it (from registers the stores of a 180 MB output cost
 //    48 us: the tile's sums have to leave before the next one's begin).
@@ -37,12 +37,12 @@
 // For fewer than 128 tokens only the rows that exist are loaded; the other
 // lanes hold garbage that nothing reads.
 //
-// Measured: 4096 tokens x 11008 x 4096 (fp32 out), 210 us, 1.76 PFLOP/s (250 us
+// Measured: 4096 tokens x 11008 x 4096 (fp32 out), 204 us, 1.81 PFLOP/s (240 us
 // in a long loop, at 1600 MHz under the power limit).  Loads and MMAs alone take
 // 113 us of it, the handshakes 22 more; reading the sums of each group back from
 // tensor memory adds 60 (it shares that memory with the MMAs).  500 tokens x 4096
-// x 11008, 35 us, bound by the tiles' traffic from L2 (10 TB/s); 37 tokens x
-// 11000 x 4096, 16.3 us.
+// x 11008, 35 us, and 37 x 11000 x 4096, 16.1 us: 0.38 us for each k-step, which
+// is what the handshakes of the four roles take without loads and MMAs, too.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -60,7 +60,7 @@ namespace {
 
 constexpr int kBM = 128;                 // tokens of a tile
 constexpr int kBK = 128;                 // bytes of K in a step: one group of scales
-constexpr int kEpiWarps = 16;
+constexpr int kEpiWarps = 8;              // (sixteen: the largest case 210 us instead of 204, others the same)
 constexpr int kThreads = 32 * (kEpiWarps + 3);
 constexpr int kStoreBytes = 2048;        // 32 rows x 64 bytes of outputs, for each epilogue warp
 constexpr int kFactorSteps = 4;          // k-steps of a slot of factors
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (any) {
-          // 16 columns at a time; four warps on each scheduler take turns
+          // 16 columns at a time; two warps on each scheduler take turns
           const float2 f = make_float2(fac, fac);
           const uint32_t src = tmem + lane_base + static_cast<uint32_t>(buf * BN + cols0);
 #pragma unroll
