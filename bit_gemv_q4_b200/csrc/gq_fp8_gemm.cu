@@ -39,10 +39,11 @@
 //
 // Measured: 4096 tokens x 11008 x 4096 (fp32 out), 204 us, 1.81 PFLOP/s (240 us
 // in a long loop, at 1600 MHz under the power limit).  Loads and MMAs alone take
-// 113 us of it, the handshakes 22 more; reading the sums of each group back from
-// tensor memory adds 60 (it shares that memory with the MMAs).  500 tokens x 4096
-// x 11008, 35 us, and 37 x 11000 x 4096, 16.1 us: 0.38 us for each k-step, which
-// is what the handshakes of the four roles take without loads and MMAs, too.
+// 113 us; with sixteen promoting warps the whole took 212, without the reads of
+// tensor memory 197, without the MMAs 186, without either and without loads 172:
+// the handshakes and sums of each k-step bound it.  So they do 500 tokens x 4096
+// x 11008, 35 us, and 37 x 11000 x 4096, 16.1 us: 0.38 us a k-step, 0.37 without
+// loads, MMAs and reads.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(256) fp8_sum_kernel(const float* parts, void* 
 }
 
 // ------------------------------------------------------------------- host
-// Tiles of 128 x 128 take one unit of time for a k-step (0.42 us) and about
+// Tiles of 128 x 128 take one unit of time for a k-step (0.38 us) and about
 // three more for a tile or piece; a second launch to add pieces up takes five,
 // and writing and reading them an eighth for each of 128 rows.  A pair's 256 x
 // 256 tile takes 1.55 units a k-step, on half as many SM pairs.  The plan with
