@@ -7,6 +7,13 @@ Python or CPU fallback, and importing this package fails if the library has
 not been built (``python bit_gemv_q4_b200/build.py``).
 
 PyTorch is used only to allocate device memory and to name the stream.
+
+`stream` (a torch stream or a raw handle) names the stream of one call, the
+current one otherwise; what the call reads has to be ready on it.  The outputs
+that the router, the expert layer and the 8-bit calls make on a named stream
+are memory of that stream: order later use on other streams after it
+(Stream.wait_stream), and record such use (Tensor.record_stream) if the tensor
+may be dropped before it has happened.
 """
 from __future__ import annotations
 
@@ -557,6 +564,16 @@ def _raw_stream(stream, device: torch.device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new(like: torch.Tensor, shape, dtype, stream: int) -> torch.Tensor:
+    """An output of a call on `stream`, in memory of that stream: what the current stream has freed it
+    may still be reading.  (Use on another stream is the caller's to order, and to record before the
+    tensor is dropped.)"""
+    if stream == torch._C._cuda_getCurrentRawStream(like.device.index):
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device)):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _workspace(name: str, workspace, need: int, device: torch.device, stream: int):
     """(address, bytes, what keeps the memory until the launch)."""
     if isinstance(workspace, str):
@@ -598,11 +615,11 @@ def gq_moe_route(x: torch.Tensor, Wr: torch.Tensor, k: int, bias: torch.Tensor |
         raise ValueError("bias holds E fp32 values")
     s = _raw_stream(stream, x.device)
     if ids is None:
-        ids = x.new_empty((T, k), dtype=torch.int32)
+        ids = _new(x, (T, k), torch.int32, s)
     elif ids.dtype != torch.int32 or ids.numel() != T * k:
         raise ValueError("ids holds T * k int32 values")
     if weights is None:
-        weights = x.new_empty((T, k), dtype=torch.float32)
+        weights = _new(x, (T, k), torch.float32, s)
     elif weights.dtype != torch.float32 or weights.numel() != T * k:
         raise ValueError("weights holds T * k fp32 values")
     ws, ws_bytes, keep = _workspace("route", workspace, _size("gq_moe_route_workspace_bytes", T, E), x.device, s)
@@ -631,7 +648,7 @@ def _moe(name: str, fmt: int, gate, up, down, E: int, I: int, x: torch.Tensor, i
         raise ValueError("gate, up or down is smaller than the tiled storage of E experts")
     s = _raw_stream(stream, x.device)
     if out is None:
-        out = x.new_empty((T, H), dtype=y_dtype)
+        out = _new(x, (T, H), y_dtype, s)
     elif out.dtype not in _DTYPE_CODE or out.numel() != T * H:
         raise ValueError("out holds T * H values")
     ws, ws_bytes, keep = _workspace(name, workspace, _size("gq_moe_workspace_bytes", fmt, H, I, T, k), x.device, s)
@@ -698,15 +715,16 @@ def gq_quantize_fp8(x: torch.Tensor, rows: int, out: torch.Tensor | None = None,
     if rows not in (1, 128):
         raise ValueError("rows is 1 or 128")
     R, K = x.shape
+    s = _raw_stream(stream, x.device)
     given = out is not None or scales is not None
     if out is None:
-        out = x.new_empty((R, K), dtype=torch.float8_e4m3fn)
+        out = _new(x, (R, K), torch.float8_e4m3fn, s)
     if scales is None:
-        scales = x.new_empty((-(-R // rows), -(-K // 128)), dtype=torch.float32)
+        scales = _new(x, (-(-R // rows), -(-K // 128)), torch.float32, s)
     if given and _fp8_pair(out, scales, rows, "out") != (R, K):
         raise ValueError("out has another shape than x")
     _check(lib.gq_quantize_fp8(_ptr(x), _DTYPE_CODE[x.dtype], R, K, rows, _ptr(out), _ptr(scales),
-                               _ptr(dev_status), _raw_stream(stream, x.device)), "gq_quantize_fp8")
+                               _ptr(dev_status), s), "gq_quantize_fp8")
     return out, scales
 
 
@@ -719,12 +737,13 @@ def gq_dequantize_fp8(q: torch.Tensor, scales: torch.Tensor, rows: int, dtype=to
     R, K = _fp8_pair(q, scales, rows, "q")
     if dtype not in _DTYPE_CODE:
         raise TypeError("outputs must be float32, float16 or bfloat16")
+    s = _raw_stream(stream, q.device)
     if out is None:
-        out = q.new_empty((R, K), dtype=dtype)
+        out = _new(q, (R, K), dtype, s)
     elif out.dtype not in _DTYPE_CODE or out.numel() != R * K:
         raise ValueError("out holds R * K values")
     _check(lib.gq_dequantize_fp8(_ptr(q), _ptr(scales), R, K, rows, _ptr(out), _DTYPE_CODE[out.dtype],
-                                 _raw_stream(stream, q.device)), "gq_dequantize_fp8")
+                                 s), "gq_dequantize_fp8")
     return out
 
 
@@ -747,7 +766,7 @@ def gq_gemm_fp8(W: torch.Tensor, w_scales: torch.Tensor, X: torch.Tensor, x_scal
         raise TypeError("outputs must be float32, float16 or bfloat16")
     s = _raw_stream(stream, X.device)
     if out is None:
-        out = X.new_empty((B, M), dtype=y_dtype)
+        out = _new(X, (B, M), y_dtype, s)
     elif out.dtype not in _DTYPE_CODE or out.numel() != B * M:
         raise ValueError("out holds B * M values")
     ws, ws_bytes, keep = _workspace("gq_gemm_fp8", workspace, _size("gq_gemm_fp8_workspace_bytes", M, K, B),
