@@ -526,7 +526,7 @@ def _auto_workspace(name: str, need: int, device: torch.device, stream: int):
         return ws
     # cleared on the call's own stream; a captured call keeps a workspace of its own, which its
     # graph clears
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+    with torch.cuda.stream(_stream_object(stream, device)):
         capturing = torch._C._cuda_isCurrentStreamCapturing()
         if ws is None or ws[2] < need or capturing:
             t = torch.zeros(need, dtype=torch.uint8, device=device)
@@ -564,13 +564,21 @@ def _raw_stream(stream, device: torch.device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _stream_object(stream: int, device: torch.device):
+    """A raw handle as a stream that torch allocates and launches on.  (Handles 0 and 1 are the default
+    stream; ExternalStream(0) would be some stream of torch's pool.)"""
+    if stream in (0, 1):
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(stream, device=device)
+
+
 def _new(like: torch.Tensor, shape, dtype, stream: int) -> torch.Tensor:
     """An output of a call on `stream`, in memory of that stream: what the current stream has freed it
     may still be reading.  (Use on another stream is the caller's to order, and to record before the
     tensor is dropped.)"""
     if stream == torch._C._cuda_getCurrentRawStream(like.device.index):
         return like.new_empty(shape, dtype=dtype)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device)):
+    with torch.cuda.stream(_stream_object(stream, like.device)):
         return like.new_empty(shape, dtype=dtype)
 
 

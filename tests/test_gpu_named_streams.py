@@ -78,3 +78,29 @@ def test_named_stream_inside_a_capture(name):
         graph.replay()
         torch.cuda.synchronize()
         assert same(got, want)
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("stream", [0, 1, "object"])
+def test_the_default_stream_named_while_another_is_current(name, stream, monkeypatch):
+    # its workspace and its outputs are made, and the workspace cleared, on the default stream
+    call = calls()[name]
+    want = call()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(gq, "_call_ws", {})
+    seen = []
+
+    def watched(make):
+        def made(*args, **kw):
+            seen.append(torch.cuda.current_stream().cuda_stream)
+            return make(*args, **kw)
+        return made
+
+    monkeypatch.setattr(torch, "zeros", watched(torch.zeros))
+    monkeypatch.setattr(torch.Tensor, "new_empty", watched(torch.Tensor.new_empty))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = call(stream=torch.cuda.default_stream() if stream == "object" else stream)
+    torch.cuda.synchronize()
+    assert same(got, want)
+    assert seen and all(s == 0 for s in seen)
