@@ -48,7 +48,7 @@ EXPORTS = (
     "gq_tiled_bytes", "gq_repack_q4_0", "gq_repack_ksb", "gq_gemv_q4_0_tiled", "gq_gemv_ksb_tiled",
     "gq_gemv_q4_0_tiled_grouped", "gq_gemv_ksb_tiled_grouped",
     "gq_moe_route_workspace_bytes", "gq_moe_route",
-    "gq_moe_workspace_bytes", "gq_moe_q4_0_tiled", "gq_moe_ksb_tiled",
+    "gq_moe_workspace_bytes", "gq_moe_q4_0_tiled", "gq_moe_ksb_tiled", "gq_selftest_moe_timeout",
     "gq_fp8_scales", "gq_quantize_fp8", "gq_dequantize_fp8",
     "gq_gemm_fp8_workspace_bytes", "gq_gemm_fp8",
 )
@@ -136,6 +136,9 @@ def _load() -> ctypes.CDLL:
         f.argtypes = [vp, vp, vp, i64, i64, i64, vp, c_int, i64, vp, vp, i64, vp, c_int, vp,
                       ctypes.c_size_t, c_uint, vp, vp]
         f.restype = c_int
+    L.gq_selftest_moe_timeout.argtypes = [vp, vp, vp, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp,
+                                          ctypes.c_size_t, vp, vp]
+    L.gq_selftest_moe_timeout.restype = c_int
     L.gq_fp8_scales.argtypes = [i64, i64, i64]
     L.gq_fp8_scales.restype = ctypes.c_size_t
     L.gq_quantize_fp8.argtypes = [vp, c_int, i64, i64, i64, vp, vp, vp, vp]
@@ -693,6 +696,30 @@ def gq_moe_ksb_tiled(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, E
     """gq_moe_q4_0_tiled on super-block experts."""
     return _moe("gq_moe_ksb_tiled", GQ_FMT_KSB, gate, up, down, E, I, x, ids, weights, y_dtype, out,
                 workspace, flags, dev_status, stream)
+
+
+@_on_device
+def gq_selftest_moe_timeout(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, E: int, I: int,
+                            x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, y: torch.Tensor,
+                            dev_status: torch.Tensor, workspace="auto", stream=None) -> None:
+    """gq_moe_q4_0_tiled on fp16 x and y with a grid barrier that is never passed; the bounded waits
+    must report GQ_DEV_TIMEOUT in dev_status (see include/gq.h).  workspace: as for the layer, "auto"
+    the same one that gq_moe_q4_0_tiled uses."""
+    T, H = x.shape
+    k = ids.shape[1]
+    if x.dtype != torch.float16 or y.dtype != torch.float16 or y.numel() != T * H:
+        raise ValueError("x and y are fp16 [T, H]")
+    if ids.dtype != torch.int32 or weights.dtype != torch.float32 or ids.shape != (T, k) or weights.shape != (T, k):
+        raise ValueError("ids and weights are [T, k], int32 and fp32")
+    gu, dn = _size("gq_tiled_bytes", GQ_FMT_Q4_0, E * I, H), _size("gq_tiled_bytes", GQ_FMT_Q4_0, E * H, I)
+    if gate.numel() < gu or up.numel() < gu or down.numel() < dn:
+        raise ValueError("gate, up or down is smaller than the tiled storage of E experts")
+    s = _raw_stream(stream, x.device)
+    ws, ws_bytes, keep = _workspace("gq_moe_q4_0_tiled", workspace,
+                                    _size("gq_moe_workspace_bytes", GQ_FMT_Q4_0, H, I, T, k), x.device, s)
+    _check(lib.gq_selftest_moe_timeout(_ptr(gate), _ptr(up), _ptr(down), E, H, I, _ptr(x), T, _ptr(ids),
+                                       _ptr(weights), k, _ptr(y), ws, ws_bytes, _ptr(dev_status), s),
+           "gq_selftest_moe_timeout")
 
 
 def gq_fp8_scales(R: int, K: int, rows: int) -> int:

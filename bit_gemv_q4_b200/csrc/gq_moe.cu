@@ -109,10 +109,11 @@ struct MoeArgs {
   void* y;                  // [T][H]
   float* h;                 // [pairs][I], by slot
   float* out;               // [pairs][H], by pair
-  unsigned* hmax;           // [2][pairs] largest |h| of a slot as bits; see hmax_set()
+  unsigned long long* hmax; // [pairs] largest |h| of a slot, under the call's number; see note_hmax()
   unsigned long long* arrivals;  // at the grid barriers, a multiple of the grid between calls
   int* dev_status;
   long long budget;
+  int missing;              // arrivals that a grid barrier waits for in vain (the self-test), or 0
   int T, k, E, H;
   Div by_grid;
   int single;               // one token: down's rows run over its slots
@@ -136,7 +137,7 @@ struct Col {
 struct Plan {
   int nseg[2];
   int go;                              // the grid barrier was passed
-  unsigned* hmax_now;                  // the set of this call
+  unsigned long long call;             // this call's number; see note_hmax()
   unsigned common;                     // a single token's largest |weight * h|
   // of a string's segments
   int ncols;                           // tokens of all segments
@@ -266,6 +267,25 @@ __device__ __forceinline__ float scale_of(unsigned maxbits) {
   return __uint_as_float(static_cast<unsigned>(127 + 14 - max(e, -100)) << 23);
 }
 
+// The largest |h| of a slot is agreed on through the workspace, by all CTAs that
+// have rows of it.  An entry is the number of the call that wrote it (48 bits)
+// over the upper 16 bits of the value's (its exponent, which sets the scale, and
+// seven bits more): entries of other calls are smaller and count as zero, so none
+// has to be cleared, and what a call leaves that gave up at a barrier does no harm.
+// The number is one more than the barriers that the grid has passed: no CTA of
+// this call can have changed it before this CTA arrives, and it grows with every
+// call, also with one that gives up (all its CTAs arrive at its barriers).
+__device__ __forceinline__ unsigned long long call_number(const MoeArgs& a) {
+  return __ldcg(a.arrivals) / gridDim.x + 1;
+}
+__device__ __forceinline__ void note_hmax(const MoeArgs& a, const Plan& pl, int slot, unsigned bits) {
+  atomicMax(a.hmax + slot, pl.call << 16 | bits >> 15);
+}
+__device__ __forceinline__ unsigned read_hmax(const MoeArgs& a, const Plan& pl, int slot) {
+  const unsigned long long v = __ldcg(a.hmax + slot);
+  return v >> 16 == pl.call ? static_cast<unsigned>(v & 0xFFFFu) << 15 : 0u;
+}
+
 // Columns that the B fragments of a segment have room for: a power of two, so
 // that every offset in the inner loop is a constant.
 __device__ __forceinline__ int col_pitch(int ncol) {
@@ -294,7 +314,7 @@ __device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& 
   if (i < segs) sg = pl.seg[!GATE_UP][seg0 + i];
   if (c < sg.n) {
     const int row = GATE_UP ? pl.order[sg.slot0 + c] / a.k : sg.slot0 + c;
-    unsigned top = find ? 0u : GATE_UP ? 0x46800000u : __ldcg(pl.hmax_now + row);  // (2^14: a scale of 1)
+    unsigned top = find ? 0u : GATE_UP ? 0x46800000u : read_hmax(a, pl, row);  // (2^14: a scale of 1)
     float mul = 1.0f;
     if (single) {
       mul = pl.weight[pl.order[row]];
@@ -780,7 +800,7 @@ __device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Pl
     if (threadIdx.x < st.segs * kMaxCols) {
       const int i = threadIdx.x / kMaxCols, c = threadIdx.x % kMaxCols;
       const Seg sh = pl.seg[0][st.seg0 + i];
-      if (c < sh.n) atomicMax(pl.hmax_now + sh.slot0 + c, pl.hmax[i][c]);
+      if (c < sh.n) note_hmax(a, pl, sh.slot0 + c, pl.hmax[i][c]);
     }
   }
 }
@@ -848,7 +868,7 @@ __device__ __forceinline__ bool grid_wait(const MoeArgs& a, Plan& pl, unsigned l
     for (;;) {
       unsigned long long v;
       asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(a.arrivals) : "memory");
-      if (v >= target) break;
+      if (v >= target + a.missing) break;
       if (clock64() - t0 > a.budget) {
         go = 0;
         break;
@@ -858,22 +878,6 @@ __device__ __forceinline__ bool grid_wait(const MoeArgs& a, Plan& pl, unsigned l
   }
   __syncthreads();
   return pl.go != 0;
-}
-
-// The set of hmax that this call uses: by the parity of the barriers that the
-// grid has passed, which no CTA of this call can have changed before this CTA
-// arrives.  It is all zeros; the other set is cleared here for a call after one
-// barrier, and this call's own set at the end of a call with two.
-__device__ __forceinline__ void hmax_set(const MoeArgs& a, Plan& pl) {
-  if (threadIdx.x == 0) {
-    const unsigned long long n = __ldcg(a.arrivals);
-    pl.hmax_now = a.hmax + ((n / gridDim.x) & 1) * kMaxPairs;
-  }
-  if (blockIdx.x == 0) {
-    __syncthreads();
-    unsigned* other = pl.hmax_now == a.hmax ? a.hmax + kMaxPairs : a.hmax;
-    for (int i = threadIdx.x; i < kMaxPairs; i += kThreads) other[i] = 0u;
-  }
 }
 
 template <int FMT>
@@ -891,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   __syncthreads();
   pdl_wait();  // ids and x are final
   pdl_launch_dependents();
-  hmax_set(a, pl);
+  if (threadIdx.x == 0) pl.call = call_number(a);
   make_plan(pl, a);
   {
     Work<FMT, true> gate_up;
@@ -920,11 +924,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     if (threadIdx.x == 0) report(a.dev_status, GQ_DEV_TIMEOUT);
     return;
   }
-  // y[t] = sum_j w[t][j] * out[t][j] over the slots that name an expert; the
-  // slots' largest values are cleared for the next call
+  // y[t] = sum_j w[t][j] * out[t][j] over the slots that name an expert
   const int n = a.T * a.H;
   const int i0 = static_cast<int>(blockIdx.x * kThreads + threadIdx.x);
-  if (i0 < a.T * a.k) pl.hmax_now[i0] = 0u;
   for (int i = i0; i < n; i += static_cast<int>(gridDim.x) * kThreads) {
     const int t = i / a.H, c = i - t * a.H;
     float v = 0.f;
@@ -947,7 +949,7 @@ Ws ws_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
   Ws w;
   w.arrivals = 0;
   w.hmax = 256;
-  w.h = w.hmax + 2 * kMaxPairs * 4;  // one size for every call, so that calls of any sizes may follow
+  w.h = w.hmax + kMaxPairs * 8;  // one size for every call, so that calls of any sizes may follow
   w.out = w.h + round256(static_cast<size_t>(T * k * I) * 4);
   w.total = w.out + round256(static_cast<size_t>(T * k * H) * 4);
   return w;
@@ -1032,7 +1034,8 @@ template <int FMT>
 gq_status moe_entry(const void* gate, const void* up, const void* down, int64_t E, int64_t H,
                     int64_t I, const void* x, int x_dtype, int64_t T, const int32_t* ids,
                     const float* weights, int64_t k, void* y, int y_dtype, void* workspace,
-                    size_t ws_bytes, unsigned flags, int* dev_status, void* stream) {
+                    size_t ws_bytes, unsigned flags, int* dev_status, void* stream,
+                    long long budget = kWaitBudget, int missing = 0) {
   if (E < 0 || H < 0 || I < 0 || T < 0 || k < 0) return GQ_ERR_INVALID_ARG;
   if (!valid_act_dtype(x_dtype) || !valid_act_dtype(y_dtype)) return GQ_ERR_DTYPE;
   if (flags & ~GQ_GEMV_PDL) return GQ_ERR_INVALID_ARG;
@@ -1076,10 +1079,11 @@ gq_status moe_entry(const void* gate, const void* up, const void* down, int64_t 
   a.y = y;
   a.h = reinterpret_cast<float*>(ws + l.h);
   a.out = reinterpret_cast<float*>(ws + l.out);
-  a.hmax = reinterpret_cast<unsigned*>(ws + l.hmax);
+  a.hmax = reinterpret_cast<unsigned long long*>(ws + l.hmax);
   a.arrivals = reinterpret_cast<unsigned long long*>(ws + l.arrivals);
   a.dev_status = dev_status;
-  a.budget = kWaitBudget;
+  a.budget = budget;
+  a.missing = missing;
   a.T = static_cast<int>(T);
   a.k = static_cast<int>(k);
   a.E = static_cast<int>(E);
@@ -1116,6 +1120,16 @@ GQ_API gq_status gq_moe_ksb_tiled(const void* gate, const void* up, const void* 
                                   int* dev_status, void* stream) {
   return gq::moe_entry<GQ_FMT_KSB>(gate, up, down, E, H, I, x, x_dtype, T, ids, weights, k, y, y_dtype,
                                    workspace, ws_bytes, flags, dev_status, stream);
+}
+
+GQ_API gq_status gq_selftest_moe_timeout(const void* gate, const void* up, const void* down, int64_t E,
+                                         int64_t H, int64_t I, const void* x, int64_t T,
+                                         const int32_t* ids, const float* weights, int64_t k, void* y,
+                                         void* workspace, size_t ws_bytes, int* dev_status,
+                                         void* stream) {
+  if (!dev_status) return GQ_ERR_INVALID_ARG;
+  return gq::moe_entry<GQ_FMT_Q4_0>(gate, up, down, E, H, I, x, GQ_F16, T, ids, weights, k, y, GQ_F16,
+                                    workspace, ws_bytes, 0u, dev_status, stream, 2000000LL, 1);
 }
 
 }  // extern "C"

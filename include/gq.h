@@ -390,9 +390,8 @@ GQ_API gq_status gq_gemm_ksb(const void* W, int64_t M, int64_t K,
  * an expert in or out.)
  * workspace / ws_bytes: at least gq_moe_route_workspace_bytes(T, E) bytes
  *   (GQ_ERR_WORKSPACE otherwise), 256-byte aligned, all zero before its first
- *   use; a successful call leaves it ready for the next call of any sizes;
- *   after a call that fails, zero it again.  Calls that may run at the same
- *   time need separate workspaces.
+ *   use; every call leaves it ready for the next call of any sizes.  Calls that
+ *   may run at the same time need separate workspaces.
  * flags: GQ_ROUTE_* and GQ_GEMV_PDL.  This call and those below may always be
  *   scheduled while the previous kernel on the stream is still running: they
  *   wait for it before they read or write anything, so GQ_GEMV_PDL changes
@@ -429,9 +428,9 @@ GQ_API gq_status gq_moe_route(const void* x, int x_dtype, int64_t T, int64_t H, 
  * do not depend on scheduling.  Non-finite values of a token stay in its own
  * outputs.
  * workspace / ws_bytes: at least gq_moe_workspace_bytes(...) bytes, 256-byte
- *   aligned, all zero before its first use; a successful call leaves it ready
- *   for the next call of any sizes; after a call that fails, zero it again.
- *   Calls that may run at the same time need separate workspaces.
+ *   aligned, all zero before its first use; every call leaves it ready for the
+ *   next call of any sizes, one that reports GQ_DEV_TIMEOUT too.  Calls that may
+ *   run at the same time need separate workspaces.
  * flags: 0 or GQ_GEMV_PDL (which changes nothing, as for the router).
  * One cooperative launch with a CTA on every SM of the device: it starts when
  *   all of them are free of other kernels' shared memory (GQ_ERR_CUDA if the
@@ -449,6 +448,18 @@ GQ_API gq_status gq_moe_ksb_tiled(const void* gate, const void* up, const void* 
                                   const int32_t* ids, const float* weights, int64_t k, void* y,
                                   int y_dtype, void* workspace, size_t ws_bytes, unsigned flags,
                                   int* dev_status, void* stream);
+
+/* Self-test of the layer's bounded waits (no counterpart on the pages): runs
+ * gq_moe_q4_0_tiled (fp16 x and y) on the given buffers with a grid barrier that
+ * waits for one arrival more than there are CTAs, and a ~1 ms wait budget.  The
+ * waits run out; the kernel ORs GQ_DEV_TIMEOUT into *dev_status (required), lets
+ * the copies it did issue land and exits; y is unspecified, and the workspace is
+ * ready for the next call.  Nothing faults, traps or hangs. */
+GQ_API gq_status gq_selftest_moe_timeout(const void* gate, const void* up, const void* down, int64_t E,
+                                         int64_t H, int64_t I, const void* x, int64_t T,
+                                         const int32_t* ids, const float* weights, int64_t k, void* y,
+                                         void* workspace, size_t ws_bytes, int* dev_status,
+                                         void* stream);
 
 /* 8-bit blocks (no counterpart on the pages: the library's rule for block
  * quantization, with e4m3 floating-point codes).  A matrix of R rows of K
