@@ -50,7 +50,7 @@ EXPORTS = (
     "gq_moe_route_workspace_bytes", "gq_moe_route",
     "gq_moe_workspace_bytes", "gq_moe_q4_0_tiled", "gq_moe_ksb_tiled", "gq_selftest_moe_timeout",
     "gq_fp8_scales", "gq_quantize_fp8", "gq_dequantize_fp8",
-    "gq_gemm_fp8_workspace_bytes", "gq_gemm_fp8",
+    "gq_gemm_fp8_workspace_bytes", "gq_gemm_fp8", "gq_selftest_gemm_fp8_timeout",
 )
 
 _DTYPE_CODE = {torch.float32: GQ_F32, torch.float16: GQ_F16, torch.bfloat16: GQ_BF16}
@@ -150,6 +150,8 @@ def _load() -> ctypes.CDLL:
     L.gq_gemm_fp8.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, c_int, vp, ctypes.c_size_t, c_uint, vp,
                               vp]
     L.gq_gemm_fp8.restype = c_int
+    L.gq_selftest_gemm_fp8_timeout.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, vp, ctypes.c_size_t, vp, vp]
+    L.gq_selftest_gemm_fp8_timeout.restype = c_int
     return L
 
 
@@ -809,3 +811,20 @@ def gq_gemm_fp8(W: torch.Tensor, w_scales: torch.Tensor, X: torch.Tensor, x_scal
     _check(lib.gq_gemm_fp8(_ptr(W), _ptr(w_scales), M, K, _ptr(X), _ptr(x_scales), B, _ptr(out),
                            _DTYPE_CODE[out.dtype], ws, ws_bytes, flags, _ptr(dev_status), s), "gq_gemm_fp8")
     return out
+
+
+@_on_device
+def gq_selftest_gemm_fp8_timeout(W: torch.Tensor, w_scales: torch.Tensor, X: torch.Tensor,
+                                 x_scales: torch.Tensor, Y: torch.Tensor, dev_status: torch.Tensor,
+                                 workspace="auto", stream=None) -> None:
+    """gq_gemm_fp8 (fp32 Y [B, M]) with a first stage that never fills; the bounded waits must report
+    GQ_DEV_TIMEOUT in dev_status (see include/gq.h).  More tokens than the kernel for few takes."""
+    M, K = _fp8_pair(W, w_scales, 128, "W")
+    B, K2 = _fp8_pair(X, x_scales, 1, "X")
+    if K != K2 or Y.dtype != torch.float32 or Y.numel() != B * M:
+        raise ValueError("W is [M, K], X [B, K] and Y [B, M] in fp32")
+    s = _raw_stream(stream, X.device)
+    ws, ws_bytes, keep = _workspace("gq_gemm_fp8", workspace, _size("gq_gemm_fp8_workspace_bytes", M, K, B),
+                                    X.device, s)
+    _check(lib.gq_selftest_gemm_fp8_timeout(_ptr(W), _ptr(w_scales), M, K, _ptr(X), _ptr(x_scales), B, _ptr(Y),
+                                            ws, ws_bytes, _ptr(dev_status), s), "gq_selftest_gemm_fp8_timeout")

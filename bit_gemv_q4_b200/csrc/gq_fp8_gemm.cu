@@ -84,6 +84,7 @@ struct Args {
   long long budget;
   int64_t M;
   int B, kblocks, ytype, xrows;  // xrows: rows of an X box
+  int skip;                      // k-steps of each CTA that are never loaded (the self-test: the first), or 0
   int tma_y;                     // Y's rows are whole 16-byte pieces, so that TMA can store them
   Split sp;
   float* parts;  // [pieces][rows][BN] of cut tiles
@@ -351,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
+          if (g < a.skip) continue;
           uint8_t* st = fsm + ring + s * C::kStageBytes;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           load_box<PAIR>(st, &xmap, ks * kBK, row0, &full[s]);
@@ -359,11 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) fail();
       // every issued copy lands before shared memory is released (a pair's count in the leader)
-      for (int i = max(0, g - kStages); i < g && rank == 0; ++i)
-        if (!mbar_wait(&full[i % kStages], (i / kStages) & 1u, a.budget)) {
-          report(a.dev_status, GQ_DEV_TIMEOUT);
-          break;
-        }
+      for (int i = max(a.skip, g - kStages); i < g && rank == 0; ++i)
+        if (!mbar_wait(&full[i % kStages], (i / kStages) & 1u, kWaitBudget)) report(a.dev_status, GQ_DEV_TIMEOUT);
     }
     __syncwarp();
   } else if (warp == kEpiWarps + 1) {
@@ -538,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == kEpiWarps + 1) {
-    if (lane == 0 && !mbar_wait(done, 0, a.budget)) report(a.dev_status, GQ_DEV_TIMEOUT);
+    if (lane == 0 && !mbar_wait(done, 0, kWaitBudget)) report(a.dev_status, GQ_DEV_TIMEOUT);
     __syncwarp();
     tc_fence_after();
   }
@@ -661,20 +660,10 @@ gq_status launch_fp8(const CUtensorMap& xmap, const CUtensorMap& wmap, const CUt
                 a);
 }
 
-}  // namespace
-}  // namespace gq
-
-extern "C" {
-
-GQ_API size_t gq_gemm_fp8_workspace_bytes(int64_t M, int64_t K, int64_t B) {
-  if (M <= 0 || K <= 0 || B <= 0 || !gq::gemm_dims(M, K, B)) return 0;
-  return gq::ws_bytes_of(gq::choose(M, K, B), M, K, B);
-}
-
-GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, int64_t K, const void* X,
-                             const float* x_scales, int64_t B, void* Y, int y_dtype, void* workspace,
-                             size_t ws_bytes, unsigned flags, int* dev_status, void* stream) {
-  using namespace gq;
+// gq_gemm_fp8 with a wait budget; `skip` k-steps of each CTA are never loaded.
+gq_status gemm_fp8(const void* W, const float* w_scales, int64_t M, int64_t K, const void* X, const float* x_scales,
+                   int64_t B, void* Y, int y_dtype, void* workspace, size_t ws_bytes, unsigned flags, int* dev_status,
+                   void* stream, long long budget, int skip) {
   if (M < 0 || K < 0 || B < 0) return GQ_ERR_INVALID_ARG;
   if (!valid_act_dtype(y_dtype)) return GQ_ERR_DTYPE;
   if (flags & ~GQ_GEMV_PDL) return GQ_ERR_INVALID_ARG;
@@ -702,7 +691,8 @@ GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, in
   a.sw = w_scales;
   a.Y = Y;
   a.dev_status = dev_status;
-  a.budget = kWaitBudget;
+  a.budget = budget;
+  a.skip = skip;
   a.M = M;
   a.B = static_cast<int>(B);
   a.kblocks = static_cast<int>((K + kBK - 1) / kBK);
@@ -729,6 +719,32 @@ GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, in
   const int64_t threads = B * c.sp.tm * (128 / 4);
   return launch(fp8_sum_kernel<128>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, s, true,
                 a.parts, Y, M, a.B, static_cast<int>(B < kBM ? B : kBM), c.sp.tm, c.sp.cuts, y_dtype);
+}
+
+}  // namespace
+}  // namespace gq
+
+extern "C" {
+
+GQ_API size_t gq_gemm_fp8_workspace_bytes(int64_t M, int64_t K, int64_t B) {
+  if (M <= 0 || K <= 0 || B <= 0 || !gq::gemm_dims(M, K, B)) return 0;
+  return gq::ws_bytes_of(gq::choose(M, K, B), M, K, B);
+}
+
+GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, int64_t K, const void* X,
+                             const float* x_scales, int64_t B, void* Y, int y_dtype, void* workspace,
+                             size_t ws_bytes, unsigned flags, int* dev_status, void* stream) {
+  return gq::gemm_fp8(W, w_scales, M, K, X, x_scales, B, Y, y_dtype, workspace, ws_bytes, flags, dev_status, stream,
+                      gq::kWaitBudget, 0);
+}
+
+GQ_API gq_status gq_selftest_gemm_fp8_timeout(const void* W, const float* w_scales, int64_t M, int64_t K,
+                                              const void* X, const float* x_scales, int64_t B, void* Y,
+                                              void* workspace, size_t ws_bytes, int* dev_status, void* stream) {
+  if (!dev_status) return GQ_ERR_INVALID_ARG;
+  if (M > 0 && K > 0 && B > 0 && gq::fp8_gemv_takes(M, K, B)) return GQ_ERR_SHAPE;  // (a kernel without waits)
+  return gq::gemm_fp8(W, w_scales, M, K, X, x_scales, B, Y, GQ_F32, workspace, ws_bytes, 0u, dev_status, stream,
+                      2000000LL, 1);
 }
 
 }  // extern "C"

@@ -502,6 +502,16 @@ GQ_API gq_status gq_gemm_fp8(const void* W, const float* w_scales, int64_t M, in
                              const float* x_scales, int64_t B, void* Y, int y_dtype, void* workspace,
                              size_t ws_bytes, unsigned flags, int* dev_status, void* stream);
 
+/* Self-test of the product's bounded waits (no counterpart on the pages): runs
+ * gq_gemm_fp8 (fp32 Y) on the given buffers with a producer that never fills its
+ * first pipeline stage, and a ~1 ms wait budget.  The waits run out; the kernel
+ * ORs GQ_DEV_TIMEOUT into *dev_status (required), lets the copies it did issue
+ * land and exits; Y is unspecified.  Nothing faults, traps or hangs.  Sizes that
+ * take the kernel for few tokens, which waits for nothing, give GQ_ERR_SHAPE. */
+GQ_API gq_status gq_selftest_gemm_fp8_timeout(const void* W, const float* w_scales, int64_t M, int64_t K,
+                                              const void* X, const float* x_scales, int64_t B, void* Y,
+                                              void* workspace, size_t ws_bytes, int* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
