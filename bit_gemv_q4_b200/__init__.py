@@ -569,6 +569,25 @@ def _raw_stream(stream, device: torch.device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _device(t: torch.Tensor) -> int:
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("tensors passed to libgq must live on a CUDA device")
+    return d
+
+
+def _at(t: torch.Tensor | None, device: int) -> int | None:
+    """_ptr of a tensor that has to be on the call's device: one GPU's kernel may not read another's
+    memory."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        raise ValueError("tensors of one call must live on one CUDA device")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libgq must be contiguous")
+    return t.data_ptr() or None
+
+
 def _stream_object(stream: int, device: torch.device):
     """A raw handle as a stream that torch allocates and launches on.  (Handles 0 and 1 are the default
     stream; ExternalStream(0) would be some stream of torch's pool.)"""
@@ -598,7 +617,7 @@ def _workspace(name: str, workspace, need: int, device: torch.device, stream: in
         return ptr, size, keep
     if workspace is None:
         return None, 0, None
-    return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
+    return _at(workspace, device.index), workspace.numel() * workspace.element_size(), workspace
 
 
 def gq_moe_route_workspace_bytes(T: int, E: int) -> int:
@@ -626,7 +645,7 @@ def gq_moe_route(x: torch.Tensor, Wr: torch.Tensor, k: int, bias: torch.Tensor |
     E = Wr.shape[0]
     if bias is not None and (bias.dtype != torch.float32 or bias.numel() != E):
         raise ValueError("bias holds E fp32 values")
-    s = _raw_stream(stream, x.device)
+    d, s = _device(x), _raw_stream(stream, x.device)
     if ids is None:
         ids = _new(x, (T, k), torch.int32, s)
     elif ids.dtype != torch.int32 or ids.numel() != T * k:
@@ -636,9 +655,9 @@ def gq_moe_route(x: torch.Tensor, Wr: torch.Tensor, k: int, bias: torch.Tensor |
     elif weights.dtype != torch.float32 or weights.numel() != T * k:
         raise ValueError("weights holds T * k fp32 values")
     ws, ws_bytes, keep = _workspace("route", workspace, _size("gq_moe_route_workspace_bytes", T, E), x.device, s)
-    _check(lib.gq_moe_route(_ptr(x), _DTYPE_CODE[x.dtype], T, H, _ptr(Wr), _DTYPE_CODE[Wr.dtype], E,
-                            _ptr(bias), k, scale, _ptr(ids), _ptr(weights), ws, ws_bytes, flags,
-                            _ptr(dev_status), s), "gq_moe_route")
+    _check(lib.gq_moe_route(_at(x, d), _DTYPE_CODE[x.dtype], T, H, _at(Wr, d), _DTYPE_CODE[Wr.dtype], E,
+                            _at(bias, d), k, scale, _at(ids, d), _at(weights, d), ws, ws_bytes, flags,
+                            _at(dev_status, d), s), "gq_moe_route")
     return ids, weights
 
 
@@ -659,15 +678,15 @@ def _moe(name: str, fmt: int, gate, up, down, E: int, I: int, x: torch.Tensor, i
     gu, dn = _size("gq_tiled_bytes", fmt, E * I, H), _size("gq_tiled_bytes", fmt, E * H, I)
     if gate.numel() < gu or up.numel() < gu or down.numel() < dn:
         raise ValueError("gate, up or down is smaller than the tiled storage of E experts")
-    s = _raw_stream(stream, x.device)
+    d, s = _device(x), _raw_stream(stream, x.device)
     if out is None:
         out = _new(x, (T, H), y_dtype, s)
     elif out.dtype not in _DTYPE_CODE or out.numel() != T * H:
         raise ValueError("out holds T * H values")
     ws, ws_bytes, keep = _workspace(name, workspace, _size("gq_moe_workspace_bytes", fmt, H, I, T, k), x.device, s)
-    _check(getattr(lib, name)(_ptr(gate), _ptr(up), _ptr(down), E, H, I, _ptr(x), _DTYPE_CODE[x.dtype],
-                              T, _ptr(ids), _ptr(weights), k, _ptr(out), _DTYPE_CODE[out.dtype], ws,
-                              ws_bytes, flags, _ptr(dev_status), s), name)
+    _check(getattr(lib, name)(_at(gate, d), _at(up, d), _at(down, d), E, H, I, _at(x, d), _DTYPE_CODE[x.dtype],
+                              T, _at(ids, d), _at(weights, d), k, _at(out, d), _DTYPE_CODE[out.dtype], ws,
+                              ws_bytes, flags, _at(dev_status, d), s), name)
     return out
 
 
@@ -716,11 +735,11 @@ def gq_selftest_moe_timeout(gate: torch.Tensor, up: torch.Tensor, down: torch.Te
     gu, dn = _size("gq_tiled_bytes", GQ_FMT_Q4_0, E * I, H), _size("gq_tiled_bytes", GQ_FMT_Q4_0, E * H, I)
     if gate.numel() < gu or up.numel() < gu or down.numel() < dn:
         raise ValueError("gate, up or down is smaller than the tiled storage of E experts")
-    s = _raw_stream(stream, x.device)
+    d, s = _device(x), _raw_stream(stream, x.device)
     ws, ws_bytes, keep = _workspace("gq_moe_q4_0_tiled", workspace,
                                     _size("gq_moe_workspace_bytes", GQ_FMT_Q4_0, H, I, T, k), x.device, s)
-    _check(lib.gq_selftest_moe_timeout(_ptr(gate), _ptr(up), _ptr(down), E, H, I, _ptr(x), T, _ptr(ids),
-                                       _ptr(weights), k, _ptr(y), ws, ws_bytes, _ptr(dev_status), s),
+    _check(lib.gq_selftest_moe_timeout(_at(gate, d), _at(up, d), _at(down, d), E, H, I, _at(x, d), T, _at(ids, d),
+                                       _at(weights, d), k, _at(y, d), ws, ws_bytes, _at(dev_status, d), s),
            "gq_selftest_moe_timeout")
 
 
@@ -752,7 +771,7 @@ def gq_quantize_fp8(x: torch.Tensor, rows: int, out: torch.Tensor | None = None,
     if rows not in (1, 128):
         raise ValueError("rows is 1 or 128")
     R, K = x.shape
-    s = _raw_stream(stream, x.device)
+    d, s = _device(x), _raw_stream(stream, x.device)
     given = out is not None or scales is not None
     if out is None:
         out = _new(x, (R, K), torch.float8_e4m3fn, s)
@@ -760,8 +779,8 @@ def gq_quantize_fp8(x: torch.Tensor, rows: int, out: torch.Tensor | None = None,
         scales = _new(x, (-(-R // rows), -(-K // 128)), torch.float32, s)
     if given and _fp8_pair(out, scales, rows, "out") != (R, K):
         raise ValueError("out has another shape than x")
-    _check(lib.gq_quantize_fp8(_ptr(x), _DTYPE_CODE[x.dtype], R, K, rows, _ptr(out), _ptr(scales),
-                               _ptr(dev_status), s), "gq_quantize_fp8")
+    _check(lib.gq_quantize_fp8(_at(x, d), _DTYPE_CODE[x.dtype], R, K, rows, _at(out, d), _at(scales, d),
+                               _at(dev_status, d), s), "gq_quantize_fp8")
     return out, scales
 
 
@@ -774,12 +793,12 @@ def gq_dequantize_fp8(q: torch.Tensor, scales: torch.Tensor, rows: int, dtype=to
     R, K = _fp8_pair(q, scales, rows, "q")
     if dtype not in _DTYPE_CODE:
         raise TypeError("outputs must be float32, float16 or bfloat16")
-    s = _raw_stream(stream, q.device)
+    d, s = _device(q), _raw_stream(stream, q.device)
     if out is None:
         out = _new(q, (R, K), dtype, s)
     elif out.dtype not in _DTYPE_CODE or out.numel() != R * K:
         raise ValueError("out holds R * K values")
-    _check(lib.gq_dequantize_fp8(_ptr(q), _ptr(scales), R, K, rows, _ptr(out), _DTYPE_CODE[out.dtype],
+    _check(lib.gq_dequantize_fp8(_at(q, d), _at(scales, d), R, K, rows, _at(out, d), _DTYPE_CODE[out.dtype],
                                  s), "gq_dequantize_fp8")
     return out
 
@@ -801,15 +820,15 @@ def gq_gemm_fp8(W: torch.Tensor, w_scales: torch.Tensor, X: torch.Tensor, x_scal
         raise ValueError(f"X has {K2} columns, expected K={K}")
     if y_dtype not in _DTYPE_CODE:
         raise TypeError("outputs must be float32, float16 or bfloat16")
-    s = _raw_stream(stream, X.device)
+    d, s = _device(X), _raw_stream(stream, X.device)
     if out is None:
         out = _new(X, (B, M), y_dtype, s)
     elif out.dtype not in _DTYPE_CODE or out.numel() != B * M:
         raise ValueError("out holds B * M values")
     ws, ws_bytes, keep = _workspace("gq_gemm_fp8", workspace, _size("gq_gemm_fp8_workspace_bytes", M, K, B),
                                     X.device, s)
-    _check(lib.gq_gemm_fp8(_ptr(W), _ptr(w_scales), M, K, _ptr(X), _ptr(x_scales), B, _ptr(out),
-                           _DTYPE_CODE[out.dtype], ws, ws_bytes, flags, _ptr(dev_status), s), "gq_gemm_fp8")
+    _check(lib.gq_gemm_fp8(_at(W, d), _at(w_scales, d), M, K, _at(X, d), _at(x_scales, d), B, _at(out, d),
+                           _DTYPE_CODE[out.dtype], ws, ws_bytes, flags, _at(dev_status, d), s), "gq_gemm_fp8")
     return out
 
 
@@ -823,8 +842,8 @@ def gq_selftest_gemm_fp8_timeout(W: torch.Tensor, w_scales: torch.Tensor, X: tor
     B, K2 = _fp8_pair(X, x_scales, 1, "X")
     if K != K2 or Y.dtype != torch.float32 or Y.numel() != B * M:
         raise ValueError("W is [M, K], X [B, K] and Y [B, M] in fp32")
-    s = _raw_stream(stream, X.device)
+    d, s = _device(X), _raw_stream(stream, X.device)
     ws, ws_bytes, keep = _workspace("gq_gemm_fp8", workspace, _size("gq_gemm_fp8_workspace_bytes", M, K, B),
                                     X.device, s)
-    _check(lib.gq_selftest_gemm_fp8_timeout(_ptr(W), _ptr(w_scales), M, K, _ptr(X), _ptr(x_scales), B, _ptr(Y),
-                                            ws, ws_bytes, _ptr(dev_status), s), "gq_selftest_gemm_fp8_timeout")
+    _check(lib.gq_selftest_gemm_fp8_timeout(_at(W, d), _at(w_scales, d), M, K, _at(X, d), _at(x_scales, d), B, _at(Y, d),
+                                            ws, ws_bytes, _at(dev_status, d), s), "gq_selftest_gemm_fp8_timeout")
