@@ -748,12 +748,23 @@ def gq_fp8_scales(R: int, K: int, rows: int) -> int:
     return int(lib.gq_fp8_scales(int(R), int(K), int(rows)))
 
 
-def _fp8_pair(q: torch.Tensor, scales: torch.Tensor, rows: int, what: str):
+def _fp8_codes(q: torch.Tensor, what: str):
     if q.dim() != 2 or q.dtype != torch.float8_e4m3fn:
         raise TypeError(f"{what} must be a float8_e4m3fn matrix")
-    R, K = q.shape
-    if scales.dtype != torch.float32 or scales.numel() < -(-R // rows) * -(-K // 128):
-        raise ValueError(f"{what} needs an fp32 scale for each block of {rows} x 128 values")
+    return q.shape
+
+
+def _check_scales(scales: torch.Tensor, R: int, K: int, rows: int, what: str) -> None:
+    # (a matrix of another shape holds scales of other blocks, or has other rows between)
+    rb, kb = -(-R // rows), -(-K // 128)
+    if (scales.dtype != torch.float32 or scales.numel() != rb * kb
+            or scales.dim() == 2 and scales.shape != (rb, kb)):
+        raise ValueError(f"{what} needs one fp32 scale for each block of {rows} x 128 values, [{rb}, {kb}]")
+
+
+def _fp8_pair(q: torch.Tensor, scales: torch.Tensor, rows: int, what: str):
+    R, K = _fp8_codes(q, what)
+    _check_scales(scales, R, K, rows, what)
     return R, K
 
 
@@ -771,14 +782,15 @@ def gq_quantize_fp8(x: torch.Tensor, rows: int, out: torch.Tensor | None = None,
     if rows not in (1, 128):
         raise ValueError("rows is 1 or 128")
     R, K = x.shape
+    if out is not None and _fp8_codes(out, "out") != (R, K):
+        raise ValueError("out has another shape than x")
+    if scales is not None:
+        _check_scales(scales, R, K, rows, "out")
     d, s = _device(x), _raw_stream(stream, x.device)
-    given = out is not None or scales is not None
     if out is None:
         out = _new(x, (R, K), torch.float8_e4m3fn, s)
     if scales is None:
         scales = _new(x, (-(-R // rows), -(-K // 128)), torch.float32, s)
-    if given and _fp8_pair(out, scales, rows, "out") != (R, K):
-        raise ValueError("out has another shape than x")
     _check(lib.gq_quantize_fp8(_at(x, d), _DTYPE_CODE[x.dtype], R, K, rows, _at(out, d), _at(scales, d),
                                _at(dev_status, d), s), "gq_quantize_fp8")
     return out, scales

@@ -90,3 +90,26 @@ def test_tensors_on_the_host_are_refused(two_gpus):
             host = torch.zeros(tensors[name].shape).to(tensors[name].dtype)
             with pytest.raises(ValueError, match="CUDA device"):
                 call(**dict(tensors, **{name: host}))
+
+
+def codes(R, K):
+    return torch.zeros(R, K).to(torch.float8_e4m3fn)
+
+
+def test_scales_of_another_block_shape_are_refused():
+    W, X = codes(256, 512), codes(4, 512)
+    right, xs = torch.zeros(2, 4), torch.zeros(4, 4)
+    for bad in (torch.zeros(256, 4),        # scales of 1 x 128 blocks
+                torch.zeros(2, 5),          # rows further apart
+                torch.zeros(4, 2), torch.zeros(3, 4), torch.zeros(9), torch.zeros(2, 4).double()):
+        with pytest.raises(ValueError, match="scale"):
+            gq.gq_gemm_fp8(W, bad, X, xs)
+        with pytest.raises(ValueError, match="scale"):
+            gq.gq_dequantize_fp8(W, bad, 128)
+        with pytest.raises(ValueError, match="scale"):
+            gq.gq_quantize_fp8(torch.zeros(256, 512), 128, out=W, scales=bad)
+    for bad in (torch.zeros(1, 4), torch.zeros(5, 4), torch.zeros(2, 8), torch.zeros(4, 5)):
+        with pytest.raises(ValueError, match="scale"):
+            gq.gq_gemm_fp8(W, right, X, bad)
+    gq._fp8_pair(W, right, 128, "W")            # as they are made
+    gq._fp8_pair(W, right.view(-1), 128, "W")   # or in one row
