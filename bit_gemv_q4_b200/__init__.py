@@ -558,9 +558,15 @@ def _on_device(call):
 
 @functools.lru_cache(maxsize=4096)
 def _size(name: str, *args) -> int:
-    """A size function of the library, its answers kept (they depend on the arguments and the GPU
-    model alone)."""
+    """A size function of the library, its answers kept (they depend on the arguments alone)."""
     return int(getattr(lib, name)(*args))
+
+
+@functools.lru_cache(maxsize=4096)
+def _gemm_fp8_ws(device: int, M: int, K: int, B: int) -> int:
+    """gq_gemm_fp8_workspace_bytes on the GPU `device`, the current one; kept for each GPU, since how
+    tiles are cut depends on its number of SMs."""
+    return int(lib.gq_gemm_fp8_workspace_bytes(M, K, B))
 
 
 def _raw_stream(stream, device: torch.device) -> int:
@@ -832,13 +838,12 @@ def gq_gemm_fp8(W: torch.Tensor, w_scales: torch.Tensor, X: torch.Tensor, x_scal
         raise ValueError(f"X has {K2} columns, expected K={K}")
     if y_dtype not in _DTYPE_CODE:
         raise TypeError("outputs must be float32, float16 or bfloat16")
-    d, s = _device(X), _raw_stream(stream, X.device)
+    d, s = _device(W), _raw_stream(stream, W.device)
     if out is None:
         out = _new(X, (B, M), y_dtype, s)
     elif out.dtype not in _DTYPE_CODE or out.numel() != B * M:
         raise ValueError("out holds B * M values")
-    ws, ws_bytes, keep = _workspace("gq_gemm_fp8", workspace, _size("gq_gemm_fp8_workspace_bytes", M, K, B),
-                                    X.device, s)
+    ws, ws_bytes, keep = _workspace("gq_gemm_fp8", workspace, _gemm_fp8_ws(d, M, K, B), W.device, s)
     _check(lib.gq_gemm_fp8(_at(W, d), _at(w_scales, d), M, K, _at(X, d), _at(x_scales, d), B, _at(out, d),
                            _DTYPE_CODE[out.dtype], ws, ws_bytes, flags, _at(dev_status, d), s), "gq_gemm_fp8")
     return out
@@ -854,8 +859,7 @@ def gq_selftest_gemm_fp8_timeout(W: torch.Tensor, w_scales: torch.Tensor, X: tor
     B, K2 = _fp8_pair(X, x_scales, 1, "X")
     if K != K2 or Y.dtype != torch.float32 or Y.numel() != B * M:
         raise ValueError("W is [M, K], X [B, K] and Y [B, M] in fp32")
-    d, s = _device(X), _raw_stream(stream, X.device)
-    ws, ws_bytes, keep = _workspace("gq_gemm_fp8", workspace, _size("gq_gemm_fp8_workspace_bytes", M, K, B),
-                                    X.device, s)
+    d, s = _device(W), _raw_stream(stream, W.device)
+    ws, ws_bytes, keep = _workspace("gq_gemm_fp8", workspace, _gemm_fp8_ws(d, M, K, B), W.device, s)
     _check(lib.gq_selftest_gemm_fp8_timeout(_at(W, d), _at(w_scales, d), M, K, _at(X, d), _at(x_scales, d), B, _at(Y, d),
                                             ws, ws_bytes, _at(dev_status, d), s), "gq_selftest_gemm_fp8_timeout")

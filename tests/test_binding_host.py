@@ -113,3 +113,19 @@ def test_scales_of_another_block_shape_are_refused():
             gq.gq_gemm_fp8(W, right, X, bad)
     gq._fp8_pair(W, right, 128, "W")            # as they are made
     gq._fp8_pair(W, right.view(-1), 128, "W")   # or in one row
+
+
+def test_workspace_sizes_are_each_gpus_own(monkeypatch):
+    # two GPUs with other numbers of SMs, on which the same product is cut into other pieces
+    current = [0]
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0)
+    monkeypatch.setattr(gq.lib, "gq_gemm_fp8_workspace_bytes", lambda M, K, B: 1000 * (current[0] + 1))
+    monkeypatch.setattr(gq.lib, "gq_gemm_fp8", lambda *args: 0)
+    asked = []
+    monkeypatch.setattr(gq, "_auto_workspace", lambda name, need, device, stream: asked.append(need) or (None, None, need))
+    for gpu in (0, 1, 0, 1):
+        current[0] = gpu
+        gq.gq_gemm_fp8(OnGpu(301, 272, dtype=E4M3, gpu=gpu), OnGpu(3, 3, gpu=gpu), OnGpu(41, 272, dtype=E4M3, gpu=gpu),
+                       OnGpu(41, 3, gpu=gpu), out=OnGpu(41, 301, gpu=gpu))
+    assert asked == [1000, 2000, 1000, 2000]
