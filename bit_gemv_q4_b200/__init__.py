@@ -569,17 +569,17 @@ def _gemm_fp8_ws(device: int, M: int, K: int, B: int) -> int:
     return int(lib.gq_gemm_fp8_workspace_bytes(M, K, B))
 
 
-def _raw_stream(stream, device: torch.device) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _device(t: torch.Tensor) -> int:
+def _where(t: torch.Tensor, stream):
+    """Of a call whose tensors are on t's device: (device, raw stream, and that stream again if it is
+    not the current one)."""
     d = t.get_device()
     if d < 0:
         raise ValueError("tensors passed to libgq must live on a CUDA device")
-    return d
+    current = torch._C._cuda_getCurrentRawStream(d)
+    if stream is None:
+        return d, current, None
+    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return d, s, None if s == current else s
 
 
 def _at(t: torch.Tensor | None, device: int) -> int | None:
@@ -602,13 +602,13 @@ def _stream_object(stream: int, device: torch.device):
     return torch.cuda.ExternalStream(stream, device=device)
 
 
-def _new(like: torch.Tensor, shape, dtype, stream: int) -> torch.Tensor:
-    """An output of a call on `stream`, in memory of that stream: what the current stream has freed it
+def _new(like: torch.Tensor, shape, dtype, named: int | None) -> torch.Tensor:
+    """An output of a call, in memory of the stream that it names: what the current stream has freed it
     may still be reading.  (Use on another stream is the caller's to order, and to record before the
     tensor is dropped.)"""
-    if stream == torch._C._cuda_getCurrentRawStream(like.device.index):
+    if named is None:
         return like.new_empty(shape, dtype=dtype)
-    with torch.cuda.stream(_stream_object(stream, like.device)):
+    with torch.cuda.stream(_stream_object(named, like.device)):
         return like.new_empty(shape, dtype=dtype)
 
 
@@ -651,13 +651,13 @@ def gq_moe_route(x: torch.Tensor, Wr: torch.Tensor, k: int, bias: torch.Tensor |
     E = Wr.shape[0]
     if bias is not None and (bias.dtype != torch.float32 or bias.numel() != E):
         raise ValueError("bias holds E fp32 values")
-    d, s = _device(x), _raw_stream(stream, x.device)
+    d, s, named = _where(x, stream)
     if ids is None:
-        ids = _new(x, (T, k), torch.int32, s)
+        ids = _new(x, (T, k), torch.int32, named)
     elif ids.dtype != torch.int32 or ids.numel() != T * k:
         raise ValueError("ids holds T * k int32 values")
     if weights is None:
-        weights = _new(x, (T, k), torch.float32, s)
+        weights = _new(x, (T, k), torch.float32, named)
     elif weights.dtype != torch.float32 or weights.numel() != T * k:
         raise ValueError("weights holds T * k fp32 values")
     ws, ws_bytes, keep = _workspace("route", workspace, _size("gq_moe_route_workspace_bytes", T, E), x.device, s)
@@ -684,9 +684,9 @@ def _moe(name: str, fmt: int, gate, up, down, E: int, I: int, x: torch.Tensor, i
     gu, dn = _size("gq_tiled_bytes", fmt, E * I, H), _size("gq_tiled_bytes", fmt, E * H, I)
     if gate.numel() < gu or up.numel() < gu or down.numel() < dn:
         raise ValueError("gate, up or down is smaller than the tiled storage of E experts")
-    d, s = _device(x), _raw_stream(stream, x.device)
+    d, s, named = _where(x, stream)
     if out is None:
-        out = _new(x, (T, H), y_dtype, s)
+        out = _new(x, (T, H), y_dtype, named)
     elif out.dtype not in _DTYPE_CODE or out.numel() != T * H:
         raise ValueError("out holds T * H values")
     ws, ws_bytes, keep = _workspace(name, workspace, _size("gq_moe_workspace_bytes", fmt, H, I, T, k), x.device, s)
@@ -741,7 +741,7 @@ def gq_selftest_moe_timeout(gate: torch.Tensor, up: torch.Tensor, down: torch.Te
     gu, dn = _size("gq_tiled_bytes", GQ_FMT_Q4_0, E * I, H), _size("gq_tiled_bytes", GQ_FMT_Q4_0, E * H, I)
     if gate.numel() < gu or up.numel() < gu or down.numel() < dn:
         raise ValueError("gate, up or down is smaller than the tiled storage of E experts")
-    d, s = _device(x), _raw_stream(stream, x.device)
+    d, s, named = _where(x, stream)
     ws, ws_bytes, keep = _workspace("gq_moe_q4_0_tiled", workspace,
                                     _size("gq_moe_workspace_bytes", GQ_FMT_Q4_0, H, I, T, k), x.device, s)
     _check(lib.gq_selftest_moe_timeout(_at(gate, d), _at(up, d), _at(down, d), E, H, I, _at(x, d), T, _at(ids, d),
@@ -754,22 +754,22 @@ def gq_fp8_scales(R: int, K: int, rows: int) -> int:
     return int(lib.gq_fp8_scales(int(R), int(K), int(rows)))
 
 
-def _fp8_codes(q: torch.Tensor, what: str):
-    if q.dim() != 2 or q.dtype != torch.float8_e4m3fn:
+def _check_codes(q: torch.Tensor, what: str) -> None:
+    if q.dtype != torch.float8_e4m3fn or q.dim() != 2:
         raise TypeError(f"{what} must be a float8_e4m3fn matrix")
-    return q.shape
 
 
 def _check_scales(scales: torch.Tensor, R: int, K: int, rows: int, what: str) -> None:
     # (a matrix of another shape holds scales of other blocks, or has other rows between)
     rb, kb = -(-R // rows), -(-K // 128)
-    if (scales.dtype != torch.float32 or scales.numel() != rb * kb
-            or scales.dim() == 2 and scales.shape != (rb, kb)):
+    if scales.dtype != torch.float32 or (scales.shape != (rb, kb)
+                                         and (scales.dim() == 2 or scales.numel() != rb * kb)):
         raise ValueError(f"{what} needs one fp32 scale for each block of {rows} x 128 values, [{rb}, {kb}]")
 
 
 def _fp8_pair(q: torch.Tensor, scales: torch.Tensor, rows: int, what: str):
-    R, K = _fp8_codes(q, what)
+    _check_codes(q, what)
+    R, K = q.shape
     _check_scales(scales, R, K, rows, what)
     return R, K
 
@@ -788,15 +788,17 @@ def gq_quantize_fp8(x: torch.Tensor, rows: int, out: torch.Tensor | None = None,
     if rows not in (1, 128):
         raise ValueError("rows is 1 or 128")
     R, K = x.shape
-    if out is not None and _fp8_codes(out, "out") != (R, K):
-        raise ValueError("out has another shape than x")
+    if out is not None:
+        _check_codes(out, "out")
+        if out.shape != x.shape:
+            raise ValueError("out has another shape than x")
     if scales is not None:
         _check_scales(scales, R, K, rows, "out")
-    d, s = _device(x), _raw_stream(stream, x.device)
+    d, s, named = _where(x, stream)
     if out is None:
-        out = _new(x, (R, K), torch.float8_e4m3fn, s)
+        out = _new(x, (R, K), torch.float8_e4m3fn, named)
     if scales is None:
-        scales = _new(x, (-(-R // rows), -(-K // 128)), torch.float32, s)
+        scales = _new(x, (-(-R // rows), -(-K // 128)), torch.float32, named)
     _check(lib.gq_quantize_fp8(_at(x, d), _DTYPE_CODE[x.dtype], R, K, rows, _at(out, d), _at(scales, d),
                                _at(dev_status, d), s), "gq_quantize_fp8")
     return out, scales
@@ -811,9 +813,9 @@ def gq_dequantize_fp8(q: torch.Tensor, scales: torch.Tensor, rows: int, dtype=to
     R, K = _fp8_pair(q, scales, rows, "q")
     if dtype not in _DTYPE_CODE:
         raise TypeError("outputs must be float32, float16 or bfloat16")
-    d, s = _device(q), _raw_stream(stream, q.device)
+    d, s, named = _where(q, stream)
     if out is None:
-        out = _new(q, (R, K), dtype, s)
+        out = _new(q, (R, K), dtype, named)
     elif out.dtype not in _DTYPE_CODE or out.numel() != R * K:
         raise ValueError("out holds R * K values")
     _check(lib.gq_dequantize_fp8(_at(q, d), _at(scales, d), R, K, rows, _at(out, d), _DTYPE_CODE[out.dtype],
@@ -838,9 +840,9 @@ def gq_gemm_fp8(W: torch.Tensor, w_scales: torch.Tensor, X: torch.Tensor, x_scal
         raise ValueError(f"X has {K2} columns, expected K={K}")
     if y_dtype not in _DTYPE_CODE:
         raise TypeError("outputs must be float32, float16 or bfloat16")
-    d, s = _device(W), _raw_stream(stream, W.device)
+    d, s, named = _where(W, stream)
     if out is None:
-        out = _new(X, (B, M), y_dtype, s)
+        out = _new(X, (B, M), y_dtype, named)
     elif out.dtype not in _DTYPE_CODE or out.numel() != B * M:
         raise ValueError("out holds B * M values")
     ws, ws_bytes, keep = _workspace("gq_gemm_fp8", workspace, _gemm_fp8_ws(d, M, K, B), W.device, s)
@@ -859,7 +861,7 @@ def gq_selftest_gemm_fp8_timeout(W: torch.Tensor, w_scales: torch.Tensor, X: tor
     B, K2 = _fp8_pair(X, x_scales, 1, "X")
     if K != K2 or Y.dtype != torch.float32 or Y.numel() != B * M:
         raise ValueError("W is [M, K], X [B, K] and Y [B, M] in fp32")
-    d, s = _device(W), _raw_stream(stream, W.device)
+    d, s, named = _where(W, stream)
     ws, ws_bytes, keep = _workspace("gq_gemm_fp8", workspace, _gemm_fp8_ws(d, M, K, B), W.device, s)
     _check(lib.gq_selftest_gemm_fp8_timeout(_at(W, d), _at(w_scales, d), M, K, _at(X, d), _at(x_scales, d), B, _at(Y, d),
                                             ws, ws_bytes, _at(dev_status, d), s), "gq_selftest_gemm_fp8_timeout")
