@@ -14,6 +14,13 @@ that the router, the expert layer and the 8-bit calls make on a named stream
 are memory of that stream: order later use on other streams after it
 (Stream.wait_stream), and record such use (Tensor.record_stream) if the tensor
 may be dropped before it has happened.
+
+`workspace="auto"` of those calls is a buffer kept for each call, device and
+stream.  A call that torch.cuda.graph captures gets one of its own from the
+graph's memory, and every replay clears it before the call; with a workspace
+tensor given (zeroed once, one for calls that do not overlap) nothing is
+cleared.  A capture made without torch.cuda.graph needs outputs and workspaces
+that the program keeps.
 """
 from __future__ import annotations
 

@@ -37,13 +37,13 @@
 // For fewer than 128 tokens only the rows that exist are loaded; the other
 // lanes hold garbage that nothing reads.
 //
-// Measured: 4096 tokens x 11008 x 4096 (fp32 out), 204 us, 1.81 PFLOP/s (240 us
-// in a long loop, at 1600 MHz under the power limit).  Loads and MMAs alone take
-// 113 us; with sixteen promoting warps the whole took 212, without the reads of
-// tensor memory 197, without the MMAs 186, without either and without loads 172:
-// the handshakes and sums of each k-step bound it.  So they do 500 tokens x 4096
-// x 11008, 35 us, and 37 x 11000 x 4096, 16.1 us: 0.38 us a k-step, 0.37 without
-// loads, MMAs and reads.
+// Measured: 4096 tokens x 11008 x 4096 (fp32 out), 209 us, 1.77 PFLOP/s, in short
+// runs and 238 us in a long loop, at 1610 MHz under the power limit.  Loads and
+// MMAs alone take 113 us; with sixteen promoting warps the whole took 212, without
+// the reads of tensor memory 197, without the MMAs 186, without either and without
+// loads 172: the handshakes and sums of each k-step bound it.  So they do 500
+// tokens x 4096 x 11008, 35 us (39 in a long loop), and 37 x 11000 x 4096, 16.3 us:
+// 0.38 us a k-step, 0.37 without loads, MMAs and reads.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -577,11 +577,13 @@ __global__ void __launch_bounds__(256) fp8_sum_kernel(const float* parts, void* 
 // and writing and reading them an eighth for each of 128 rows.  A pair's 256 x
 // 256 tile takes 1.55 units a k-step, on half as many SM pairs.  The plan with
 // the shortest longest CTA is taken.
-// Measured, 128 x 128 (uncut) against pairs: 500 tokens x 4096 x 4096, 17.6 and
-// 23.6 us; 1000 tokens, 30.9 and 24.9; 200 tokens x 11008 x 4096, 39.3 and 24.1;
-// 2048 tokens, 131 and 99.5.  Whole tiles against pieces: 128 tokens x 4096 x
-// 11008, 35.2 and 22.7 (four); 300 tokens, 35.9 and 42.3 (three); 256 tokens x
-// 2048 x 2048, 10.3 and 14.3 (two).
+// Measured, 128 x 128 (uncut) against pairs: 500 tokens x 4096 x 4096, 16.2 and
+// 21.0 us; 1000 tokens, 29.0 and 22.0; 200 tokens x 11008 x 4096, 28.8 and 22.0;
+// 500 tokens, 45 and 42 (where the rule takes the former); 2048 tokens, 143 and
+// 100.  Whole tiles against pieces: 128 tokens x 4096 x 11008, 37 and 18.2 (four);
+// 300 tokens, 36.4 and 34.3 (three; the rule takes whole ones); 256 tokens x 2048 x
+// 2048, 9.6 and 10.8 (two); 64 tokens x 4096 x 4096, 15.2 and 10.6 (four); 37
+// tokens x 11000 x 4096, 16.3 and 17.0 (three).
 struct Choice {
   int bn;
   bool pair;

@@ -5,8 +5,8 @@
 // ids[t][j], with G, U, D decoded from Q4_0 blocks ("GGUF 量化内幕 第4章" 4.3:
 // d * (code - 8)) or super-blocks ("GGUF K-quants" 套娃, step 5).  The taken
 // experts' weights set the time (the decode setting of the TurboQuant W4A8
-// post, section 2.3): every byte of them is read once, and nothing else is
-// large.
+// post, section 2.3): every byte of them is read once for each segment of the
+// expert's tokens (below), and nothing else is large.
 //
 // One cooperative launch of one CTA per SM in three phases with a grid barrier
 // between them: gate and up with the activation (h, fp32, in the workspace),
@@ -37,11 +37,19 @@
 // to the low mantissa bits of 1024, from which 1032 is subtracted, or stays in
 // the high nibble (1024 + 16 code, times 1/16, minus 72).  The warp MMA's eight
 // columns are the expert's tokens.  Activations are scaled by a power of two
-// for each token so that the largest lies in [2^14, 2^15); 16-bit inputs then
-// enter as one fp16 column, exact down to 2^-39 of the largest.  fp32 inputs,
-// and h when y is fp32, enter as two columns (the fp16 value and the fp16
-// remainder: 22 bits); for a 16-bit y, h enters as one column, rounded to 11
-// bits, which is below the rounding of y.  Products are exact, sums are fp32.
+// for each token so that the largest lies in [2^14, 2^15).  fp16 x needs no scale
+// and enters as one exact column.  bf16 x enters as one column, too: exact above
+// 2^-31 of the largest, and to half of fp16's smallest step, 2^-39 of the largest,
+// below.  fp32 inputs, and h when y is fp32, enter as two columns (the fp16 value
+// and the fp16 remainder: 22 bits, and the same 2^-39).  For a 16-bit y, h enters
+// as one column, rounded to 11 bits.  For bf16 y that is well below y's own
+// rounding (8 bits).  For fp16 y it is the same step, once for each term of the
+// sum: the error against 64 bits of one token on six of 64 experts is 2.8e-4 of
+// the values, 2.1e-4 with y's rounding alone.  Two columns would end that; they
+// took 24.9 us for 24.3 there, 57.1 for 55.6 on two of eight 4096 x 11008 experts
+// and 90.7 for 87.1 at 32 tokens (with the router), since half as many tokens fit
+// a segment.  A scale is 2^114 at most, so values are cut to 2^-138 at the least.
+// Products are exact, sums are fp32.
 //
 // Measured, weights cold: one token on two of eight 4096 x 11008 experts, 152 MB
 // in 47.5 us: 16 and 9.5 us are the two streams (6.2 and 5.2 TB/s), 5 the plan
@@ -149,7 +157,7 @@ struct Plan {
   // in dynamic shared memory
   Seg* seg[2];                         // [pairs] of each phase
   short* order;                        // [pairs] slot -> pair
-  float* weight;                       // [pairs] 0 where the id names nothing
+  float* weight;                       // [pairs]; used only where the id names an expert
   int* id;                             // [pairs, rounded up to 4] the expert, or kNobody
 };
 
@@ -572,7 +580,7 @@ template <bool GATE_UP>
 __device__ __forceinline__ unsigned put(const MoeArgs& a, const Phase& ph, const Plan& pl, const Seg& sg, int c,
                                         int row, float v, float up) {
   if constexpr (GATE_UP) {
-    // within 2 steps; a quotient by an infinity is zero
+    // within 2 steps; a quotient by 2^126 or more is zero (silu of less than -87)
     const float h = __fdividef(v, 1.0f + expf(-v)) * up;
     __stcg(a.h + static_cast<int64_t>(sg.slot0 + c) * (ph.groups * 16) + row, h);
     return __float_as_uint(h) & 0x7FFFFFFFu;
@@ -973,8 +981,10 @@ size_t shape_smem(MoeArgs& a) {
   size_t tab = 0, b = 0;
   // one token: a column (or two) for each slot, if all of them fit beside the parts
   const size_t slots = static_cast<size_t>(a.k) * padded(a.ph[1].K) * 2 * (a.ph[1].two ? 2 : 1);
-  // and if they are few enough for every CTA to read them all: 16384 values
-  // took 2 us less than a third phase, 22016 took 2 us more
+  // and if they are few enough for every CTA to read them all: up to 16384 values
+  // no measured shape loses by it.  Against a third phase, in us with the router: 8 x 2048 values 46.9 and 49.6, 16 x 1024 (on rows
+  // of 512) 23.6 and 23.6, 2 x 11008 54.4 and 55.5; 16 x 2048 on rows of 2048 48.0
+  // and 49.7, but on rows of 512 29.7 and 26.3; 4 x 11008 81.4 and 79.4
   a.single = a.T == 1 && a.k * padded(a.ph[1].K) <= 16384 &&
              slots + kWarps * 2 * 16 * 2 * sizeof(float) <= left;
   for (int f = 0; f < 2; ++f) {
