@@ -40,22 +40,19 @@
 // for each token so that the largest lies in [2^14, 2^15).  fp16 x needs no scale
 // and enters as one exact column.  bf16 x enters as one column, too: exact above
 // 2^-31 of the largest, and to half of fp16's smallest step, 2^-39 of the largest,
-// below.  fp32 inputs, and h when y is fp32, enter as two columns (the fp16 value
-// and the fp16 remainder: 22 bits, and the same 2^-39).  For a 16-bit y, h enters
-// as one column, rounded to 11 bits.  For bf16 y that is well below y's own
-// rounding (8 bits).  For fp16 y it is the same step, once for each term of the
-// sum: the error against 64 bits of one token on six of 64 experts is 2.8e-4 of
-// the values, 2.1e-4 with y's rounding alone.  Two columns would end that; they
-// took 24.9 us for 24.3 there, 57.1 for 55.6 on two of eight 4096 x 11008 experts
-// and 90.7 for 87.1 at 32 tokens (with the router), since half as many tokens fit
-// a segment.  A scale is 2^114 at most, so values are cut to 2^-138 at the least.
-// Products are exact, sums are fp32.
+// below.  fp32 x, and h always, enter as two columns (the fp16 value and the fp16
+// remainder: 22 bits, and the same 2^-39).  (h as one column, 11 bits, let 40 % of
+// the fp16 and 10 % of the bf16 outputs be rounded to another value than 64 bits
+// give; it took 24.5 us for 25.0 with one token on six of 64 experts, 56.2 for 57.5
+// on two of eight 4096 x 11008 ones, and 87.2 for 91.5 at 32 tokens, where twice as
+// many fit a segment, all with the router.)  A scale is 2^114 at most, so values
+// are cut to 2^-138 at the least.  Products are exact, sums are fp32.
 //
 // Measured, weights cold: one token on two of eight 4096 x 11008 experts, 152 MB
-// in 47.5 us: 16 and 9.5 us are the two streams (6.2 and 5.2 TB/s), 5 the plan
-// and x, 5 h, 12 joins, barriers, the sum and the launch.  32 tokens on 64
-// experts of 2048 x 1408, 299 MB in 80 us; one token on six of them, 29 MB in
-// 18.4 us.  Bound by memory while weights stream, by the latency of the steps
+// in 49 us: about 16 and 10 are the two streams (6.2 and 5.1 TB/s), 5 the plan
+// and x, 6 h, 12 joins, barriers, the sum and the launch.  32 tokens on 64
+// experts of 2048 x 1408, 299 MB in 85 us; one token on six of them, 29 MB in
+// 18.9 us.  Bound by memory while weights stream, by the latency of the steps
 // between elsewhere (where warps wait longest for instructions, all of them new).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -104,10 +101,16 @@ struct Phase {
   int stages;               // of a row group
   Div by_groups, by_item, by_vecs;  // row groups, stages of an item, 8-value pieces of a padded row
   int64_t group_bytes;
-  int two;                  // two columns for each token
+  int two;                  // two columns for each token (always so for down)
   int cap;                  // tokens of a segment at most, a power of two
   int part;                 // floats of a part in the table
 };
+
+// Down's activations are two terms each, whatever the types; x's are where x is fp32.
+template <bool GATE_UP>
+__device__ __forceinline__ bool two_terms(const Phase& ph) {
+  return !GATE_UP || ph.two;
+}
 
 struct MoeArgs {
   Phase ph[2];
@@ -313,7 +316,7 @@ __host__ __device__ __forceinline__ int padded(int K) { return (K + 255) & ~255;
 // product of all slots.
 template <bool GATE_UP>
 __device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& pl, int seg0, int segs) {
-  const bool single = !GATE_UP && a.single;
+  const bool single = !GATE_UP && a.single, two = two_terms<GATE_UP>(ph);
   const int type = GATE_UP ? a.xtype : GQ_F32;
   const bool find = GATE_UP && type != GQ_F16;
   const int i = threadIdx.x / kMaxCols, c = threadIdx.x % kMaxCols;
@@ -333,9 +336,9 @@ __device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& 
     for (int j = 0; j < i; ++j) {
       const int n = pl.seg[!GATE_UP][seg0 + j].n;
       before += n;
-      off += col_pitch(ph.two ? 2 * n : n) * padded(ph.K) * 2;
+      off += col_pitch(two ? 2 * n : n) * padded(ph.K) * 2;
     }
-    pl.col[before + c] = Col{row, mul, off + (ph.two ? 2 * c : c) * 64, col_pitch(ph.two ? 2 * sg.n : sg.n)};
+    pl.col[before + c] = Col{row, mul, off + (two ? 2 * c : c) * 64, col_pitch(two ? 2 * sg.n : sg.n)};
     pl.top[before + c] = top;
     pl.hmax[i][c] = 0u;
     if (c == 0) pl.boff[i] = off;
@@ -393,7 +396,7 @@ __device__ __forceinline__ void load_b(const MoeArgs& a, const Phase& ph, Plan& 
       }
     };
     store(d);
-    if (ph.two) store(d + 64);
+    if (two) store(d + 64);
   };
   put8(first, threadIdx.x);
   for (int i0 = kThreads; i0 < nvec; i0 += kThreads) put8(fetch(i0 + threadIdx.x), i0 + threadIdx.x);
@@ -600,15 +603,16 @@ template <bool GATE_UP>
 __device__ __forceinline__ void finish(const MoeArgs& a, const Phase& ph, const Plan& pl, const Seg& sg, int local,
                                        int g, const float acc[4], const float gate[4], unsigned top[2]) {
   const int lane = threadIdx.x & 31, g8 = lane >> 2, t = lane & 3;
+  const bool two = two_terms<GATE_UP>(ph);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int c = ph.two ? t : 2 * t + i;
-    if (c < sg.n && !(ph.two && i)) {
+    const int c = two ? t : 2 * t + i;
+    if (c < sg.n && !(two && i)) {
       const float f = pl.inv[local][c];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const float v = ph.two ? acc[2 * half] + acc[2 * half + 1] : acc[2 * half + i];
-        const float w = ph.two ? gate[2 * half] + gate[2 * half + 1] : gate[2 * half + i];
+        const float v = two ? acc[2 * half] + acc[2 * half + 1] : acc[2 * half + i];
+        const float w = two ? gate[2 * half] + gate[2 * half + 1] : gate[2 * half + i];
         const unsigned m = put<GATE_UP>(a, ph, pl, sg, c, 16 * g + g8 + 8 * half, (GATE_UP ? w : v) * f, v * f);
         top[i] = max(top[i], m);
       }
@@ -655,7 +659,7 @@ struct Work {
     int bytes = 0;
     while (r < r1 && st.segs < kMaxSegs) {
       const int s = st.seg0 + st.segs;
-      bytes += col_pitch(ph.two ? 2 * pl.seg[!GATE_UP][s].n : pl.seg[!GATE_UP][s].n) * padded(ph.K) * 2;
+      bytes += col_pitch(two_terms<GATE_UP>(ph) ? 2 * pl.seg[!GATE_UP][s].n : pl.seg[!GATE_UP][s].n) * padded(ph.K) * 2;
       if (bytes > a.bbytes && st.segs) break;  // (one segment always fits)
       r = min(r1, (s + 1) * ph.groups);
       ++st.segs;
@@ -769,25 +773,26 @@ __device__ __forceinline__ void join_parts(const MoeArgs& a, const Phase& ph, Pl
                                            unsigned tu, bool cut, const Seg& sg, int local, int g, unsigned u1,
                                            unsigned end) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool two = two_terms<GATE_UP>(ph);
   __syncthreads();  // the parts are there; nobody reads B any more
   if (cut) {
-    const int pitch = col_pitch(ph.two ? 2 * sg.n : sg.n);
+    const int pitch = col_pitch(two ? 2 * sg.n : sg.n);
     const int row = lane & 15, half = lane >> 4;
     unsigned tops = 0;  // lane c: token c's largest
     // two tokens at a time, a lane for each row
 #pragma unroll 1  // (run through once, so that each instruction has to be fetched: short code is faster)
     for (int c0 = 0; c0 < sg.n; c0 += 2) {
-      const int c = min(c0 + half, sg.n - 1), at = row * pitch + (ph.two ? 2 * c : c), up = 16 * pitch;
+      const int c = min(c0 + half, sg.n - 1), at = row * pitch + (two ? 2 * c : c), up = 16 * pitch;
       const float* d = first_part() + at;
-      float v = ph.two ? d[0] + d[1] : d[0], u = 0.f;
-      if (GATE_UP) u = ph.two ? d[up] + d[up + 1] : d[up];
+      float v = two ? d[0] + d[1] : d[0], u = 0.f;
+      if (GATE_UP) u = two ? d[up] + d[up + 1] : d[up];
       d = later_part(a, ph, warp + 1) + at;
       unsigned begin = u1;
       for (unsigned w = warp + 1; begin < end; ++w) {
         const unsigned next = tu * (w + 1) / kWarps;
         if (next > begin) {  // (a warp without stages has no part)
-          v += ph.two ? d[0] + d[1] : d[0];
-          if (GATE_UP) u += ph.two ? d[up] + d[up + 1] : d[up];
+          v += two ? d[0] + d[1] : d[0];
+          if (GATE_UP) u += two ? d[up] + d[up + 1] : d[up];
         }
         begin = next;
         d += ph.part;
@@ -835,8 +840,10 @@ __device__ __forceinline__ void run_phase(const MoeArgs& a, Plan& pl, Work<FMT, 
     while (u < u1) {
       sg = pl.seg[!GATE_UP][s];
       const int ue = min(u1, base + ph.groups * all);
-      switch (col_pitch(ph.two ? 2 * sg.n : sg.n)) {
-        case 1: stream<FMT, 1, GATE_UP>(a, ph, pl, wk, sg, s - st.seg0, u, ue, g, k, whole, slot); break;
+      switch (col_pitch(two_terms<GATE_UP>(ph) ? 2 * sg.n : sg.n)) {
+        case 1:
+          if constexpr (GATE_UP) stream<FMT, 1, GATE_UP>(a, ph, pl, wk, sg, s - st.seg0, u, ue, g, k, whole, slot);
+          break;  // (down has two columns at least)
         case 2: stream<FMT, 2, GATE_UP>(a, ph, pl, wk, sg, s - st.seg0, u, ue, g, k, whole, slot); break;
         case 4: stream<FMT, 4, GATE_UP>(a, ph, pl, wk, sg, s - st.seg0, u, ue, g, k, whole, slot); break;
         default: stream<FMT, 8, GATE_UP>(a, ph, pl, wk, sg, s - st.seg0, u, ue, g, k, whole, slot);
@@ -979,12 +986,14 @@ size_t shape_smem(MoeArgs& a) {
   const size_t plan = (static_cast<size_t>(pairs) * (2 * sizeof(Seg) + 2 + 8) + 12 + 15) & ~size_t(15);
   const size_t left = kDynSmem - kRingBytes - plan;
   size_t tab = 0, b = 0;
-  // one token: a column (or two) for each slot, if all of them fit beside the parts
-  const size_t slots = static_cast<size_t>(a.k) * padded(a.ph[1].K) * 2 * (a.ph[1].two ? 2 : 1);
-  // and if they are few enough for every CTA to read them all: up to 16384 values
-  // no measured shape loses by it.  Against a third phase, in us with the router: 8 x 2048 values 46.9 and 49.6, 16 x 1024 (on rows
-  // of 512) 23.6 and 23.6, 2 x 11008 54.4 and 55.5; 16 x 2048 on rows of 2048 48.0
-  // and 49.7, but on rows of 512 29.7 and 26.3; 4 x 11008 81.4 and 79.4
+  // one token: two columns for each slot, if all of them fit beside the parts
+  const size_t slots = static_cast<size_t>(a.k) * padded(a.ph[1].K) * 2 * 2;
+  // and if they are few enough for every CTA to read them all.  It saves a barrier
+  // and costs the most where there are few rows.  Against a third phase, in us with
+  // the router: 6 x 1408 values on 2048 rows 25.3 and 27.4; 8 x 2048 on 4096 rows
+  // 48.4 and 49.8; 16 x 1024 on 1024 rows 26.8 and 26.8, on 512 24.6 and 23.5; 2 x
+  // 11008 on 4096 rows 55.9 and 56.8, on 512 25.2 and 23.5; 16 x 1408 on 512 27.4 and
+  // 24.3.
   a.single = a.T == 1 && a.k * padded(a.ph[1].K) <= 16384 &&
              slots + kWarps * 2 * 16 * 2 * sizeof(float) <= left;
   for (int f = 0; f < 2; ++f) {
@@ -1081,7 +1090,7 @@ gq_status moe_entry(const void* gate, const void* up, const void* down, int64_t 
     return ph;
   };
   a.ph[0] = phase(gate, up, I, H, x_dtype == GQ_F32);
-  a.ph[1] = phase(down, nullptr, H, I, y_dtype == GQ_F32);
+  a.ph[1] = phase(down, nullptr, H, I, true);
   a.by_grid = make_div(static_cast<unsigned>(sm_count()));
   a.x = x;
   a.ids = ids;

@@ -418,17 +418,15 @@ GQ_API gq_status gq_moe_route(const void* x, int x_dtype, int64_t T, int64_t H, 
  *      other value outside [0, E) counts as -1 and sets GQ_DEV_RANGE.  A token
  *      may name an expert more than once.  A token that names none gets zeros.
  *   weights: [T][k] fp32.
- * Only the experts that some token names are read, each once for up to 8
- * tokens (4 where a token takes two fp16 terms, fewer for wide matrices).
+ * Only the experts that some token names are read: gate and up once for up to 8
+ * of an expert's tokens (4 with fp32 x), down once for up to 4; fewer for wide
+ * matrices.
  * Arithmetic: products of exact codes with activations in fp16, scaled by a
  * power of two for each token; fp32 accumulation; one rounding to y_dtype.
  *   fp16 x is exact.  bf16 x is exact above 2^-31 of the token's largest |x|; the
  *     rest has an error of at most 2^-39 of that largest.
- *   fp32 x, and the activation h between the products when y is fp32, are two
- *     fp16 terms: an error of 2^-22 of each value and 2^-39 of the largest.
- *   for a 16-bit y, h is one fp16 value: an error of 2^-11 of each value and 2^-39
- *     of the largest.  (That is no more than the rounding of an fp16 y for each
- *     term of its sum, but more than it for a sum whose terms cancel.)
+ *   fp32 x, and the activation between the products, are two fp16 terms: an error
+ *     of 2^-22 of each value and 2^-39 of the largest.
  *   Scales end at 2^114: a token's absolute errors are 2^-139 at the least.
  * Results do not depend on scheduling.  Non-finite values of a token stay in its
  * own outputs.
