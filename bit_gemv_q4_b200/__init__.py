@@ -10,17 +10,16 @@ PyTorch is used only to allocate device memory and to name the stream.
 
 `stream` (a torch stream or a raw handle) names the stream of one call, the
 current one otherwise; what the call reads has to be ready on it.  The outputs
-that the router, the expert layer and the 8-bit calls make on a named stream
-are memory of that stream: order later use on other streams after it
-(Stream.wait_stream), and record such use (Tensor.record_stream) if the tensor
-may be dropped before it has happened.
+that a call makes on a named stream are memory of that stream: order later use
+on other streams after it (Stream.wait_stream), and record such use
+(Tensor.record_stream) if the tensor may be dropped before it has happened.
 
-`workspace="auto"` of those calls is a buffer kept for each call, device and
-stream.  A call that torch.cuda.graph captures gets one of its own from the
-graph's memory, and every replay clears it before the call; with a workspace
-tensor given (zeroed once, one for calls that do not overlap) nothing is
-cleared.  A capture made without torch.cuda.graph needs outputs and workspaces
-that the program keeps.
+`workspace="auto"` of the router, the expert layer and the 8-bit product is a
+buffer kept for each call, device and stream.  A call that torch.cuda.graph
+captures gets one of its own from the graph's memory, and every replay clears it
+before the call; with a workspace tensor given (zeroed once, one for calls that
+do not overlap) nothing is cleared.  A capture made without torch.cuda.graph
+needs outputs and workspaces that the program keeps.
 """
 from __future__ import annotations
 
@@ -191,6 +190,23 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _stream_object(stream: int, device: torch.device):
+    """A raw handle as a stream that torch allocates and launches on.  (Handles 0 and 1 are the default
+    stream; ExternalStream(0) would be some stream of torch's pool.)"""
+    if stream in (0, 1):
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(stream, device=device)
+
+
+def _make(make, shape, dtype, device: torch.device, stream) -> torch.Tensor:
+    """torch.empty or torch.zeros of a call's output or workspace, on the call's stream: what the current
+    stream has freed it may still be reading, and a workspace has to be clear before the call."""
+    if stream is None or device.type != "cuda":
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_stream_object(_stream(stream), device)):
+        return make(shape, dtype=dtype, device=device)
+
+
 def _ptr(t: torch.Tensor | None) -> int | None:
     if t is None:
         return None
@@ -211,7 +227,7 @@ def _quantize(name: str, nbytes, x: torch.Tensor, out, dev_status, stream):
         raise TypeError("quantizer input must be float32")
     n = x.numel()
     if out is None:
-        out = torch.empty(max(nbytes(n), 0), dtype=torch.uint8, device=x.device)
+        out = _make(torch.empty, max(nbytes(n), 0), torch.uint8, x.device, stream)
     _check(getattr(lib, name)(_ptr(x), n, _ptr(out), _ptr(dev_status), _stream(stream)), name)
     return out
 
@@ -230,7 +246,7 @@ def gq_quantize_q4_0_ex(x: torch.Tensor, flags: int, out: torch.Tensor | None = 
         raise TypeError("quantizer input must be float32")
     n = x.numel()
     if out is None:
-        out = torch.empty(max(gq_q4_0_bytes(n), 0), dtype=torch.uint8, device=x.device)
+        out = _make(torch.empty, max(gq_q4_0_bytes(n), 0), torch.uint8, x.device, stream)
     _check(lib.gq_quantize_q4_0_ex(_ptr(x), n, _ptr(out), int(flags), _ptr(dev_status),
                                    _stream(stream)), "gq_quantize_q4_0_ex")
     return out
@@ -244,7 +260,7 @@ def gq_quantize_ksb(x: torch.Tensor, out: torch.Tensor | None = None,
 
 def _dequantize(name: str, q: torch.Tensor, n: int, out, stream):
     if out is None:
-        out = torch.empty(n, dtype=torch.float32, device=q.device)
+        out = _make(torch.empty, n, torch.float32, q.device, stream)
     _check(getattr(lib, name)(_ptr(q), int(n), _ptr(out), _stream(stream)), name)
     return out
 
@@ -273,7 +289,7 @@ def _gemv_workspace(need: int, device: torch.device, stream) -> torch.Tensor:
     key = (device.index, _stream(stream))
     ws = _gemv_ws.get(key)
     if ws is None or ws.numel() < need:
-        ws = torch.zeros(need, dtype=torch.uint8, device=device)
+        ws = _make(torch.zeros, need, torch.uint8, device, stream)
         _gemv_ws[key] = ws
     return ws
 
@@ -287,7 +303,7 @@ def _gemv(name: str, fmt: int, W: torch.Tensor, M: int, K: int, x: torch.Tensor,
     if x2.dtype not in _DTYPE_CODE or y_dtype not in _DTYPE_CODE:
         raise TypeError("activations and outputs must be float32, float16 or bfloat16")
     if out is None:
-        out = torch.empty((B, M), dtype=y_dtype, device=x2.device)
+        out = _make(torch.empty, (B, M), y_dtype, x2.device, stream)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto', None or a uint8 CUDA tensor")
@@ -339,7 +355,7 @@ def _gemv_grouped(name: str, Ws, Ms, K: int, x: torch.Tensor, y_dtype, outs, fla
     if x2.dtype not in _DTYPE_CODE or y_dtype not in _DTYPE_CODE:
         raise TypeError("activations and outputs must be float32, float16 or bfloat16")
     if outs is None:
-        outs = [torch.empty((B, int(M)), dtype=y_dtype, device=x2.device) for M in Ms]
+        outs = [_make(torch.empty, (B, int(M)), y_dtype, x2.device, stream) for M in Ms]
     if len(outs) != len(Ws) or any(o.dtype != outs[0].dtype for o in outs):
         raise ValueError("one output per matrix, all of one dtype")
     descs = (GemvDesc * len(Ws))(*[GemvDesc(_ptr(W), int(M), _ptr(o))
@@ -378,10 +394,10 @@ def _gemm(name: str, fmt: int, W: torch.Tensor, M: int, K: int, X: torch.Tensor,
     if X2.dtype not in _DTYPE_CODE or y_dtype not in _DTYPE_CODE:
         raise TypeError("X must be bfloat16; Y float32, float16 or bfloat16")
     if out is None:
-        out = torch.empty((B, M), dtype=y_dtype, device=X2.device)
+        out = _make(torch.empty, (B, M), y_dtype, X2.device, stream)
     need = gq_gemm_workspace_bytes(fmt, M, K, B)
     if workspace is None and need > 0:
-        workspace = torch.zeros(need, dtype=torch.uint8, device=X2.device)
+        workspace = _make(torch.zeros, need, torch.uint8, X2.device, stream)
     ws_bytes = workspace.numel() if workspace is not None else 0
     _check(getattr(lib, name)(_ptr(W), int(M), int(K), _ptr(X2), _DTYPE_CODE[X2.dtype], B,
                               _ptr(out), _DTYPE_CODE[out.dtype], _ptr(workspace), ws_bytes,
@@ -413,7 +429,7 @@ def gq_gemv_q4_0_noalloc(W: torch.Tensor, M: int, K: int, x: torch.Tensor, y_dty
     if x2.shape != (1, K) or x2.dtype != torch.float16:
         raise ValueError("x must be one fp16 vector of length K")
     if out is None:
-        out = torch.empty((1, M), dtype=y_dtype, device=x2.device)
+        out = _make(torch.empty, (1, M), y_dtype, x2.device, stream)
     _check(lib.gq_gemv_q4_0_noalloc(_ptr(W), int(M), int(K), _ptr(x2), _ptr(out),
                                     _DTYPE_CODE[out.dtype], int(flags), _ptr(dev_status),
                                     _stream(stream)), "gq_gemv_q4_0_noalloc")
@@ -435,7 +451,7 @@ def gq_stream_read(buf: torch.Tensor, sink: torch.Tensor | None = None,
     `sink` (an int32 tensor of one element, zeroed here when not given): the
     practical read ceiling of one launch of that size."""
     if sink is None:
-        sink = torch.zeros(1, dtype=torch.int32, device=buf.device)
+        sink = _make(torch.zeros, 1, torch.int32, buf.device, stream)
     nbytes = buf.numel() * buf.element_size()
     _check(lib.gq_stream_read(_ptr(buf), nbytes, _ptr(sink), _stream(stream)), "gq_stream_read")
     return sink
@@ -451,7 +467,7 @@ def gq_repack(fmt: int, W: torch.Tensor, M: int, K: int, out: torch.Tensor | Non
     """Canonical packed rows (uint8 CUDA tensor) -> tiled storage (uint8)."""
     n = gq_tiled_bytes(fmt, M, K)
     if out is None:
-        out = torch.empty(n, dtype=torch.uint8, device=W.device)
+        out = _make(torch.empty, n, torch.uint8, W.device, stream)
     name = "gq_repack_q4_0" if fmt == GQ_FMT_Q4_0 else "gq_repack_ksb"
     _check(getattr(lib, name)(_ptr(W), int(M), int(K), _ptr(out), _stream(stream)), name)
     return out
@@ -465,7 +481,7 @@ def _gemv_tiled(name: str, T: torch.Tensor, M: int, K: int, x: torch.Tensor, y_d
     if x1.dtype not in _DTYPE_CODE or y_dtype not in _DTYPE_CODE:
         raise TypeError("activations and outputs must be float32, float16 or bfloat16")
     if out is None:
-        out = torch.empty((1, M), dtype=y_dtype, device=x1.device)
+        out = _make(torch.empty, (1, M), y_dtype, x1.device, stream)
     _check(getattr(lib, name)(_ptr(T), int(M), int(K), _ptr(x1), _DTYPE_CODE[x1.dtype],
                               _ptr(out), _DTYPE_CODE[out.dtype], int(flags), _ptr(dev_status),
                               _stream(stream)), name)
@@ -496,7 +512,7 @@ def _gemv_tiled_grouped(name: str, Ts, Ms, K: int, x: torch.Tensor, y_dtype, out
     if x1.dtype not in _DTYPE_CODE or y_dtype not in _DTYPE_CODE:
         raise TypeError("activations and outputs must be float32, float16 or bfloat16")
     if outs is None:
-        outs = [torch.empty((1, int(M)), dtype=y_dtype, device=x1.device) for M in Ms]
+        outs = [_make(torch.empty, (1, int(M)), y_dtype, x1.device, stream) for M in Ms]
     if len(outs) != len(Ts) or any(o.dtype != outs[0].dtype for o in outs):
         raise ValueError("one output per matrix, all of one dtype")
     descs = (GemvDesc * len(Ts))(*[GemvDesc(_ptr(T), int(M), _ptr(o))
@@ -599,14 +615,6 @@ def _at(t: torch.Tensor | None, device: int) -> int | None:
     if not t.is_contiguous():
         raise ValueError("tensors passed to libgq must be contiguous")
     return t.data_ptr() or None
-
-
-def _stream_object(stream: int, device: torch.device):
-    """A raw handle as a stream that torch allocates and launches on.  (Handles 0 and 1 are the default
-    stream; ExternalStream(0) would be some stream of torch's pool.)"""
-    if stream in (0, 1):
-        return torch.cuda.default_stream(device)
-    return torch.cuda.ExternalStream(stream, device=device)
 
 
 def _new(like: torch.Tensor, shape, dtype, named: int | None) -> torch.Tensor:
